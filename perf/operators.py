@@ -13,7 +13,8 @@ them.  Operators:
 
 The quantiser of a block: with m its largest magnitude, the scale is the smallest power of two s with
 m <= top * s (top = 448 for e4m3, 57344 for e5m2; s = 1 for a block of zeros) and each code is x / s
-rounded to nearest, ties to even.  Products take any positive scales.
+rounded to nearest, ties to even.  Products take any positive scales.  Row groups keep their scales
+group-major, [groups][T]; weights row-major, [N blocks][K blocks].
 """
 import math
 
@@ -101,12 +102,12 @@ def _pow2_scale(amax, top):
 
 
 def _quantise_rows(x, fmt):
-    """[T][K] -> codes [T][K] and fp32 scales [T][groups]."""
+    """[T][K] -> codes [T][K] and fp32 scales [groups][T]."""
     T, K = x.shape
     g = _groups(K)
     f = torch.nn.functional.pad(x.float(), (0, g * BLOCK - K)).view(T, g, BLOCK)
     s = _pow2_scale(f.abs().amax(2), TOP[fmt])
-    return (f / s[:, :, None]).view(T, g * BLOCK)[:, :K].to(fmt), s
+    return (f / s[:, :, None]).view(T, g * BLOCK)[:, :K].to(fmt), s.t().contiguous()
 
 
 def _quantise_blocks(w):
@@ -121,7 +122,7 @@ def _quantise_blocks(w):
 def _rows(codes, scale):
     """The values that row-grouped codes stand for, fp32."""
     K = codes.shape[1]
-    return codes.float() * scale.float().repeat_interleave(BLOCK, 1)[:, :K]
+    return codes.float() * scale.float().t().repeat_interleave(BLOCK, 1)[:, :K]
 
 
 def _blocks(codes, scale):
@@ -195,7 +196,7 @@ def prepare(case, seed):
         s["x"] = _activations(g, T, K)
         s["y"] = empty(T, N, dtype=torch.bfloat16)
         if case["keep"]:
-            s["codes"], s["scale"] = empty(T, K, dtype=E4M3), empty(T, _groups(K), dtype=scale_t)
+            s["codes"], s["scale"] = empty(T, K, dtype=E4M3), empty(_groups(K), T, dtype=scale_t)
     elif op == "dgrad":
         s["dy"] = _gradients(g, T, N)
         s["dx"] = empty(T, K, dtype=torch.bfloat16)
@@ -209,9 +210,9 @@ def prepare(case, seed):
         h = (1.5 * torch.randn(T, K, generator=g, device="cuda")).bfloat16()
         if op == "act":
             s["h"] = h
-            s["codes"], s["scale"] = empty(T, K, dtype=E4M3), empty(T, _groups(K), dtype=torch.float32)
+            s["codes"], s["scale"] = empty(T, K, dtype=E4M3), empty(_groups(K), T, dtype=torch.float32)
             if case["next"] == "fp8":
-                s["y_codes"], s["y_scale"] = empty(T, K, dtype=E4M3), empty(T, _groups(K), dtype=torch.float32)
+                s["y_codes"], s["y_scale"] = empty(T, K, dtype=E4M3), empty(_groups(K), T, dtype=torch.float32)
             else:
                 s["y"] = empty(T, K, dtype=torch.bfloat16)
         else:
@@ -312,7 +313,7 @@ def _exact_codes(x, fmt):
     T, K = x.shape
     bits, low = (3, -6) if fmt == E4M3 else (2, -14)     # mantissa bits, smallest normal exponent
     codes = torch.empty(T, K, dtype=torch.float64, device=x.device)
-    scale = torch.ones(T, _groups(K), dtype=torch.float64, device=x.device)
+    scale = torch.ones(_groups(K), T, dtype=torch.float64, device=x.device)
     for j in range(_groups(K)):
         part = x[:, j * BLOCK:(j + 1) * BLOCK]
         m = part.abs().max(1).values
@@ -321,21 +322,20 @@ def _exact_codes(x, fmt):
         lead = torch.floor(torch.log2(v.abs().clamp(min=2.0 ** low)))
         step = torch.exp2(lead - bits)
         codes[:, j * BLOCK:(j + 1) * BLOCK] = torch.round(v / step) * step
-        scale[:, j] = s
+        scale[j] = s
     return codes, scale
 
 
 def _exact_matrix(codes, scale, row_block):
     values = codes.to(torch.float64, copy=True)
     s = scale.double()
-    for i in range(s.shape[0]):
-        if row_block > 1:
-            rows = slice(i * row_block, (i + 1) * row_block)
-            for j in range(s.shape[1]):
-                values[rows, j * BLOCK:(j + 1) * BLOCK] *= s[i, j]
     if row_block == 1:
+        for j in range(s.shape[0]):
+            values[:, j * BLOCK:(j + 1) * BLOCK] *= s[j][:, None]
+        return values
+    for i in range(s.shape[0]):
         for j in range(s.shape[1]):
-            values[:, j * BLOCK:(j + 1) * BLOCK] *= s[:, j:j + 1]
+            values[i * row_block:(i + 1) * row_block, j * BLOCK:(j + 1) * BLOCK] *= s[i, j]
     return values
 
 
