@@ -49,7 +49,11 @@ typedef enum {
 typedef enum {
     RTQ_F32 = 0,  /* IEEE binary32                                               */
     RTQ_BF16 = 1, /* bfloat16 bit patterns (uint16), rounded to nearest-even      */
-    RTQ_I32 = 2   /* int32 accumulators: rtq_qgemm output (INT8, CODEBOOK_I8)   */
+    RTQ_I32 = 2,  /* int32 accumulators: rtq_qgemm output (INT8, CODEBOOK_I8)   */
+    RTQ_E4M3 = 3, /* 8-bit float codes, 4 exponent and 3 mantissa bits, bias 7, largest 448, no
+                   * infinity, NaN 0x7f and 0xff (OCP): the rtq_fp8_* and rtq_act_fp8_* calls */
+    RTQ_E5M2 = 4, /* 8-bit float codes, 5 exponent and 2 mantissa bits, largest 57344 (OCP) */
+    RTQ_E8M0 = 5  /* scale bytes, 2^(b - 127), 255 NaN                           */
 } rtq_dtype;
 
 typedef enum {
@@ -286,6 +290,109 @@ rtq_status rtq_rotated_qlinear_asym(const void* x, rtq_dtype xt, int64_t T, cons
                                     const int32_t* w_sum, int64_t N, void* y, rtq_dtype yt, void* workspace,
                                     size_t ws_bytes, void* stream);
 size_t rtq_rotated_qlinear_asym_workspace(int64_t T, int32_t d);
+
+/* ---- 8-bit floating point with a scale for each block of 128
+ *
+ * A linear layer y = x W^T whose operands are 8-bit floating point codes with block scales, and its
+ * backward pass from the codes the forward product read (they are the activation checkpoint).
+ *
+ * Formats shared by these calls
+ *   - codes: one byte per element, row-major [rows][d], E4M3 or (gradients) E5M2.  d is a multiple of
+ *     16, 16 <= d <= 2^20.
+ *   - row groups (activations, gradients): one scale for each 128 elements of a row, the last group
+ *     of a row possibly shorter.  Stored group-major: scale[ceil(d / 128)][rows].
+ *   - blocks (weights [N][K]): one scale for each 128 x 128 block, the last ones possibly smaller.
+ *     Stored row-major: scale[ceil(N / 128)][ceil(K / 128)].
+ *   - scales are F32 (any value; non-finite ones spread as in fp32 arithmetic) or E8M0, one type for
+ *     both operands of a product.  Scale arrays are 16-byte aligned like every device pointer here.
+ *   - The quantiser's rule for a block: with m its largest finite magnitude, the scale is the smallest
+ *     power of two s >= 2^-120 with m <= 448 s (E4M3) or m <= 57344 s (E5M2), and 1 when m = 0; a code
+ *     is x / s (exact) rounded to nearest, ties to even.  NaN stays NaN; an infinity becomes NaN in
+ *     E4M3 and stays infinite in E5M2.
+ * Sizes: rows, T < 2^31; N <= 2^20 where it is an output; other errors as in every call. */
+typedef enum {
+    RTQ_FP8_ROWS = 0,  /* row groups: 1 x 128, scales group-major */
+    RTQ_FP8_BLOCKS = 1 /* blocks: 128 x 128, scales row-major     */
+} rtq_fp8_layout;
+
+/* codes and scales of x [rows][d] (xt F32 or BF16).  ct: RTQ_E4M3 or RTQ_E5M2; st: RTQ_F32 or
+ * RTQ_E8M0.  rows == 0 is a no-op. */
+rtq_status rtq_fp8_quantize(const void* x, rtq_dtype xt, int64_t rows, int32_t d, rtq_fp8_layout layout,
+                            void* codes, rtq_dtype ct, void* scale, rtq_dtype st, void* stream);
+
+/* y = code * scale, [rows][d] of yt (F32 or BF16, rounded once). */
+rtq_status rtq_fp8_dequantize(const void* codes, rtq_dtype ct, const void* scale, rtq_dtype st, int64_t rows,
+                              int32_t d, rtq_fp8_layout layout, void* y, rtq_dtype yt, void* stream);
+
+/* y[t][n] = sum_kb a_scale[kb][t] w_scale[n / 128][kb] sum_{k in block kb} a[t][k] w[n][k].
+ *   a_codes [T][K] of at (E4M3 or E5M2), row groups; w_codes [N][K] E4M3, blocks; y [T][N] of yt.
+ *   Accuracy: each 128-long inner sum is one matrix instruction, which aligns its products to about
+ *   2^-14 of the largest; block sums are scaled and added in fp32.
+ *   workspace: may be NULL.  With at least rtq_fp8_qgemm_workspace(T, N, K) bytes (any contents,
+ *   16-byte aligned), products with few output tiles are split along the reduction; the fp32
+ *   partial sums are then added in a fixed order, so equal calls give equal bits.  Calls sharing a
+ *   workspace must not overlap.  T == 0 is a no-op. */
+rtq_status rtq_fp8_qgemm(const void* a_codes, rtq_dtype at, const void* a_scale, int64_t T, const void* w_codes,
+                         const void* w_scale, rtq_dtype st, int64_t N, int32_t K, void* y, rtq_dtype yt,
+                         void* workspace, size_t ws_bytes, void* stream);
+size_t rtq_fp8_qgemm_workspace(int64_t T, int64_t N, int32_t K);
+
+/* The gradient of the input from quantised output gradients, the weight codes read as they are
+ * stored for the forward product:
+ *   dx[t][k] = sum_nb g_scale[nb][t] w_scale[nb][k / 128] sum_{n in block nb} g[t][n] w[n][k].
+ *   g_codes [T][N] of gt (E4M3 or E5M2), row groups; w_codes [N][K] E4M3, blocks; dx [T][K] of dxt
+ *   (F32 or BF16).  N and K multiples of 16.  Workspace and accuracy as for rtq_fp8_qgemm. */
+rtq_status rtq_fp8_dgrad(const void* g_codes, rtq_dtype gt, const void* g_scale, int64_t T, const void* w_codes,
+                         const void* w_scale, rtq_dtype st, int32_t N, int32_t K, void* dx, rtq_dtype dxt,
+                         void* workspace, size_t ws_bytes, void* stream);
+size_t rtq_fp8_dgrad_workspace(int64_t T, int32_t N, int32_t K);
+
+/* The layer in one call: rtq_fp8_quantize(x) to E4M3 row groups, then rtq_fp8_qgemm, on one stream.
+ *   x [T][K] of xt (F32 or BF16).  x_codes [T][K] and x_scale [ceil(K / 128)][T] of st receive the codes
+ *   and scales (the checkpoint the backward calls take); both NULL: they go to the workspace.
+ *   workspace: rtq_fp8_linear_workspace(T, N, K) bytes (any contents).  Required when the codes are
+ *   not kept; with x_codes and x_scale given it may be NULL (the product is then not split). */
+rtq_status rtq_fp8_linear(const void* x, rtq_dtype xt, int64_t T, const void* w_codes, const void* w_scale,
+                          rtq_dtype st, int64_t N, int32_t K, void* x_codes, void* x_scale, void* y, rtq_dtype yt,
+                          void* workspace, size_t ws_bytes, void* stream);
+size_t rtq_fp8_linear_workspace(int64_t T, int64_t N, int32_t K);
+
+/* The input gradient in one call: rtq_fp8_quantize(dy) to row groups of gt, then rtq_fp8_dgrad.
+ *   dy [T][N] of dyt (F32 or BF16); workspace: rtq_fp8_linear_dgrad_workspace(T, N, K) bytes, required. */
+rtq_status rtq_fp8_linear_dgrad(const void* dy, rtq_dtype dyt, rtq_dtype gt, int64_t T, const void* w_codes,
+                                const void* w_scale, rtq_dtype st, int32_t N, int32_t K, void* dx, rtq_dtype dxt,
+                                void* workspace, size_t ws_bytes, void* stream);
+size_t rtq_fp8_linear_dgrad_workspace(int64_t T, int32_t N, int32_t K);
+
+/* The gradient of the weight from the 8-bit checkpoint of the input:
+ *   dw[n][k] (+)= sum_t dy[t][n] x^[t][k],  x^[t][k] = x_scale[k / 128][t] x_codes[t][k] rounded to bf16
+ *   (exact for power-of-two scales, as rtq_fp8_quantize writes them), summed in fp32.
+ *   dy [T][N] BF16, N a multiple of 8; x_codes [T][K] E4M3, row groups; dw [N][K] of dwt (F32 or BF16),
+ *   accumulate 0 (overwrite) or 1 (add; a BF16 dw is read, added in fp32 and rounded again).  T == 0
+ *   writes zeros, or with accumulate leaves dw as it is.  workspace as for rtq_fp8_qgemm, of
+ *   rtq_fp8_wgrad_workspace(T, N, K) bytes. */
+rtq_status rtq_fp8_wgrad(const void* dy, int64_t T, const void* x_codes, const void* x_scale, rtq_dtype st,
+                         int32_t N, int32_t K, void* dw, rtq_dtype dwt, int32_t accumulate, void* workspace,
+                         size_t ws_bytes, void* stream);
+size_t rtq_fp8_wgrad_workspace(int64_t T, int32_t N, int32_t K);
+
+typedef enum {
+    RTQ_ACT_GELU_TANH = 1, /* h/2 (1 + tanh(sqrt(2/pi) (h + 0.044715 h^3))) */
+    RTQ_ACT_GELU = 2,      /* h/2 (1 + erf(h / sqrt 2))                     */
+    RTQ_ACT_SILU = 3       /* h / (1 + exp(-h))                             */
+} rtq_act;
+
+/* An activation function with its input kept in 8 bits, in one pass over h [rows][d] (F32 or BF16):
+ *   h_codes (E4M3), h_scale (row groups): rtq_fp8_quantize(h), the checkpoint;
+ *   y = f(h): either y [rows][d] of h's type (y_codes and y_scale NULL), or y_codes, y_scale (E4M3, row
+ *   groups) for the next product (y NULL). */
+rtq_status rtq_act_fp8_forward(const void* h, rtq_dtype ht, int64_t rows, int32_t d, rtq_act act, void* h_codes,
+                               void* h_scale, void* y, void* y_codes, void* y_scale, rtq_dtype st, void* stream);
+
+/* Its backward pass from the checkpoint: dh = dy f'(h^), h^ = h_scale h_codes.  dy, dh [rows][d] of dyt
+ * (F32 or BF16); dh may be dy itself. */
+rtq_status rtq_act_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_codes, const void* h_scale,
+                                rtq_dtype st, int64_t rows, int32_t d, rtq_act act, void* dh, void* stream);
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* rtq_last_error(void);

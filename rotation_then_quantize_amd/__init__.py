@@ -20,6 +20,10 @@ LIB_PATH = os.path.join(_PKG, "librtq.so")
 
 RTQ_OK, RTQ_ERR_INVALID_ARG, RTQ_ERR_UNSUPPORTED, RTQ_ERR_MISALIGNED, RTQ_ERR_HIP = 0, -1, -2, -3, -4
 RTQ_F32, RTQ_BF16, RTQ_I32 = 0, 1, 2
+RTQ_E4M3, RTQ_E5M2, RTQ_E8M0 = 3, 4, 5
+RTQ_FP8_ROWS, RTQ_FP8_BLOCKS = 0, 1
+RTQ_ACT_GELU_TANH, RTQ_ACT_GELU, RTQ_ACT_SILU = 1, 2, 3
+FP8_BLOCK = 128   # elements per scale of 8-bit floating point codes
 RTQ_INT8, RTQ_CODEBOOK, RTQ_CODEBOOK_I8, RTQ_INT8_TILED = 0, 1, 2, 3
 RTQ_CODEBOOK_TILED, RTQ_CODEBOOK_I8_TILED = 4, 5
 TILE_ROWS, TILE_K = 256, 64   # the tiled layouts: 256-row tiles, K slices of 64 elements
@@ -42,7 +46,11 @@ def tiled_code_bytes(rows: int, d: int, mode: int, bits: int = 8) -> int:
 EXPORTS = ("rtq_rpbh_make", "rtq_lloyd_max", "rtq_rpbh_rotate", "rtq_quantize_rows", "rtq_qgemm",
            "rtq_qgemm_ws", "rtq_qgemm_workspace", "rtq_rotated_qlinear", "rtq_rotated_qlinear_workspace",
            "rtq_quantize_rows_asym", "rtq_qgemm_asym", "rtq_rotated_qlinear_asym",
-           "rtq_rotated_qlinear_asym_workspace", "rtq_rotated_qlinear_noalloc", "rtq_last_error")
+           "rtq_rotated_qlinear_asym_workspace", "rtq_rotated_qlinear_noalloc", "rtq_fp8_quantize",
+           "rtq_fp8_dequantize", "rtq_fp8_qgemm", "rtq_fp8_qgemm_workspace", "rtq_fp8_dgrad",
+           "rtq_fp8_dgrad_workspace", "rtq_fp8_linear", "rtq_fp8_linear_workspace", "rtq_fp8_linear_dgrad",
+           "rtq_fp8_linear_dgrad_workspace", "rtq_fp8_wgrad", "rtq_fp8_wgrad_workspace", "rtq_act_fp8_forward",
+           "rtq_act_fp8_backward", "rtq_last_error")
 
 NOALLOC_SCRATCH_BYTES = 96 << 20   # RTQ_NOALLOC_SCRATCH_BYTES
 
@@ -94,11 +102,27 @@ def load_library():
     lib.rtq_rotated_qlinear_asym.argtypes = [vp, i32, i64, R, vp, vp, i32, vp, vp, i64, vp, i32, vp, sz, vp]
     lib.rtq_rotated_qlinear_asym_workspace.argtypes = [i64, i32]
     lib.rtq_rotated_qlinear_asym_workspace.restype = sz
+    lib.rtq_fp8_quantize.argtypes = [vp, i32, i64, i32, i32, vp, i32, vp, i32, vp]
+    lib.rtq_fp8_dequantize.argtypes = [vp, i32, vp, i32, i64, i32, i32, vp, i32, vp]
+    lib.rtq_fp8_qgemm.argtypes = [vp, i32, vp, i64, vp, vp, i32, i64, i32, vp, i32, vp, sz, vp]
+    lib.rtq_fp8_dgrad.argtypes = [vp, i32, vp, i64, vp, vp, i32, i32, i32, vp, i32, vp, sz, vp]
+    lib.rtq_fp8_linear.argtypes = [vp, i32, i64, vp, vp, i32, i64, i32, vp, vp, vp, i32, vp, sz, vp]
+    lib.rtq_fp8_linear_dgrad.argtypes = [vp, i32, i32, i64, vp, vp, i32, i32, i32, vp, i32, vp, sz, vp]
+    lib.rtq_fp8_wgrad.argtypes = [vp, i64, vp, vp, i32, i32, i32, vp, i32, i32, vp, sz, vp]
+    lib.rtq_act_fp8_forward.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, i32, vp]
+    lib.rtq_act_fp8_backward.argtypes = [vp, i32, vp, vp, i32, i64, i32, i32, vp, vp]
+    for name, n in (("rtq_fp8_qgemm_workspace", i64), ("rtq_fp8_linear_workspace", i64),
+                    ("rtq_fp8_dgrad_workspace", i32), ("rtq_fp8_linear_dgrad_workspace", i32),
+                    ("rtq_fp8_wgrad_workspace", i32)):
+        getattr(lib, name).argtypes = [i64, n, i32]
+        getattr(lib, name).restype = sz
     lib.rtq_last_error.argtypes = []
     lib.rtq_last_error.restype = ctypes.c_char_p
     for name in ("rtq_rpbh_make", "rtq_lloyd_max", "rtq_rpbh_rotate", "rtq_quantize_rows", "rtq_qgemm",
                  "rtq_qgemm_ws", "rtq_rotated_qlinear", "rtq_quantize_rows_asym", "rtq_qgemm_asym",
-                 "rtq_rotated_qlinear_asym", "rtq_rotated_qlinear_noalloc"):
+                 "rtq_rotated_qlinear_asym", "rtq_rotated_qlinear_noalloc", "rtq_fp8_quantize", "rtq_fp8_dequantize",
+                 "rtq_fp8_qgemm", "rtq_fp8_dgrad", "rtq_fp8_linear", "rtq_fp8_linear_dgrad", "rtq_fp8_wgrad",
+                 "rtq_act_fp8_forward", "rtq_act_fp8_backward"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -348,3 +372,261 @@ def rotated_qlinear_asym(x, R: Rpbh, w_codes, w_scale, w_zero, w_sum, y, workspa
                                                    _ptr(y), _dtype_code(y), _ptr(workspace), workspace.numel(),
                                                    _stream(stream)))
     return y
+
+
+# ------------------------------------------------------------------ 8-bit floating point, scales for blocks of 128
+#
+# Codes are torch.float8_e4m3fn (gradients also float8_e5m2) tensors, scales float32 or
+# float8_e8m0fnu.  Tensors are contiguous and on one device; the calls run on that device, on
+# `stream` or its current stream.
+
+def fp8_groups(d: int) -> int:
+    """Scales along d elements (blocks of 128, the last one possibly shorter)."""
+    return -(-d // FP8_BLOCK)
+
+
+def _fp8_types():
+    torch = _torch()
+    return {torch.float8_e4m3fn: RTQ_E4M3, torch.float8_e5m2: RTQ_E5M2}
+
+
+def _scale_types():
+    torch = _torch()
+    return {torch.float32: RTQ_F32, torch.float8_e8m0fnu: RTQ_E8M0}
+
+
+def _float_types():
+    torch = _torch()
+    return {torch.float32: RTQ_F32, torch.bfloat16: RTQ_BF16}
+
+
+def _operand(t, name: str, types: dict, shape=None, like=None) -> int:
+    """Type code of a device tensor, after checking its type, shape, layout and device."""
+    if t.dtype not in types:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {'two dimensions' if shape is None else tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    return types[t.dtype]
+
+
+class _Launch:
+    """The device and stream of one call, and its workspace."""
+
+    def __init__(self, like, stream):
+        torch = _torch()
+        if stream is not None and stream.device != like.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
+        self._device = like.device
+        self._guard = torch.cuda.device(like.device)
+        self._user_stream = stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        self.stream = _stream(self._user_stream)
+        return self
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+    def workspace(self, given, need: int):
+        """(pointer, bytes) of the caller's workspace, or of a temporary one of `need` bytes."""
+        if given is None:
+            if need == 0:
+                self._ws = None
+                return 0, 0
+            self._ws = _stream_local_workspace(_torch(), need, self._device, self._user_stream)
+        else:
+            if given.device != self._device:
+                raise ValueError(f"workspace is on {given.device}, expected {self._device}")
+            if not given.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+            self._ws = given
+        return _ptr(self._ws), self._ws.numel() * self._ws.element_size()
+
+
+def fp8_quantize(x, codes, scale, blocks: bool = False, stream=None):
+    """Codes and power-of-two scales of x [rows][d]: row groups of 128 (scale [groups][rows],
+    group-major) or, with blocks, 128 x 128 blocks (scale [row blocks][column blocks])."""
+    xt = _operand(x, "x", _float_types())
+    rows, d = x.shape
+    ct = _operand(codes, "codes", _fp8_types(), x.shape, x)
+    st = _operand(scale, "scale", _scale_types(),
+                  (fp8_groups(rows), fp8_groups(d)) if blocks else (fp8_groups(d), rows), x)
+    with _Launch(x, stream) as go:
+        _check(load_library().rtq_fp8_quantize(_ptr(x), xt, rows, d, RTQ_FP8_BLOCKS if blocks else RTQ_FP8_ROWS,
+                                               _ptr(codes), ct, _ptr(scale), st, go.stream))
+    return codes, scale
+
+
+def fp8_dequantize(codes, scale, y, blocks: bool = False, stream=None):
+    """y = code * scale, for codes and scales as fp8_quantize writes them."""
+    ct = _operand(codes, "codes", _fp8_types())
+    rows, d = codes.shape
+    st = _operand(scale, "scale", _scale_types(),
+                  (fp8_groups(rows), fp8_groups(d)) if blocks else (fp8_groups(d), rows), codes)
+    yt = _operand(y, "y", _float_types(), codes.shape, codes)
+    with _Launch(codes, stream) as go:
+        _check(load_library().rtq_fp8_dequantize(_ptr(codes), ct, _ptr(scale), st, rows, d,
+                                                 RTQ_FP8_BLOCKS if blocks else RTQ_FP8_ROWS, _ptr(y), yt, go.stream))
+    return y
+
+
+def _fp8_weight(w_codes, w_scale, like):
+    """(N, K, scale type code) of block-scaled weight codes."""
+    torch = _torch()
+    _operand(w_codes, "w_codes", {torch.float8_e4m3fn: RTQ_E4M3}, None, like)
+    N, K = w_codes.shape
+    return N, K, _operand(w_scale, "w_scale", _scale_types(), (fp8_groups(N), fp8_groups(K)), like)
+
+
+def _same_scale(a, name: str, w_scale):
+    if a.dtype != w_scale.dtype:
+        raise TypeError(f"{name} is {a.dtype}, w_scale {w_scale.dtype}: the scales of a product share one type")
+
+
+def fp8_qgemm_workspace(T: int, N: int, K: int) -> int:
+    return int(load_library().rtq_fp8_qgemm_workspace(T, N, K))
+
+
+def fp8_qgemm(a_codes, a_scale, w_codes, w_scale, y, workspace=None, stream=None):
+    """y [T][N] = a W^T of row-group codes a [T][K] and block codes W [N][K]."""
+    N, K, st = _fp8_weight(w_codes, w_scale, a_codes)
+    T = a_codes.shape[0]
+    at = _operand(a_codes, "a_codes", _fp8_types(), (T, K))
+    _operand(a_scale, "a_scale", _scale_types(), (fp8_groups(K), T), a_codes)
+    _same_scale(a_scale, "a_scale", w_scale)
+    yt = _operand(y, "y", _float_types(), (T, N), a_codes)
+    with _Launch(a_codes, stream) as go:
+        ws, nbytes = go.workspace(workspace, fp8_qgemm_workspace(T, N, K))
+        _check(load_library().rtq_fp8_qgemm(_ptr(a_codes), at, _ptr(a_scale), T, _ptr(w_codes), _ptr(w_scale), st, N, K,
+                                            _ptr(y), yt, ws, nbytes, go.stream))
+    return y
+
+
+def fp8_dgrad_workspace(T: int, N: int, K: int) -> int:
+    return int(load_library().rtq_fp8_dgrad_workspace(T, N, K))
+
+
+def fp8_dgrad(g_codes, g_scale, w_codes, w_scale, dx, workspace=None, stream=None):
+    """dx [T][K] = g W of row-group codes g [T][N] (quantised output gradients) and block codes W [N][K]."""
+    N, K, st = _fp8_weight(w_codes, w_scale, g_codes)
+    T = g_codes.shape[0]
+    gt = _operand(g_codes, "g_codes", _fp8_types(), (T, N))
+    _operand(g_scale, "g_scale", _scale_types(), (fp8_groups(N), T), g_codes)
+    _same_scale(g_scale, "g_scale", w_scale)
+    dxt = _operand(dx, "dx", _float_types(), (T, K), g_codes)
+    with _Launch(g_codes, stream) as go:
+        ws, nbytes = go.workspace(workspace, fp8_dgrad_workspace(T, N, K))
+        _check(load_library().rtq_fp8_dgrad(_ptr(g_codes), gt, _ptr(g_scale), T, _ptr(w_codes), _ptr(w_scale), st, N, K,
+                                            _ptr(dx), dxt, ws, nbytes, go.stream))
+    return dx
+
+
+def fp8_linear_workspace(T: int, N: int, K: int) -> int:
+    return int(load_library().rtq_fp8_linear_workspace(T, N, K))
+
+
+def fp8_linear(x, w_codes, w_scale, y, x_codes=None, x_scale=None, workspace=None, stream=None):
+    """y [T][N] = quantise(x) W^T for x [T][K] and block codes W [N][K].  With x_codes [T][K] (e4m3)
+    and x_scale [groups][T] the codes the product read are kept: the checkpoint fp8_wgrad takes."""
+    torch = _torch()
+    N, K, st = _fp8_weight(w_codes, w_scale, x)
+    T = x.shape[0]
+    xt = _operand(x, "x", _float_types(), (T, K))
+    yt = _operand(y, "y", _float_types(), (T, N), x)
+    if (x_codes is None) != (x_scale is None):
+        raise ValueError("x_codes and x_scale are given together or not at all")
+    if x_codes is not None:
+        _operand(x_codes, "x_codes", {torch.float8_e4m3fn: RTQ_E4M3}, (T, K), x)
+        _operand(x_scale, "x_scale", _scale_types(), (fp8_groups(K), T), x)
+        _same_scale(x_scale, "x_scale", w_scale)
+    with _Launch(x, stream) as go:
+        ws, nbytes = go.workspace(workspace, fp8_linear_workspace(T, N, K))
+        _check(load_library().rtq_fp8_linear(_ptr(x), xt, T, _ptr(w_codes), _ptr(w_scale), st, N, K, _ptr(x_codes),
+                                             _ptr(x_scale), _ptr(y), yt, ws, nbytes, go.stream))
+    return y
+
+
+def fp8_linear_dgrad_workspace(T: int, N: int, K: int) -> int:
+    return int(load_library().rtq_fp8_linear_dgrad_workspace(T, N, K))
+
+
+def fp8_linear_dgrad(dy, w_codes, w_scale, dx, grad_dtype=None, workspace=None, stream=None):
+    """dx [T][K] = quantise(dy) W for dy [T][N] and block codes W [N][K]; grad_dtype is the format dy is
+    quantised to, torch.float8_e5m2 (default) or torch.float8_e4m3fn."""
+    torch = _torch()
+    N, K, st = _fp8_weight(w_codes, w_scale, dy)
+    T = dy.shape[0]
+    dyt = _operand(dy, "dy", _float_types(), (T, N))
+    dxt = _operand(dx, "dx", _float_types(), (T, K), dy)
+    grad_dtype = torch.float8_e5m2 if grad_dtype is None else grad_dtype
+    if grad_dtype not in _fp8_types():
+        raise TypeError(f"grad_dtype: unsupported dtype {grad_dtype}")
+    with _Launch(dy, stream) as go:
+        ws, nbytes = go.workspace(workspace, fp8_linear_dgrad_workspace(T, N, K))
+        _check(load_library().rtq_fp8_linear_dgrad(_ptr(dy), dyt, _fp8_types()[grad_dtype], T, _ptr(w_codes),
+                                                   _ptr(w_scale), st, N, K, _ptr(dx), dxt, ws, nbytes, go.stream))
+    return dx
+
+
+def fp8_wgrad_workspace(T: int, N: int, K: int) -> int:
+    return int(load_library().rtq_fp8_wgrad_workspace(T, N, K))
+
+
+def fp8_wgrad(dy, x_codes, x_scale, dw, accumulate: bool = False, workspace=None, stream=None):
+    """dw [N][K] = dy^T x^ (added to dw with accumulate) for dy [T][N] (bf16) and the checkpoint x^ of the
+    layer's input: codes [T][K] (e4m3) and scales [groups][T]."""
+    torch = _torch()
+    _operand(dy, "dy", {torch.bfloat16: RTQ_BF16})
+    T, N = dy.shape
+    _operand(x_codes, "x_codes", {torch.float8_e4m3fn: RTQ_E4M3}, (T, x_codes.shape[-1]), dy)
+    K = x_codes.shape[1]
+    st = _operand(x_scale, "x_scale", _scale_types(), (fp8_groups(K), T), dy)
+    dwt = _operand(dw, "dw", _float_types(), (N, K), dy)
+    with _Launch(dy, stream) as go:
+        ws, nbytes = go.workspace(workspace, fp8_wgrad_workspace(T, N, K))
+        _check(load_library().rtq_fp8_wgrad(_ptr(dy), T, _ptr(x_codes), _ptr(x_scale), st, N, K, _ptr(dw), dwt,
+                                            1 if accumulate else 0, ws, nbytes, go.stream))
+    return dw
+
+
+def act_fp8_forward(h, act: int, h_codes, h_scale, y=None, y_codes=None, y_scale=None, stream=None):
+    """y = f(h) with h kept as codes [rows][d] (e4m3) and scales [groups][rows]; f is RTQ_ACT_GELU_TANH,
+    RTQ_ACT_GELU or RTQ_ACT_SILU.  y comes back as y (h's type), or quantised as y_codes, y_scale."""
+    torch = _torch()
+    e4m3 = {torch.float8_e4m3fn: RTQ_E4M3}
+    ht = _operand(h, "h", _float_types())
+    rows, d = h.shape
+    _operand(h_codes, "h_codes", e4m3, h.shape, h)
+    st = _operand(h_scale, "h_scale", _scale_types(), (fp8_groups(d), rows), h)
+    if (y_codes is None) != (y_scale is None) or (y is None) == (y_codes is None):
+        raise ValueError("give either y, or y_codes and y_scale")
+    if y is not None:
+        _operand(y, "y", {h.dtype: ht}, h.shape, h)
+    else:
+        _operand(y_codes, "y_codes", e4m3, h.shape, h)
+        _operand(y_scale, "y_scale", {h_scale.dtype: st}, (fp8_groups(d), rows), h)
+    with _Launch(h, stream) as go:
+        _check(load_library().rtq_act_fp8_forward(_ptr(h), ht, rows, d, act, _ptr(h_codes), _ptr(h_scale), _ptr(y),
+                                                  _ptr(y_codes), _ptr(y_scale), st, go.stream))
+    return y if y is not None else (y_codes, y_scale)
+
+
+def act_fp8_backward(dy, h_codes, h_scale, act: int, dh, stream=None):
+    """dh = dy f'(h^) from the checkpoint of h (act_fp8_forward).  dh may be dy."""
+    torch = _torch()
+    dyt = _operand(dy, "dy", _float_types())
+    rows, d = dy.shape
+    _operand(h_codes, "h_codes", {torch.float8_e4m3fn: RTQ_E4M3}, dy.shape, dy)
+    st = _operand(h_scale, "h_scale", _scale_types(), (fp8_groups(d), rows), dy)
+    _operand(dh, "dh", {dy.dtype: dyt}, dy.shape, dy)
+    with _Launch(dy, stream) as go:
+        _check(load_library().rtq_act_fp8_backward(_ptr(dy), dyt, _ptr(h_codes), _ptr(h_scale), st, rows, d, act,
+                                                   _ptr(dh), go.stream))
+    return dh

@@ -1,0 +1,62 @@
+// fp8_tile.h -- what the 8-bit products' tile kernels share: buffer loads into LDS, waits, and the
+// matrix instruction.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8_device.h"
+
+// The LDS-writing loads set M0 in inline assembly; M0 is otherwise unused by these kernels.
+#pragma clang diagnostic ignored "-Winline-asm"
+
+namespace rtq {
+namespace fp8 {
+
+constexpr int kBufferWord3 = 0x00020000;     // gfx9 buffer descriptor word 3 (raw, 32-bit dwords)
+constexpr uint32_t kOob = 0x80000000u;       // an offset past every descriptor used here: loads give 0
+
+// Raw buffer descriptor over [base, base + bytes): loads at offsets >= bytes return zero.
+__device__ __forceinline__ v4i make_rsrc(const void* base, uint32_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    v4i r;
+    r.x = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(b)));
+    r.y = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(b >> 32) & 0xffffu));
+    r.z = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes));
+    r.w = kBufferWord3;
+    return r;
+}
+
+// 16 bytes per lane from buffer offset voff to LDS address lds_addr + 16 * lane.
+__device__ __forceinline__ void load_to_lds(v4i rsrc, uint32_t voff, uint32_t lds_addr) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(static_cast<int>(lds_addr))), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+// orders a wave's own LDS accesses against the barrier that hands their memory on
+__device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Wait until at most n vector-memory operations of this wave are outstanding.
+template <int n>
+__device__ __forceinline__ void wait_vmcnt() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
+
+typedef __attribute__((address_space(3))) v2i* lds_v2i;
+// 8 x 16 bytes transposed: the 16 lanes of a group give the addresses of 8 bytes each, two lanes to a
+// row; lane i of the group gets byte i of the rows, first row first.
+__device__ __forceinline__ v2i read_tr8(uint32_t lds_addr) {
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i>(lds_addr));
+}
+
+// 16 x 16 x 128 product of e4m3 (first operand: weights) and e4m3 or e5m2 codes, 32 codes of one row a
+// lane.  Lane l of the result holds column l % 16 (second operand's row), rows 4 (l / 16) .. +4.
+template <bool kE5M2>
+__device__ __forceinline__ v4f mfma(const v8i& w, const v8i& a, v4f c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, kE5M2 ? 1 : 0, 0, 0, 0, 0);
+}
+
+}  // namespace fp8
+}  // namespace rtq

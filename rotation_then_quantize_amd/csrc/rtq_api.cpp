@@ -14,10 +14,13 @@
 #include "../../include/rtq.h"
 #include "rtq_host.h"
 #include "rtq_internal.h"
+#include "rtq_status.h"
+
+namespace rtq {
 
 namespace {
-
 thread_local std::string g_err;
+}
 
 rtq_status fail(rtq_status s, const char* fmt, ...) {
     char buf[512];
@@ -39,17 +42,22 @@ rtq_status hip_status(hipError_t e, const char* what) {
     return fail(RTQ_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-#define RTQ_TRY(expr)                     \
-    do {                                  \
-        rtq_status _s = (expr);           \
-        if (_s != RTQ_OK) return _s;      \
-    } while (0)
-
 rtq_status check_ptr(const void* p, const char* name) {
     if (p == nullptr) return fail(RTQ_ERR_INVALID_ARG, "%s is NULL", name);
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return fail(RTQ_ERR_MISALIGNED, "%s is not 16-byte aligned", name);
     return RTQ_OK;
 }
+
+const char* last_error_text() { return g_err.c_str(); }
+
+}  // namespace rtq
+
+namespace {
+
+using rtq::check_ptr;
+using rtq::fail;
+using rtq::hip_status;
+using rtq::ok;
 
 // d: a multiple of 64 whose block count d/64 is a power of two, 64..16384.
 rtq_status check_d(int64_t d) {
@@ -540,6 +548,6 @@ rtq_status rtq_rotated_qlinear_asym(const void* x, rtq_dtype xt, int64_t T, cons
     return hip_status(rtq::launch_gemm_i8(gp.i8, s), "gemm_i8 launch");
 }
 
-const char* rtq_last_error(void) { return g_err.c_str(); }
+const char* rtq_last_error(void) { return rtq::last_error_text(); }
 
 }  // extern "C"
