@@ -23,22 +23,6 @@ namespace {
 
 using namespace fp8;
 
-constexpr int BK = kFp8Block;   // reduction bytes per LDS stage: one block of scales
-
-struct GemmParams {
-    const uint8_t* a;
-    const void* a_scale;
-    const uint8_t* w;
-    const void* w_scale;
-    int64_t M, N;
-    int R;
-    int tiles_m, tiles_n;
-    int64_t w_out_stride, w_red_stride;   // weight scale of (output block, reduction block)
-    int split;                            // equal ranges of the reduction per tile
-    void* y;                              // output (split 1), or fp32 partials [split][M][N]
-    bool y_bf16;
-};
-
 // Four consecutive outputs of row m from column n.
 __device__ __forceinline__ void store4(void* y, bool bf16, int64_t M, int64_t N, int64_t m, int64_t n, const v4f& v) {
     if (m >= M || n >= N) return;
@@ -63,7 +47,7 @@ __device__ __forceinline__ void store4(void* y, bool bf16, int64_t M, int64_t N,
 
 template <int BM, int BN, int kWavesM, int kWavesN, int kSlots, bool kTrans, bool kE5M2>
 __global__ void __launch_bounds__(64 * kWavesM * kWavesN)
-fp8_gemm_kernel(GemmParams p, bool e8m0) {
+fp8_gemm_kernel(Fp8GemmParams p) {
     constexpr int kWaves = kWavesM * kWavesN;
     constexpr int WM = BM / kWavesM, WN = BN / kWavesN;
     constexpr int TM = WM / 16, TN = WN / 16;
@@ -155,10 +139,10 @@ fp8_gemm_kernel(GemmParams p, bool e8m0) {
         if (kb0 + s < kb1) issue(kb0 + s);
     constexpr int kLoads = kALoads + kWLoads;
     for (int kb = kb0; kb < kb1; ++kb) {
-        const float sw = load_scale(p.w_scale, e8m0, wblock * p.w_out_stride + kb * p.w_red_stride);
+        const float sw = load_scale(p.w_scale, p.e8m0, wblock * p.w_out_stride + kb * p.w_red_stride);
         float s[TM];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) s[i] = load_scale(p.a_scale, e8m0, kb * p.M + mi[i]) * sw;
+        for (int i = 0; i < TM; ++i) s[i] = load_scale(p.a_scale, p.e8m0, kb * p.M + mi[i]) * sw;
         // block kb has landed (later blocks may be in flight), in every wave; block kb - 1 is read
         if (kSlots > 2 && kb + kSlots - 2 < kb1)
             wait_vmcnt<(kSlots - 2) * kLoads>();
@@ -232,6 +216,8 @@ int choose_split(int64_t tiles, int blocks) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplit)));
 }
 
+bool use_large(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) >= 96; }
+
 template <bool kTrans, bool kE5M2>
 hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
     constexpr int kSlots = 4;
@@ -240,7 +226,8 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
     int per_cu = 0;
     hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), 256, lds, &per_cu);
     if (e != hipSuccess) return e;
-    GemmParams p{};
+    Fp8GemmParams p{};
+    p.e8m0 = g.e8m0;
     p.a = static_cast<const uint8_t*>(g.a);
     p.a_scale = g.a_scale;
     p.w = static_cast<const uint8_t*>(g.w);
@@ -252,12 +239,17 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
     p.tiles_n = static_cast<int>((g.N + kTile - 1) / kTile);
     p.w_out_stride = kTrans ? 1 : fp8_groups(g.R);
     p.w_red_stride = kTrans ? fp8_groups(g.N) : 1;
+    p.y_bf16 = g.y_bf16;
+    if (use_large(g.M, g.N)) {
+        p.y = g.y;
+        p.split = 1;
+        return launch_fp8_gemm_large(p, kTrans, kE5M2, stream);
+    }
     const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
     p.split = choose_split(tiles, static_cast<int>(fp8_groups(g.R)));
     if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(p.split) * g.M * g.N * sizeof(float)) p.split = 1;
     p.y = p.split > 1 ? g.workspace : g.y;
-    p.y_bf16 = g.y_bf16;
-    kernel<<<static_cast<unsigned>(tiles * p.split), 256, lds, stream>>>(p, g.e8m0);
+    kernel<<<static_cast<unsigned>(tiles * p.split), 256, lds, stream>>>(p);
     e = hipGetLastError();
     if (e != hipSuccess || p.split == 1) return e;
     const int64_t n = g.M * g.N;
@@ -270,6 +262,7 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int R, bool trans) {
     (void)trans;
+    if (use_large(M, N)) return 0;
     const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
     const int split = choose_split(tiles, static_cast<int>(fp8_groups(R)));
     return split > 1 ? static_cast<size_t>(split) * M * N * sizeof(float) : 0;

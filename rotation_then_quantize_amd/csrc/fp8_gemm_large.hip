@@ -1,0 +1,366 @@
+// fp8_gemm_large.hip -- the 8-bit product for outputs of many tiles: 256 x 256 outputs per workgroup.
+//
+// A workgroup of 8 waves (two per SIMD) owns 256 x 256 outputs, each wave 128 x 64 of them as 8 x 4
+// tiles of v_mfma_f32_16x16x128_f8f6f4.  One LDS stage is one block of 128 along the reduction: 256
+// rows x 128 bytes of each operand (64 KB), two stages.  An instruction from a zero accumulator gives a
+// tile's sum over the block; its four values per lane are multiplied into the running sum by the
+// block's scale four instructions later, so the vector unit works in the matrix unit's shadow (4 fp32
+// multiply-adds, 16 clocks, per 32-clock instruction).
+//
+// Pipeline.  Stage s + 2 is loaded into stage s's slot as soon as every wave has read its last fragments
+// of stage s, which is two row tiles before the stage's end; the barrier that says so also says that
+// stage s + 1 has landed, so the fragments of its first tiles are read while the last tiles of stage s
+// are multiplied.  One barrier per stage.  Loads write LDS directly (no staging registers).
+//
+// Scales.  Each stage's 256 row scales, times the weight's two block scales, go through LDS (written by
+// one thread per row a stage ahead), arranged so that a lane reads the scales of its 8 row tiles as two
+// 16-byte words.
+//
+// Persistent: one workgroup per CU walks its tiles, loading the next tile's first two stages before the
+// epilogue of the current one.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "fp8_internal.h"
+#include "fp8_tile.h"
+#include "rtq_internal.h"
+
+namespace rtq {
+namespace {
+
+using namespace fp8;
+
+constexpr int BN = 256;
+constexpr int kWavesM = 2, kWavesN = 4, kWaves = kWavesM * kWavesN;
+constexpr int kThreads = 64 * kWaves;
+constexpr int WN = BN / kWavesN, TN = WN / 16;
+constexpr int kXcds = 8;
+constexpr int kMaxM = 256;
+constexpr int kRing = 2 * (kMaxM + BN) * BK;
+constexpr int kScaleBytes = 2 * 2 * kMaxM * static_cast<int>(sizeof(float));   // [slot][column block][row]
+constexpr int kStageOut = kWaves * 16 * 128;                                   // epilogue: 16 rows x 128 bytes a wave
+constexpr int kLds = kRing + kScaleBytes + kStageOut;
+
+// Tile index within the XCD-ordered sequence -> (tile_m, tile_n), in bands of 8 N-tiles.
+__device__ __forceinline__ void tile_of(int lin, int tiles_m, int tiles_n, int* tm, int* tn) {
+    constexpr int kBand = 8;
+    const int band = lin / (kBand * tiles_m);
+    const int in_band = lin % (kBand * tiles_m);
+    const int band_w = min(kBand, tiles_n - band * kBand);
+    *tm = in_band / band_w;
+    *tn = band * kBand + in_band % band_w;
+}
+
+struct LargeParams {
+    Fp8GemmParams g;
+    int full;      // tiles [0, full) are taken whole; the rest as two halves of 128 rows
+};
+
+template <int BM, bool kTrans, bool kE5M2, bool kE8M0>
+__device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds, int first, int end, int stride) {
+    constexpr int WM = BM / kWavesM, TM = WM / 16;
+    constexpr int kABytes = BM * BK, kStage = kABytes + BN * BK;
+    constexpr int kALoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves;   // 1 KB loads per wave
+    constexpr int kHalves = kMaxM / BM;                                   // tiles of BM rows per 256-row tile
+    static_assert(TM % 2 == 0 && TM >= 4, "row tiles");
+    const Fp8GemmParams& p = lp.g;
+    const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+    float* s_scale = reinterpret_cast<float*>(lds + kRing);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / kWavesN, wn = wave % kWavesN;
+    const int g = lane >> 4, l15 = lane & 15;
+    const int nk = (p.R + BK - 1) / BK;
+
+    if (first >= end) return;
+    int lin = first;
+    int64_t m0 = 0, n0 = 0;
+    v4i rsa, rsw;
+    auto set_tile = [&]() {
+        int tm, tn;
+        tile_of(lin / kHalves, p.tiles_m, p.tiles_n, &tm, &tn);
+        m0 = static_cast<int64_t>(tm) * kMaxM + (lin % kHalves) * BM;
+        n0 = static_cast<int64_t>(tn) * BN;
+        const int rows_a = static_cast<int>(max<int64_t>(0, min<int64_t>(BM, p.M - m0)));
+        rsa = make_rsrc(p.a + m0 * p.R, static_cast<uint32_t>(rows_a) * static_cast<uint32_t>(p.R));
+        if constexpr (!kTrans)
+            rsw = make_rsrc(p.w + n0 * p.R, static_cast<uint32_t>(min<int64_t>(BN, p.N - n0)) * static_cast<uint32_t>(p.R));
+    };
+
+    // Load geometry.  Instruction q of wave w fills LDS rows 8 (8 q + w) .. +8 of an operand (128 bytes
+    // each), lane L the 16 bytes at 16 L; chunk c of row r sits at c ^ (r & 7).  Transposed weights: rows
+    // of 256 bytes (one n), 4 a load, chunk c of row r at c ^ (r & 15).
+    const int kcol = ((lane & 7) ^ (lane >> 3)) << 4;
+    const uint32_t a_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * p.R + kcol);
+    const int tr_row = 4 * wave + (lane >> 4);
+    const uint32_t w_off = kTrans ? static_cast<uint32_t>(tr_row * static_cast<int>(p.N) + (((lane & 15) ^ (tr_row & 15)) << 4))
+                                  : a_off;
+    const uint32_t a_step = static_cast<uint32_t>(8 * kWaves * p.R);                                // rows q -> q + 1
+    const uint32_t w_step = kTrans ? static_cast<uint32_t>(4 * kWaves) * static_cast<uint32_t>(p.N) : a_step;
+    const uint32_t wave_lds = static_cast<uint32_t>(wave * 1024);
+
+    // The stage's scales: thread t holds row t % BM's scale and, for its wave's column block, the
+    // weight's, until they are written to LDS (with 128 rows, threads 256.. write the same again).
+    const int s_row = tid % WM, s_cb = (wave * 64 / BM) & 1;
+    const int s_at = s_cb * kMaxM + ((tid % BM / WM) * 16 + (s_row & 15)) * TM + (s_row >> 4);
+    float r_a = 0.f, r_w = 0.f;
+    auto load_scales = [&](int kb) {
+        const int64_t m = min<int64_t>(m0 + tid % BM, p.M - 1);
+        const int64_t c = min<int64_t>(n0 / BK + s_cb, (p.N - 1) / BK);
+        r_a = load_scale(p.a_scale, kE8M0, static_cast<int64_t>(kb) * p.M + m);
+        r_w = load_scale(p.w_scale, kE8M0, c * p.w_out_stride + kb * p.w_red_stride);
+    };
+    auto write_scales = [&](int slot, float a, float w) { s_scale[slot * 2 * kMaxM + s_at] = a * w; };
+    auto issue = [&](int kb, int slot) {
+        const uint32_t base = lds_base + static_cast<uint32_t>(slot * kStage) + wave_lds;
+        // past the row's end: an offset that every descriptor refuses (loads then give zeros)
+        const uint32_t k0 = kb * BK + kcol < p.R ? static_cast<uint32_t>(kb * BK) : kOob;
+#pragma unroll
+        for (int q = 0; q < kALoads; ++q) load_to_lds(rsa, a_off + q * a_step + k0, base + q * kWaves * 1024);
+        if constexpr (kTrans) {
+            const int rows = min(BK, p.R - kb * BK);
+            rsw = make_rsrc(p.w + static_cast<int64_t>(kb) * BK * p.N + n0, static_cast<uint32_t>(rows * p.N - n0));
+        }
+#pragma unroll
+        for (int q = 0; q < kWLoads; ++q)
+            load_to_lds(rsw, w_off + q * w_step + (kTrans ? 0u : k0), base + kABytes + q * kWaves * 1024);
+        load_scales(kb);
+    };
+
+    const uint32_t f0 = static_cast<uint32_t>(l15 * BK + (((2 * g) ^ (lane & 7)) << 4));
+    const uint32_t f1 = static_cast<uint32_t>(l15 * BK + (((2 * g + 1) ^ (lane & 7)) << 4));
+    auto read_rows = [&](const uint8_t* base) {
+        const v4i x = *reinterpret_cast<const v4i*>(base + f0), y = *reinterpret_cast<const v4i*>(base + f1);
+        return v8i{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    };
+    auto read_a = [&](int slot, int i) { return read_rows(lds + slot * kStage + (wm * WM + i * 16) * BK); };
+    auto read_w = [&](int slot, int j) {
+        if constexpr (kTrans) {
+            v2i r[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = 32 * g + 8 * q + (l15 >> 1);
+                const int chunk = (wn * WN / 16 + j) ^ (row & 15);
+                r[q] = read_tr8(lds_base + static_cast<uint32_t>(slot * kStage + kABytes + row * BN + (chunk << 4) + (lane & 1) * 8));
+            }
+            return v8i{r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
+        } else {
+            return read_rows(lds + slot * kStage + kABytes + (wn * WN + j * 16) * BK);
+        }
+    };
+
+    v4f acc[TM][TN], d[TN];
+    v8i fw[TN], fa[2];
+    float sc[TM], s_last = 0.f;
+    auto read_scales = [&](int slot) {
+        const v4f* q = reinterpret_cast<const v4f*>(s_scale + slot * 2 * kMaxM + (wn / 2) * kMaxM + (wm * 16 + l15) * TM);
+#pragma unroll
+        for (int i = 0; i < TM / 4; ++i) {
+            const v4f x = q[i];
+            sc[4 * i] = x[0];
+            sc[4 * i + 1] = x[1];
+            sc[4 * i + 2] = x[2];
+            sc[4 * i + 3] = x[3];
+        }
+    };
+    auto add = [&](v4f& a, const v4f& x, float s) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = __builtin_fmaf(x[r], s, a[r]);
+    };
+
+    // One stage (block s of the reduction).  kMore: stage s + 1 follows; kMore2: s + 2 too.
+    auto stage = [&](auto more, auto more2, int s) {
+        constexpr bool kMore = decltype(more)::value, kMore2 = decltype(more2)::value;
+        const int slot = s & 1;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                // the sums of the row tile before this one, four instructions old
+                if (i == 0)
+                    add(acc[TM - 1][j], d[j], s_last);
+                else
+                    add(acc[i - 1][j], d[j], sc[i - 1]);
+                d[j] = mfma<kE5M2>(fw[j], fa[i & 1], v4f{0.f, 0.f, 0.f, 0.f});
+                if (i == TM - 1 && kMore) fw[j] = read_w(1 - slot, j);
+            }
+            if (i == 0) read_scales(slot);
+            if (i + 2 < TM) fa[i & 1] = read_a(slot, i + 2);
+            if (i == TM - 2 && kMore) {
+                lds_done();          // this wave's last fragments of the stage are in registers
+                wait_vmcnt<0>();     // its part of stage s + 1, and that stage's scales, have landed
+                write_scales(1 - slot, r_a, r_w);
+                lds_done();
+                barrier();
+                if constexpr (kMore2) issue(s + 2, slot);
+                fa[0] = read_a(1 - slot, 0);
+            }
+            if (i == TM - 1 && kMore) fa[1] = read_a(1 - slot, 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        s_last = sc[TM - 1];
+    };
+    constexpr auto T = std::true_type{};
+    constexpr auto F = std::false_type{};
+
+    // the first two stages of a tile: the first one's scales wait in registers of their own
+    float q_a = 0.f, q_w = 0.f;
+    auto prefetch = [&]() {
+        issue(0, 0);
+        q_a = r_a;
+        q_w = r_w;
+        if (nk > 1) issue(1, 1);
+    };
+    set_tile();
+    prefetch();
+    while (true) {
+        wait_vmcnt<0>();
+        write_scales(0, q_a, q_w);
+        lds_done();
+        barrier();
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            d[j] = v4f{0.f, 0.f, 0.f, 0.f};
+            fw[j] = read_w(0, j);
+        }
+        s_last = 0.f;
+        fa[0] = read_a(0, 0);
+        fa[1] = read_a(0, 1);
+        int s = 0;
+        for (; s + 2 < nk; ++s) stage(T, T, s);
+        if (s + 1 < nk) stage(T, F, s++);
+        stage(F, F, s);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) add(acc[TM - 1][j], d[j], s_last);
+        lds_done();
+        barrier();   // every wave has read its fragments: the ring can be refilled
+
+        const int64_t cm0 = m0 + wm * WM, cn0 = n0 + wn * WN;
+        lin += stride;
+        const bool next = lin < end;
+        if (next) {
+            set_tile();
+            prefetch();
+        }
+        // Epilogue: 16 rows at a time through the wave's 2 KB of LDS (128 bytes a row, chunk c of row r at
+        // c ^ (r & 7)), so that the streaming stores write whole runs of 128 bytes.
+        uint8_t* stg = lds + kRing + kScaleBytes + wave * 2048;
+        const int rr = lane >> 3, rc = lane & 7;
+        const bool vec = p.N % (p.y_bf16 ? 8 : 4) == 0;
+        if (p.y_bf16) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    *reinterpret_cast<uint2*>(stg + l15 * 128 + (((2 * j + (g >> 1)) ^ (l15 & 7)) << 4) + (g & 1) * 8) =
+                        uint2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+                lds_done();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = rr + 8 * h;
+                    const v4i x = *reinterpret_cast<const v4i*>(stg + row * 128 + ((rc ^ (row & 7)) << 4));
+                    const int64_t m = cm0 + i * 16 + row, n = cn0 + rc * 8;
+                    if (m < p.M && n < p.N) {
+                        uint16_t* y = static_cast<uint16_t*>(p.y) + m * p.N + n;
+                        if (vec) {
+                            __builtin_nontemporal_store(x, reinterpret_cast<v4i*>(y));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (n + e < p.N) y[e] = static_cast<uint16_t>(static_cast<uint32_t>(x[e / 2]) >> (16 * (e & 1)));
+                        }
+                    }
+                }
+                lds_done();
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int hj = 0; hj < TN / 2; ++hj) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<v4f*>(stg + l15 * 128 + (((4 * j + g) ^ (l15 & 7)) << 4)) = acc[i][2 * hj + j];
+                    lds_done();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = rr + 8 * h;
+                        const v4f x = *reinterpret_cast<const v4f*>(stg + row * 128 + ((rc ^ (row & 7)) << 4));
+                        const int64_t m = cm0 + i * 16 + row, n = cn0 + hj * 32 + rc * 4;
+                        if (m < p.M && n < p.N) {
+                            float* y = static_cast<float*>(p.y) + m * p.N + n;
+                            if (vec) {
+                                __builtin_nontemporal_store(x, reinterpret_cast<v4f*>(y));
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (n + e < p.N) y[e] = x[e];
+                            }
+                        }
+                    }
+                    lds_done();
+                }
+        }
+        if (!next) break;
+    }
+}
+
+template <bool kTrans, bool kE5M2, bool kE8M0>
+__global__ void __launch_bounds__(kThreads, 1)
+fp8_gemm_large_kernel(LargeParams p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    // Tiles are split into 8 contiguous ranges, one per XCD (block b runs on XCD b % 8); the blocks of an
+    // XCD walk their range together, in bands of 8 N-tiles, and share operand panels in that L2.
+    const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds, stride = gridDim.x / kXcds;
+    const int per = (p.full + kXcds - 1) / kXcds;
+    large_tiles<256, kTrans, kE5M2, kE8M0>(p, lds, xcd * per + local, min((xcd + 1) * per, p.full), stride);
+    const int total = p.g.tiles_m * p.g.tiles_n;
+    const int rest = 2 * (total - p.full), rper = (rest + kXcds - 1) / kXcds;
+    if (rest > 0) {
+        __syncthreads();
+        const int r0 = 2 * p.full;
+        large_tiles<128, kTrans, kE5M2, kE8M0>(p, lds, r0 + xcd * rper + local, r0 + min((xcd + 1) * rper, rest), stride);
+    }
+}
+
+template <bool kTrans, bool kE5M2, bool kE8M0>
+hipError_t launch(const Fp8GemmParams& g, hipStream_t stream) {
+    auto kernel = fp8_gemm_large_kernel<kTrans, kE5M2, kE8M0>;
+    int per_cu = 0;
+    hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), kThreads, kLds, &per_cu);
+    if (e != hipSuccess) return e;
+    LargeParams p{};
+    p.g = g;
+    p.g.tiles_m = static_cast<int>((g.M + kMaxM - 1) / kMaxM);
+    p.g.tiles_n = static_cast<int>((g.N + BN - 1) / BN);
+    const int cus = std::max(kXcds, device_cu_count() / kXcds * kXcds);
+    const int total = p.g.tiles_m * p.g.tiles_n;
+    // whole rounds of 256-row tiles; a remainder that fills at most half a round goes as 128-row halves
+    const int rest = total % cus;
+    p.full = rest > 0 && rest <= cus / 2 ? total - rest : total;
+    kernel<<<cus, kThreads, kLds, stream>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_gemm_large(const Fp8GemmParams& g, bool trans, bool e5m2, hipStream_t stream) {
+    auto pick = [&](auto t, auto f) {
+        constexpr bool kT = decltype(t)::value, kF = decltype(f)::value;
+        return g.e8m0 ? launch<kT, kF, true>(g, stream) : launch<kT, kF, false>(g, stream);
+    };
+    constexpr auto yes = std::true_type{};
+    constexpr auto no = std::false_type{};
+    if (trans) return e5m2 ? pick(yes, yes) : pick(yes, no);
+    return e5m2 ? pick(no, yes) : pick(no, no);
+}
+
+}  // namespace rtq

@@ -13,6 +13,7 @@
 namespace rtq {
 namespace fp8 {
 
+constexpr int BK = 128;                      // reduction bytes per LDS stage: one block of scales
 constexpr int kBufferWord3 = 0x00020000;     // gfx9 buffer descriptor word 3 (raw, 32-bit dwords)
 constexpr uint32_t kOob = 0x80000000u;       // an offset past every descriptor used here: loads give 0
 
@@ -58,5 +59,23 @@ __device__ __forceinline__ v4f mfma(const v8i& w, const v8i& a, v4f c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, kE5M2 ? 1 : 0, 0, 0, 0, 0);
 }
 
+// Kernel arguments of a product: out[m][n] = sum over the reduction r of a[m][r] w[n][r] (or w[r][n]).
+struct Fp8GemmParams {
+    const uint8_t* a;                     // [M][R]
+    const void* a_scale;                  // [blocks of R][M]
+    const uint8_t* w;                     // [N][R], or transposed [R][N]
+    const void* w_scale;
+    int64_t M, N;
+    int R;
+    int tiles_m, tiles_n;
+    int64_t w_out_stride, w_red_stride;   // weight scale of (output block, reduction block)
+    int split;                            // equal ranges of the reduction per tile
+    void* y;                              // output (split 1), or fp32 partials [split][M][N]
+    bool y_bf16, e8m0;
+};
+
 }  // namespace fp8
+
+hipError_t launch_fp8_gemm_large(const fp8::Fp8GemmParams& g, bool trans, bool e5m2, hipStream_t stream);
+
 }  // namespace rtq

@@ -182,6 +182,32 @@ def test_dgrad_exact(T, N, K, fmt, st):
         assert (dx[T] == 7.0).all()
 
 
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("fmt,st", [(E4M3, F32), (E5M2, E8M0), (E4M3, E8M0), (E5M2, F32)])
+@pytest.mark.parametrize("T,N,R", [(4100, 1488, 128), (4100, 1488, 144), (4099, 2288, 272), (4608, 4096, 400), (4608, 4096, 640),
+                                   (25000, 272, 528), (2500, 2800, 2064)])
+def test_large_products_exact(T, N, R, fmt, st, trans):
+    """Outputs of many 256 x 256 tiles: whole rounds of them, halves, one to many reduction blocks."""
+    step("large product", T, N, R, fmt, st, trans)
+    a = int_codes(T + R, T, R).float().to(fmt).cuda()
+    sa, w = pow2_scales(3, groups(R), T).to(st).cuda(), int_codes(N + 1, R if trans else N, N if trans else R).cuda()
+    sw = pow2_scales(4, groups(w.shape[0]), groups(w.shape[1])).to(st).cuda()
+    av = a.double() * sa.double().t().repeat_interleave(128, 1)[:, :R]
+    wv = w.double() * sw.double().repeat_interleave(128, 0)[:w.shape[0]].repeat_interleave(128, 1)[:, :w.shape[1]]
+    ref = av @ (wv if trans else wv.t().contiguous())
+    call = rtq.fp8_dgrad if trans else rtq.fp8_qgemm
+    for dtype in (F32, BF16):
+        y = torch.full((T + 1, N), 7.0, dtype=dtype, device="cuda")
+        call(a, sa, w, sw, y[:T])
+        assert torch.equal(y[:T].double(), ref.float().to(dtype).double())
+        assert (y[T] == 7.0).all()
+    if not trans:                                            # a column count that no store fits
+        y = torch.full((T + 1, N - 3), 7.0, dtype=BF16, device="cuda")
+        call(a, sa, w[:N - 3].contiguous(), sw, y[:T])
+        assert torch.equal(y[:T].double(), ref[:, :N - 3].float().bfloat16().double())
+        assert (y[T] == 7.0).all()
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 300, 2048), (16, 512, 4096), (100, 333, 1040), (300, 512, 2064)])
 def test_product_general(T, N, K):
     """General fp32 scales and codes over the whole range."""
