@@ -216,7 +216,8 @@ int choose_split(int64_t tiles, int blocks) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplit)));
 }
 
-bool use_large(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) >= 96; }
+// (the large kernel's loads run two stages ahead, so it takes reductions of at least two blocks)
+bool use_large(int64_t M, int64_t N, int R) { return R > BK && ((M + 255) / 256) * ((N + 255) / 256) >= 96; }
 
 template <bool kTrans, bool kE5M2>
 hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
@@ -240,7 +241,7 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
     p.w_out_stride = kTrans ? 1 : fp8_groups(g.R);
     p.w_red_stride = kTrans ? fp8_groups(g.N) : 1;
     p.y_bf16 = g.y_bf16;
-    if (use_large(g.M, g.N)) {
+    if (use_large(g.M, g.N, g.R)) {
         p.y = g.y;
         p.split = 1;
         return launch_fp8_gemm_large(p, kTrans, kE5M2, stream);
@@ -262,7 +263,7 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int R, bool trans) {
     (void)trans;
-    if (use_large(M, N)) return 0;
+    if (use_large(M, N, R)) return 0;
     const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
     const int split = choose_split(tiles, static_cast<int>(fp8_groups(R)));
     return split > 1 ? static_cast<size_t>(split) * M * N * sizeof(float) : 0;

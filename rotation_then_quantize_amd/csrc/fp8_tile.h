@@ -59,6 +59,13 @@ __device__ __forceinline__ v4f mfma(const v8i& w, const v8i& a, v4f c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, kE5M2 ? 1 : 0, 0, 0, 0, 0);
 }
 
+// The same with E8M0 scales, added to c: byte kByte of `scales` is that of the second operand's row (the
+// lane's), the byte above it the weight block's.
+template <bool kE5M2, int kByte>
+__device__ __forceinline__ v4f mfma_scaled(const v8i& w, const v8i& a, v4f c, int scales) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, kE5M2 ? 1 : 0, kByte + 1, scales, kByte, scales);
+}
+
 // Kernel arguments of a product: out[m][n] = sum over the reduction r of a[m][r] w[n][r] (or w[r][n]).
 struct Fp8GemmParams {
     const uint8_t* a;                     // [M][R]
