@@ -74,17 +74,17 @@ fp8_gemm_kernel(Fp8GemmParams p) {
     const v4i rsa = make_rsrc(p.a + m0 * p.R, static_cast<uint32_t>(rows_a) * static_cast<uint32_t>(p.R));
     v4i rsw = make_rsrc(p.w + (kTrans ? 0 : n0 * p.R), static_cast<uint32_t>(rows_w) * static_cast<uint32_t>(p.R));
 
-    // LDS rows of 128 bytes, chunk c (16 bytes) of row r at chunk c ^ (r & 7): eight lanes reading the
-    // same chunk of eight rows touch all banks once, and a load instruction fills 8 whole rows.
-    // Transposed weights: rows of BN bytes (row: one n of the block), chunk c of row r at
-    // c ^ ((r * BN / 256) % chunks), so that the 8 rows of a transposing read touch all banks once.
+    // LDS rows of 128 bytes, chunk c (16 bytes) of row r at chunk c ^ ((r >> 1) & 7); lane group g holds
+    // chunks g and g + 4 of its row, which makes the 16-byte reads free of bank conflicts (see the large
+    // kernel).  Transposed weights: rows of BN bytes (one n), chunk c of row r at c ^ row_swizzle(r): 8 rows
+    // of one chunk touch all banks once.
     auto row_swizzle = [](int row) { return (row * BN / 256) & (kChunks - 1); };
     auto issue = [&](int kb) {
         const uint32_t slot = lds_base + static_cast<uint32_t>(((kb - kb0) % kSlots) * kStage);
 #pragma unroll
         for (int q = 0; q < kALoads; ++q) {
             const int row = 8 * (q * kWaves + wave) + (lane >> 3);
-            const int col = kb * BK + (((lane & 7) ^ (lane >> 3)) << 4);
+            const int col = kb * BK + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
             load_to_lds(rsa, col < p.R ? static_cast<uint32_t>(row * p.R + col) : kOob,
                         slot + static_cast<uint32_t>((q * kWaves + wave) * 1024));
         }
@@ -101,14 +101,14 @@ fp8_gemm_kernel(Fp8GemmParams p) {
                 off = static_cast<uint32_t>(row * static_cast<int>(p.N) + (((lane % kChunks) ^ row_swizzle(row)) << 4));
             } else {
                 const int row = 8 * (q * kWaves + wave) + (lane >> 3);
-                const int col = kb * BK + (((lane & 7) ^ (lane >> 3)) << 4);
+                const int col = kb * BK + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
                 off = col < p.R ? static_cast<uint32_t>(row * p.R + col) : kOob;
             }
             load_to_lds(rsw, off, slot + static_cast<uint32_t>(kABytes + (q * kWaves + wave) * 1024));
         }
     };
-    const uint32_t f0 = static_cast<uint32_t>(l15 * BK + (((2 * g) ^ (lane & 7)) << 4));
-    const uint32_t f1 = static_cast<uint32_t>(l15 * BK + (((2 * g + 1) ^ (lane & 7)) << 4));
+    const uint32_t f0 = static_cast<uint32_t>(l15 * BK + ((g ^ (l15 >> 1)) << 4));
+    const uint32_t f1 = static_cast<uint32_t>(l15 * BK + (((g + 4) ^ (l15 >> 1)) << 4));
     auto read_frag = [&](const uint8_t* base) {
         const v4i x = *reinterpret_cast<const v4i*>(base + f0), y = *reinterpret_cast<const v4i*>(base + f1);
         return v8i{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -117,7 +117,7 @@ fp8_gemm_kernel(Fp8GemmParams p) {
         v2i r[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int row = 32 * g + 8 * q + (l15 >> 1);
+            const int row = 64 * (q >> 1) + 16 * g + 8 * (q & 1) + (l15 >> 1);
             r[q] = read_tr8(base + static_cast<uint32_t>(row * BN + ((chunk ^ row_swizzle(row)) << 4) + (lane & 1) * 8));
         }
         return v8i{r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};

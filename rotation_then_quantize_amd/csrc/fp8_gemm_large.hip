@@ -114,12 +114,17 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     };
 
     // Load geometry.  Instruction q of wave w fills LDS rows 8 (8 q + w) .. +8 of an operand (128 bytes
-    // each), lane L the 16 bytes at 16 L; chunk c of row r sits at c ^ (r & 7).  Transposed weights: rows
-    // of 256 bytes (one n), 4 a load, chunk c of row r at c ^ (r & 15).
-    const int kcol = ((lane & 7) ^ (lane >> 3)) << 4;
+    // each), lane L the 16 bytes at 16 L; chunk c of row r sits at c ^ ((r >> 1) & 7).  Lane group g holds
+    // chunks g and g + 4 of its row (any order serves, if both operands have it).  A 16-byte LDS read
+    // takes 16 lanes at a time, 8 of them from one lane group and 8 of the next (0-3, 12-15 and 20-27 are
+    // the first 16): with chunks g and g + 1 their rows' places fall on all 64 banks once.
+    // Transposed weights: rows of 256 bytes (one n), 4 a load, chunk c of row r at c ^ tr_swizzle(r): 8
+    // rows of one chunk for each of two lane groups touch all banks once.
+    const int kcol = ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) << 4;
     const uint32_t a_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * p.R + kcol);
     const int tr_row = 4 * wave + (lane >> 4);
-    const uint32_t w_off = kTrans ? static_cast<uint32_t>(tr_row * static_cast<int>(p.N) + (((lane & 15) ^ (tr_row & 15)) << 4))
+    auto tr_swizzle = [](int row) { return (row & 7) | ((row >> 4) & 1) << 3; };
+    const uint32_t w_off = kTrans ? static_cast<uint32_t>(tr_row * static_cast<int>(p.N) + (((lane & 15) ^ tr_swizzle(tr_row)) << 4))
                                   : a_off;
     const uint32_t a_step = static_cast<uint32_t>(8 * kWaves * p.R);                                // rows q -> q + 1
     const uint32_t w_step = kTrans ? static_cast<uint32_t>(4 * kWaves) * static_cast<uint32_t>(p.N) : a_step;
@@ -165,10 +170,10 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         ++c_kb;
     };
 
-    const uint32_t f0 = static_cast<uint32_t>(l15 * BK + (((2 * g) ^ (lane & 7)) << 4));
-    const uint32_t f1 = static_cast<uint32_t>(l15 * BK + (((2 * g + 1) ^ (lane & 7)) << 4));
-    const uint32_t tr0 = lds_base + static_cast<uint32_t>(kABytes + (32 * g + (l15 >> 1)) * BN +
-                                                          (((4 * wn) ^ (l15 >> 1)) << 4) + (lane & 1) * 8);
+    const uint32_t f0 = static_cast<uint32_t>(l15 * BK + ((g ^ (l15 >> 1)) << 4));
+    const uint32_t f1 = static_cast<uint32_t>(l15 * BK + (((g + 4) ^ (l15 >> 1)) << 4));
+    const uint32_t tr0 = lds_base + static_cast<uint32_t>(kABytes + (16 * g + (l15 >> 1)) * BN +
+                                                          (((4 * wn) ^ tr_swizzle(16 * g + (l15 >> 1))) << 4) + (lane & 1) * 8);
     auto read_rows = [&](const uint8_t* base) {
         const v4i x = *reinterpret_cast<const v4i*>(base + f0), y = *reinterpret_cast<const v4i*>(base + f1);
         return v8i{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -176,12 +181,10 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     auto read_a = [&](int slot, int i) { return read_rows(lds + slot * kStage + (wm * WM + i * 16) * BK); };
     auto read_w = [&](int slot, int j) {
         if constexpr (kTrans) {
-            // row 32 g + 8 q + r (r = l15 / 2), chunk (4 wn + j) ^ (row & 15): j and q's parity are bits of
-            // the first address, so one register serves all of them
-            const uint32_t base = tr0 + static_cast<uint32_t>(slot * kStage);
-            v2i r[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) r[q] = read_tr8((base ^ static_cast<uint32_t>((j << 4) | ((q & 1) << 7))) + q * 8 * BN);
+            // rows 16 g + r, + 8, + 64, + 72 (r = l15 / 2), chunk (4 wn + j) ^ tr_swizzle: the rows' swizzle is
+            // one and j two bits of the first address, so one register serves all of them
+            const uint32_t base = (tr0 + static_cast<uint32_t>(slot * kStage)) ^ static_cast<uint32_t>(j << 4);
+            const v2i r[4] = {read_tr8(base), read_tr8(base + 8 * BN), read_tr8(base + 64 * BN), read_tr8(base + 72 * BN)};
             return v8i{r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
         } else {
             return read_rows(lds + slot * kStage + kABytes + (wn * WN + j * 16) * BK);
