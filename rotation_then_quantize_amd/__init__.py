@@ -11,6 +11,7 @@ per token and multiplied against the quantised weights, where Pi^T Pi = I cancel
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -385,78 +386,75 @@ def fp8_groups(d: int) -> int:
     return -(-d // FP8_BLOCK)
 
 
-def _fp8_types():
+@functools.lru_cache(maxsize=None)
+def _types():
+    """Type codes of (float, 8-bit float, e4m3 only, scale) dtypes."""
     torch = _torch()
-    return {torch.float8_e4m3fn: RTQ_E4M3, torch.float8_e5m2: RTQ_E5M2}
-
-
-def _scale_types():
-    torch = _torch()
-    return {torch.float32: RTQ_F32, torch.float8_e8m0fnu: RTQ_E8M0}
-
-
-def _float_types():
-    torch = _torch()
-    return {torch.float32: RTQ_F32, torch.bfloat16: RTQ_BF16}
+    e4m3 = {torch.float8_e4m3fn: RTQ_E4M3}
+    return ({torch.float32: RTQ_F32, torch.bfloat16: RTQ_BF16}, {**e4m3, torch.float8_e5m2: RTQ_E5M2}, e4m3,
+            {torch.float32: RTQ_F32, torch.float8_e8m0fnu: RTQ_E8M0})
 
 
 def _operand(t, name: str, types: dict, shape=None, like=None) -> int:
     """Type code of a device tensor, after checking its type, shape, layout and device."""
-    if t.dtype not in types:
+    code = types.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.dim() != 2 if shape is None else t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {'two dimensions' if shape is None else tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if like is not None and t.device != like.device:
+    if like is not None and t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    return types[t.dtype]
+    return code
 
 
 class _Launch:
     """The device and stream of one call, and its workspace."""
 
     def __init__(self, like, stream):
-        torch = _torch()
         if stream is not None and stream.device != like.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
-        self._device = like.device
-        self._guard = torch.cuda.device(like.device)
+        self._like = like
         self._user_stream = stream
 
     def __enter__(self):
-        self._guard.__enter__()
-        self.stream = _stream(self._user_stream)
+        cuda = _torch().cuda
+        index = self._like.get_device()
+        self._guard = None
+        if index != cuda.current_device():
+            self._guard = cuda.device(index)
+            self._guard.__enter__()
+        stream = cuda.current_stream(index) if self._user_stream is None else self._user_stream
+        self.stream = stream.cuda_stream
         return self
 
     def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
 
     def workspace(self, given, need: int):
         """(pointer, bytes) of the caller's workspace, or of a temporary one of `need` bytes."""
         if given is None:
             if need == 0:
-                self._ws = None
                 return 0, 0
-            self._ws = _stream_local_workspace(_torch(), need, self._device, self._user_stream)
-        else:
-            if given.device != self._device:
-                raise ValueError(f"workspace is on {given.device}, expected {self._device}")
-            if not given.is_contiguous():
-                raise ValueError("workspace must be contiguous")
-            self._ws = given
-        return _ptr(self._ws), self._ws.numel() * self._ws.element_size()
+            given = self._ws = _stream_local_workspace(_torch(), need, self._like.device, self._user_stream)
+        elif given.get_device() != self._like.get_device():
+            raise ValueError(f"workspace is on {given.device}, expected {self._like.device}")
+        elif not given.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return given.data_ptr(), given.numel() * given.element_size()
 
 
 def fp8_quantize(x, codes, scale, blocks: bool = False, stream=None):
     """Codes and power-of-two scales of x [rows][d]: row groups of 128 (scale [groups][rows],
     group-major) or, with blocks, 128 x 128 blocks (scale [row blocks][column blocks])."""
-    xt = _operand(x, "x", _float_types())
+    xt = _operand(x, "x", _types()[0])
     rows, d = x.shape
-    ct = _operand(codes, "codes", _fp8_types(), x.shape, x)
-    st = _operand(scale, "scale", _scale_types(),
+    ct = _operand(codes, "codes", _types()[1], x.shape, x)
+    st = _operand(scale, "scale", _types()[3],
                   (fp8_groups(rows), fp8_groups(d)) if blocks else (fp8_groups(d), rows), x)
     with _Launch(x, stream) as go:
         _check(load_library().rtq_fp8_quantize(_ptr(x), xt, rows, d, RTQ_FP8_BLOCKS if blocks else RTQ_FP8_ROWS,
@@ -466,11 +464,11 @@ def fp8_quantize(x, codes, scale, blocks: bool = False, stream=None):
 
 def fp8_dequantize(codes, scale, y, blocks: bool = False, stream=None):
     """y = code * scale, for codes and scales as fp8_quantize writes them."""
-    ct = _operand(codes, "codes", _fp8_types())
+    ct = _operand(codes, "codes", _types()[1])
     rows, d = codes.shape
-    st = _operand(scale, "scale", _scale_types(),
+    st = _operand(scale, "scale", _types()[3],
                   (fp8_groups(rows), fp8_groups(d)) if blocks else (fp8_groups(d), rows), codes)
-    yt = _operand(y, "y", _float_types(), codes.shape, codes)
+    yt = _operand(y, "y", _types()[0], codes.shape, codes)
     with _Launch(codes, stream) as go:
         _check(load_library().rtq_fp8_dequantize(_ptr(codes), ct, _ptr(scale), st, rows, d,
                                                  RTQ_FP8_BLOCKS if blocks else RTQ_FP8_ROWS, _ptr(y), yt, go.stream))
@@ -479,10 +477,9 @@ def fp8_dequantize(codes, scale, y, blocks: bool = False, stream=None):
 
 def _fp8_weight(w_codes, w_scale, like):
     """(N, K, scale type code) of block-scaled weight codes."""
-    torch = _torch()
-    _operand(w_codes, "w_codes", {torch.float8_e4m3fn: RTQ_E4M3}, None, like)
+    _operand(w_codes, "w_codes", _types()[2], None, like)
     N, K = w_codes.shape
-    return N, K, _operand(w_scale, "w_scale", _scale_types(), (fp8_groups(N), fp8_groups(K)), like)
+    return N, K, _operand(w_scale, "w_scale", _types()[3], (fp8_groups(N), fp8_groups(K)), like)
 
 
 def _same_scale(a, name: str, w_scale):
@@ -498,12 +495,12 @@ def fp8_qgemm(a_codes, a_scale, w_codes, w_scale, y, workspace=None, stream=None
     """y [T][N] = a W^T of row-group codes a [T][K] and block codes W [N][K]."""
     N, K, st = _fp8_weight(w_codes, w_scale, a_codes)
     T = a_codes.shape[0]
-    at = _operand(a_codes, "a_codes", _fp8_types(), (T, K))
-    _operand(a_scale, "a_scale", _scale_types(), (fp8_groups(K), T), a_codes)
+    at = _operand(a_codes, "a_codes", _types()[1], (T, K))
+    _operand(a_scale, "a_scale", _types()[3], (fp8_groups(K), T), a_codes)
     _same_scale(a_scale, "a_scale", w_scale)
-    yt = _operand(y, "y", _float_types(), (T, N), a_codes)
+    yt = _operand(y, "y", _types()[0], (T, N), a_codes)
     with _Launch(a_codes, stream) as go:
-        ws, nbytes = go.workspace(workspace, fp8_qgemm_workspace(T, N, K))
+        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_qgemm_workspace(T, N, K))
         _check(load_library().rtq_fp8_qgemm(_ptr(a_codes), at, _ptr(a_scale), T, _ptr(w_codes), _ptr(w_scale), st, N, K,
                                             _ptr(y), yt, ws, nbytes, go.stream))
     return y
@@ -517,12 +514,12 @@ def fp8_dgrad(g_codes, g_scale, w_codes, w_scale, dx, workspace=None, stream=Non
     """dx [T][K] = g W of row-group codes g [T][N] (quantised output gradients) and block codes W [N][K]."""
     N, K, st = _fp8_weight(w_codes, w_scale, g_codes)
     T = g_codes.shape[0]
-    gt = _operand(g_codes, "g_codes", _fp8_types(), (T, N))
-    _operand(g_scale, "g_scale", _scale_types(), (fp8_groups(N), T), g_codes)
+    gt = _operand(g_codes, "g_codes", _types()[1], (T, N))
+    _operand(g_scale, "g_scale", _types()[3], (fp8_groups(N), T), g_codes)
     _same_scale(g_scale, "g_scale", w_scale)
-    dxt = _operand(dx, "dx", _float_types(), (T, K), g_codes)
+    dxt = _operand(dx, "dx", _types()[0], (T, K), g_codes)
     with _Launch(g_codes, stream) as go:
-        ws, nbytes = go.workspace(workspace, fp8_dgrad_workspace(T, N, K))
+        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_dgrad_workspace(T, N, K))
         _check(load_library().rtq_fp8_dgrad(_ptr(g_codes), gt, _ptr(g_scale), T, _ptr(w_codes), _ptr(w_scale), st, N, K,
                                             _ptr(dx), dxt, ws, nbytes, go.stream))
     return dx
@@ -535,19 +532,18 @@ def fp8_linear_workspace(T: int, N: int, K: int) -> int:
 def fp8_linear(x, w_codes, w_scale, y, x_codes=None, x_scale=None, workspace=None, stream=None):
     """y [T][N] = quantise(x) W^T for x [T][K] and block codes W [N][K].  With x_codes [T][K] (e4m3)
     and x_scale [groups][T] the codes the product read are kept: the checkpoint fp8_wgrad takes."""
-    torch = _torch()
     N, K, st = _fp8_weight(w_codes, w_scale, x)
     T = x.shape[0]
-    xt = _operand(x, "x", _float_types(), (T, K))
-    yt = _operand(y, "y", _float_types(), (T, N), x)
+    xt = _operand(x, "x", _types()[0], (T, K))
+    yt = _operand(y, "y", _types()[0], (T, N), x)
     if (x_codes is None) != (x_scale is None):
         raise ValueError("x_codes and x_scale are given together or not at all")
     if x_codes is not None:
-        _operand(x_codes, "x_codes", {torch.float8_e4m3fn: RTQ_E4M3}, (T, K), x)
-        _operand(x_scale, "x_scale", _scale_types(), (fp8_groups(K), T), x)
+        _operand(x_codes, "x_codes", _types()[2], (T, K), x)
+        _operand(x_scale, "x_scale", _types()[3], (fp8_groups(K), T), x)
         _same_scale(x_scale, "x_scale", w_scale)
     with _Launch(x, stream) as go:
-        ws, nbytes = go.workspace(workspace, fp8_linear_workspace(T, N, K))
+        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_linear_workspace(T, N, K))
         _check(load_library().rtq_fp8_linear(_ptr(x), xt, T, _ptr(w_codes), _ptr(w_scale), st, N, K, _ptr(x_codes),
                                              _ptr(x_scale), _ptr(y), yt, ws, nbytes, go.stream))
     return y
@@ -563,14 +559,14 @@ def fp8_linear_dgrad(dy, w_codes, w_scale, dx, grad_dtype=None, workspace=None, 
     torch = _torch()
     N, K, st = _fp8_weight(w_codes, w_scale, dy)
     T = dy.shape[0]
-    dyt = _operand(dy, "dy", _float_types(), (T, N))
-    dxt = _operand(dx, "dx", _float_types(), (T, K), dy)
+    dyt = _operand(dy, "dy", _types()[0], (T, N))
+    dxt = _operand(dx, "dx", _types()[0], (T, K), dy)
     grad_dtype = torch.float8_e5m2 if grad_dtype is None else grad_dtype
-    if grad_dtype not in _fp8_types():
+    if grad_dtype not in _types()[1]:
         raise TypeError(f"grad_dtype: unsupported dtype {grad_dtype}")
     with _Launch(dy, stream) as go:
-        ws, nbytes = go.workspace(workspace, fp8_linear_dgrad_workspace(T, N, K))
-        _check(load_library().rtq_fp8_linear_dgrad(_ptr(dy), dyt, _fp8_types()[grad_dtype], T, _ptr(w_codes),
+        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_linear_dgrad_workspace(T, N, K))
+        _check(load_library().rtq_fp8_linear_dgrad(_ptr(dy), dyt, _types()[1][grad_dtype], T, _ptr(w_codes),
                                                    _ptr(w_scale), st, N, K, _ptr(dx), dxt, ws, nbytes, go.stream))
     return dx
 
@@ -585,12 +581,12 @@ def fp8_wgrad(dy, x_codes, x_scale, dw, accumulate: bool = False, workspace=None
     torch = _torch()
     _operand(dy, "dy", {torch.bfloat16: RTQ_BF16})
     T, N = dy.shape
-    _operand(x_codes, "x_codes", {torch.float8_e4m3fn: RTQ_E4M3}, (T, x_codes.shape[-1]), dy)
+    _operand(x_codes, "x_codes", _types()[2], (T, x_codes.shape[-1]), dy)
     K = x_codes.shape[1]
-    st = _operand(x_scale, "x_scale", _scale_types(), (fp8_groups(K), T), dy)
-    dwt = _operand(dw, "dw", _float_types(), (N, K), dy)
+    st = _operand(x_scale, "x_scale", _types()[3], (fp8_groups(K), T), dy)
+    dwt = _operand(dw, "dw", _types()[0], (N, K), dy)
     with _Launch(dy, stream) as go:
-        ws, nbytes = go.workspace(workspace, fp8_wgrad_workspace(T, N, K))
+        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_wgrad_workspace(T, N, K))
         _check(load_library().rtq_fp8_wgrad(_ptr(dy), T, _ptr(x_codes), _ptr(x_scale), st, N, K, _ptr(dw), dwt,
                                             1 if accumulate else 0, ws, nbytes, go.stream))
     return dw
@@ -599,12 +595,11 @@ def fp8_wgrad(dy, x_codes, x_scale, dw, accumulate: bool = False, workspace=None
 def act_fp8_forward(h, act: int, h_codes, h_scale, y=None, y_codes=None, y_scale=None, stream=None):
     """y = f(h) with h kept as codes [rows][d] (e4m3) and scales [groups][rows]; f is RTQ_ACT_GELU_TANH,
     RTQ_ACT_GELU or RTQ_ACT_SILU.  y comes back as y (h's type), or quantised as y_codes, y_scale."""
-    torch = _torch()
-    e4m3 = {torch.float8_e4m3fn: RTQ_E4M3}
-    ht = _operand(h, "h", _float_types())
+    e4m3 = _types()[2]
+    ht = _operand(h, "h", _types()[0])
     rows, d = h.shape
     _operand(h_codes, "h_codes", e4m3, h.shape, h)
-    st = _operand(h_scale, "h_scale", _scale_types(), (fp8_groups(d), rows), h)
+    st = _operand(h_scale, "h_scale", _types()[3], (fp8_groups(d), rows), h)
     if (y_codes is None) != (y_scale is None) or (y is None) == (y_codes is None):
         raise ValueError("give either y, or y_codes and y_scale")
     if y is not None:
@@ -620,11 +615,10 @@ def act_fp8_forward(h, act: int, h_codes, h_scale, y=None, y_codes=None, y_scale
 
 def act_fp8_backward(dy, h_codes, h_scale, act: int, dh, stream=None):
     """dh = dy f'(h^) from the checkpoint of h (act_fp8_forward).  dh may be dy."""
-    torch = _torch()
-    dyt = _operand(dy, "dy", _float_types())
+    dyt = _operand(dy, "dy", _types()[0])
     rows, d = dy.shape
-    _operand(h_codes, "h_codes", {torch.float8_e4m3fn: RTQ_E4M3}, dy.shape, dy)
-    st = _operand(h_scale, "h_scale", _scale_types(), (fp8_groups(d), rows), dy)
+    _operand(h_codes, "h_codes", _types()[2], dy.shape, dy)
+    st = _operand(h_scale, "h_scale", _types()[3], (fp8_groups(d), rows), dy)
     _operand(dh, "dh", {dy.dtype: dyt}, dy.shape, dy)
     with _Launch(dy, stream) as go:
         _check(load_library().rtq_act_fp8_backward(_ptr(dy), dyt, _ptr(h_codes), _ptr(h_scale), st, rows, d, act,

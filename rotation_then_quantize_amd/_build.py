@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librtq.so")
-SOURCES = ["rpbh_rows.hip", "rpbh_quant.hip", "gemm_i8.hip", "gemm_lut.hip", "fp8_rows.hip", "fp8_gemm.hip", "fp8_gemm_large.hip",
+SOURCES = ["rpbh_rows.hip", "rpbh_quant.hip", "gemm_i8.hip", "gemm_lut.hip", "fp8_rows.hip", "fp8_gemm.hip", "fp8_gemm_large.hip", "fp8_small.hip",
            "fp8_wgrad.hip", "rtq_api.cpp", "fp8_api.cpp", "rtq_host.cpp", "launch_cache.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -229,7 +229,8 @@ rtq_status rtq_fp8_linear(const void* x, rtq_dtype xt, int64_t T, const void* w_
         RTQ_TRY(check_workspace(workspace));
         unsigned char* ws = static_cast<unsigned char*>(workspace);
         size_t left = workspace != nullptr ? ws_bytes : 0;
-        if (T > 0 && x_codes == nullptr) {
+        const bool keep = x_codes != nullptr;
+        if (T > 0 && !keep) {
             const size_t need = code_part(T, K) + scale_part(T, K);
             if (workspace == nullptr) return fail(RTQ_ERR_INVALID_ARG, "workspace is NULL");
             if (left < need) return fail(RTQ_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", left, need);
@@ -245,7 +246,10 @@ rtq_status rtq_fp8_linear(const void* x, rtq_dtype xt, int64_t T, const void* w_
         if (T == 0) return ok();
         g.workspace = left > 0 ? ws : nullptr;
         g.ws_bytes = left;
-        return quantize_then_gemm(q, g, static_cast<hipStream_t>(stream));
+        hipStream_t s = static_cast<hipStream_t>(stream);
+        if (!keep && rtq::fp8_small_linear_takes(T))
+            return hip_status(rtq::launch_fp8_small_linear(g, x, xt == RTQ_BF16, s), "fp8 product launch");
+        return quantize_then_gemm(q, g, s);
     });
 }
 

@@ -43,8 +43,12 @@ __device__ __forceinline__ float e8m0_value(uint32_t b) {
     const uint32_t u = b == 0u ? 0x00400000u : (b == 255u ? 0x7fc00000u : b << 23);
     return __uint_as_float(u);
 }
-__device__ __forceinline__ float load_scale(const void* s, bool e8m0, int64_t i) {
-    return e8m0 ? e8m0_value(static_cast<const uint8_t*>(s)[i]) : static_cast<const float*>(s)[i];
+// The scale type is a template parameter wherever scales are loaded: with a run-time flag the compiler may
+// turn the choice into lane masks and let the other type's scalar load run, past the end of the array.
+template <bool kE8M0>
+__device__ __forceinline__ float load_scale(const void* s, int64_t i) {
+    if constexpr (kE8M0) return e8m0_value(static_cast<const uint8_t*>(s)[i]);
+    return static_cast<const float*>(s)[i];
 }
 __device__ __forceinline__ void store_scale(void* s, bool e8m0, int64_t i, int e) {
     if (e8m0)

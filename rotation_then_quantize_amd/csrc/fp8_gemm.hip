@@ -45,7 +45,7 @@ __device__ __forceinline__ void store4(void* y, bool bf16, int64_t M, int64_t N,
     }
 }
 
-template <int BM, int BN, int kWavesM, int kWavesN, int kSlots, bool kTrans, bool kE5M2>
+template <int BM, int BN, int kWavesM, int kWavesN, int kSlots, bool kTrans, bool kE5M2, bool kE8M0>
 __global__ void __launch_bounds__(64 * kWavesM * kWavesN)
 fp8_gemm_kernel(Fp8GemmParams p) {
     constexpr int kWaves = kWavesM * kWavesN;
@@ -139,10 +139,10 @@ fp8_gemm_kernel(Fp8GemmParams p) {
         if (kb0 + s < kb1) issue(kb0 + s);
     constexpr int kLoads = kALoads + kWLoads;
     for (int kb = kb0; kb < kb1; ++kb) {
-        const float sw = load_scale(p.w_scale, p.e8m0, wblock * p.w_out_stride + kb * p.w_red_stride);
+        const float sw = load_scale<kE8M0>(p.w_scale, wblock * p.w_out_stride + kb * p.w_red_stride);
         float s[TM];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) s[i] = load_scale(p.a_scale, p.e8m0, kb * p.M + mi[i]) * sw;
+        for (int i = 0; i < TM; ++i) s[i] = load_scale<kE8M0>(p.a_scale, kb * p.M + mi[i]) * sw;
         // block kb has landed (later blocks may be in flight), in every wave; block kb - 1 is read
         if (kSlots > 2 && kb + kSlots - 2 < kb1)
             wait_vmcnt<(kSlots - 2) * kLoads>();
@@ -223,29 +223,18 @@ template <bool kTrans, bool kE5M2>
 hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
     constexpr int kSlots = 4;
     constexpr size_t lds = static_cast<size_t>(kSlots) * 2 * kTile * BK;
-    auto kernel = fp8_gemm_kernel<kTile, kTile, 2, 2, kSlots, kTrans, kE5M2>;
+    auto kernel = g.e8m0 ? fp8_gemm_kernel<kTile, kTile, 2, 2, kSlots, kTrans, kE5M2, true>
+                         : fp8_gemm_kernel<kTile, kTile, 2, 2, kSlots, kTrans, kE5M2, false>;
     int per_cu = 0;
     hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), 256, lds, &per_cu);
     if (e != hipSuccess) return e;
-    Fp8GemmParams p{};
-    p.e8m0 = g.e8m0;
-    p.a = static_cast<const uint8_t*>(g.a);
-    p.a_scale = g.a_scale;
-    p.w = static_cast<const uint8_t*>(g.w);
-    p.w_scale = g.w_scale;
-    p.M = g.M;
-    p.N = g.N;
-    p.R = g.R;
-    p.tiles_m = static_cast<int>((g.M + kTile - 1) / kTile);
-    p.tiles_n = static_cast<int>((g.N + kTile - 1) / kTile);
-    p.w_out_stride = kTrans ? 1 : fp8_groups(g.R);
-    p.w_red_stride = kTrans ? fp8_groups(g.N) : 1;
-    p.y_bf16 = g.y_bf16;
+    Fp8GemmParams p = fp8_gemm_params(g);
+    if (!kTrans && fp8_small_takes(g.M)) return launch_fp8_small(p, kE5M2, stream);
     if (use_large(g.M, g.N, g.R)) {
-        p.y = g.y;
-        p.split = 1;
         return launch_fp8_gemm_large(p, kTrans, kE5M2, stream);
     }
+    p.tiles_m = static_cast<int>((g.M + kTile - 1) / kTile);
+    p.tiles_n = static_cast<int>((g.N + kTile - 1) / kTile);
     const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
     p.split = choose_split(tiles, static_cast<int>(fp8_groups(g.R)));
     if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(p.split) * g.M * g.N * sizeof(float)) p.split = 1;
@@ -261,9 +250,26 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
 
 }  // namespace
 
+fp8::Fp8GemmParams fp8_gemm_params(const Fp8GemmArgs& g) {
+    fp8::Fp8GemmParams p{};
+    p.a = static_cast<const uint8_t*>(g.a);
+    p.a_scale = g.a_scale;
+    p.w = static_cast<const uint8_t*>(g.w);
+    p.w_scale = g.w_scale;
+    p.e8m0 = g.e8m0;
+    p.M = g.M;
+    p.N = g.N;
+    p.R = g.R;
+    p.w_out_stride = g.trans ? 1 : fp8_groups(g.R);
+    p.w_red_stride = g.trans ? fp8_groups(g.N) : 1;
+    p.split = 1;
+    p.y = g.y;
+    p.y_bf16 = g.y_bf16;
+    return p;
+}
+
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int R, bool trans) {
-    (void)trans;
-    if (use_large(M, N, R)) return 0;
+    if ((!trans && fp8_small_takes(M)) || use_large(M, N, R)) return 0;
     const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
     const int split = choose_split(tiles, static_cast<int>(fp8_groups(R)));
     return split > 1 ? static_cast<size_t>(split) * M * N * sizeof(float) : 0;

@@ -12,6 +12,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/rtq.h"
 #include "fp8_device.h"
 #include "fp8_internal.h"
@@ -205,9 +207,9 @@ fp8_blocks_kernel(const void* __restrict__ x, int64_t rows, int d, void* __restr
 // Elementwise passes over codes: a thread takes 8 elements of kElemRows rows.
 constexpr int kElemRows = 4;
 
-template <bool kE5M2, bool kBF16>
+template <bool kE5M2, bool kBF16, bool kE8M0>
 __global__ void __launch_bounds__(kThreads)
-fp8_dequant_kernel(const uint8_t* __restrict__ codes, const void* __restrict__ scale, bool e8m0, bool blocks,
+fp8_dequant_kernel(const uint8_t* __restrict__ codes, const void* __restrict__ scale, bool blocks,
                    int64_t rows, int d, int64_t units, void* __restrict__ y) {
     const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
     if (u >= units) return;
@@ -221,8 +223,7 @@ fp8_dequant_kernel(const uint8_t* __restrict__ codes, const void* __restrict__ s
     for (int r = 0; r < kElemRows; ++r) {
         if (r0 + r < rows) {
             q[r] = *reinterpret_cast<const uint2*>(codes + (r0 + r) * d + c);
-            s[r] = load_scale(scale, e8m0,
-                              blocks ? (r0 + r) / kFp8Block * groups + c / kFp8Block : c / kFp8Block * rows + r0 + r);
+            s[r] = load_scale<kE8M0>(scale, blocks ? (r0 + r) / kFp8Block * groups + c / kFp8Block : c / kFp8Block * rows + r0 + r);
         }
     }
 #pragma unroll
@@ -238,10 +239,10 @@ fp8_dequant_kernel(const uint8_t* __restrict__ codes, const void* __restrict__ s
     }
 }
 
-template <bool kBF16, int kAct>
+template <bool kBF16, int kAct, bool kE8M0>
 __global__ void __launch_bounds__(kThreads)
 act_backward_kernel(const void* dy, const uint8_t* __restrict__ codes, const void* __restrict__ scale,
-                    bool e8m0, int64_t rows, int d, int64_t units, void* dh) {   // dh may be dy
+                    int64_t rows, int d, int64_t units, void* dh) {   // dh may be dy
     const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
     if (u >= units) return;
     const int per_row = d / 8;
@@ -255,7 +256,7 @@ act_backward_kernel(const void* dy, const uint8_t* __restrict__ codes, const voi
         if (r0 + r < rows) {
             q[r] = *reinterpret_cast<const uint2*>(codes + (r0 + r) * d + c);
             g[r].load(dy, (r0 + r) * d + c);
-            s[r] = load_scale(scale, e8m0, c / kFp8Block * rows + r0 + r);
+            s[r] = load_scale<kE8M0>(scale, c / kFp8Block * rows + r0 + r);
         }
     }
 #pragma unroll
@@ -285,9 +286,12 @@ hipError_t act_forward(const ActForwardArgs& a, hipStream_t stream) {
 template <bool kBF16, int kAct>
 hipError_t act_backward(const ActBackwardArgs& a, hipStream_t stream) {
     const int64_t units = elem_units(a.rows, a.d);
-    act_backward_kernel<kBF16, kAct><<<elem_blocks(units), kThreads, 0, stream>>>(
-        a.dy, static_cast<const uint8_t*>(a.h_codes), a.h_scale, a.e8m0, a.rows, a.d, units, a.dh);
-    return hipGetLastError();
+    auto go = [&](auto kernel) {
+        kernel<<<elem_blocks(units), kThreads, 0, stream>>>(a.dy, static_cast<const uint8_t*>(a.h_codes), a.h_scale, a.rows,
+                                                            a.d, units, a.dh);
+        return hipGetLastError();
+    };
+    return a.e8m0 ? go(act_backward_kernel<kBF16, kAct, true>) : go(act_backward_kernel<kBF16, kAct, false>);
 }
 
 }  // namespace
@@ -314,12 +318,16 @@ hipError_t launch_fp8_quantize_blocks(const Fp8QuantArgs& a, hipStream_t stream)
 hipError_t launch_fp8_dequantize(const Fp8DequantArgs& a, hipStream_t stream) {
     const int64_t units = elem_units(a.rows, a.d);
     auto go = [&](auto kernel) {
-        kernel<<<elem_blocks(units), kThreads, 0, stream>>>(static_cast<const uint8_t*>(a.codes), a.scale, a.e8m0,
-                                                            a.blocks, a.rows, a.d, units, a.y);
+        kernel<<<elem_blocks(units), kThreads, 0, stream>>>(static_cast<const uint8_t*>(a.codes), a.scale, a.blocks, a.rows,
+                                                            a.d, units, a.y);
         return hipGetLastError();
     };
-    if (a.y_bf16) return a.e5m2 ? go(fp8_dequant_kernel<true, true>) : go(fp8_dequant_kernel<false, true>);
-    return a.e5m2 ? go(fp8_dequant_kernel<true, false>) : go(fp8_dequant_kernel<false, false>);
+    auto pick = [&](auto e8m0) {
+        constexpr bool k8 = decltype(e8m0)::value;
+        if (a.y_bf16) return a.e5m2 ? go(fp8_dequant_kernel<true, true, k8>) : go(fp8_dequant_kernel<false, true, k8>);
+        return a.e5m2 ? go(fp8_dequant_kernel<true, false, k8>) : go(fp8_dequant_kernel<false, false, k8>);
+    };
+    return a.e8m0 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 hipError_t launch_act_fp8_forward(const ActForwardArgs& a, hipStream_t stream) {

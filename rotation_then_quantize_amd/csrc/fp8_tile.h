@@ -83,6 +83,11 @@ struct Fp8GemmParams {
 
 }  // namespace fp8
 
+struct Fp8GemmArgs;
+fp8::Fp8GemmParams fp8_gemm_params(const Fp8GemmArgs& g);
+// The product for at most 16 rows (weights [N][R]): from codes, or quantising the rows on the way.
+bool fp8_small_takes(int64_t M);
+hipError_t launch_fp8_small(const fp8::Fp8GemmParams& g, bool e5m2, hipStream_t stream);
 hipError_t launch_fp8_gemm_large(const fp8::Fp8GemmParams& g, bool trans, bool e5m2, hipStream_t stream);
 
 }  // namespace rtq

@@ -34,7 +34,6 @@ struct WgradParams {
     const uint16_t* dy;
     const uint8_t* x;
     const void* x_scale;
-    bool e8m0;
     int64_t T;
     int N, K;
     int tiles_n, tiles_k;
@@ -59,6 +58,7 @@ __device__ __forceinline__ void put4(void* dw, bool bf16, bool accumulate, int64
     }
 }
 
+template <bool kE8M0>
 __global__ void __launch_bounds__(256)
 fp8_wgrad_kernel(WgradParams p) {
     __shared__ __attribute__((aligned(16))) uint8_t s_dy[BT * kRow];
@@ -105,7 +105,7 @@ fp8_wgrad_kernel(WgradParams p) {
         if (t < p.T) {
             if (n0 + col < p.N) d = *reinterpret_cast<const uint4*>(p.dy + t * p.N + n0 + col);
             if (k0 + col < p.K) q = *reinterpret_cast<const uint2*>(p.x + t * p.K + k0 + col);
-            sc = load_scale(p.x_scale, p.e8m0, xs_row + t);
+            sc = load_scale<kE8M0>(p.x_scale, xs_row + t);
         }
         float v[8];
         decode4<false>(q.x, v);
@@ -172,7 +172,6 @@ hipError_t launch_fp8_wgrad(const Fp8WgradArgs& g, hipStream_t stream) {
     p.dy = static_cast<const uint16_t*>(g.dy);
     p.x = static_cast<const uint8_t*>(g.x_codes);
     p.x_scale = g.x_scale;
-    p.e8m0 = g.e8m0;
     p.T = g.T;
     p.N = g.N;
     p.K = g.K;
@@ -185,7 +184,10 @@ hipError_t launch_fp8_wgrad(const Fp8WgradArgs& g, hipStream_t stream) {
     p.dw = p.split > 1 ? g.workspace : g.dw;
     p.dw_bf16 = g.dw_bf16;
     p.accumulate = g.accumulate;
-    fp8_wgrad_kernel<<<static_cast<unsigned>(tiles * p.split), 256, 0, stream>>>(p);
+    if (g.e8m0)
+        fp8_wgrad_kernel<true><<<static_cast<unsigned>(tiles * p.split), 256, 0, stream>>>(p);
+    else
+        fp8_wgrad_kernel<false><<<static_cast<unsigned>(tiles * p.split), 256, 0, stream>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.split == 1) return e;
     wgrad_reduce_kernel<<<static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, stream>>>(

@@ -137,7 +137,7 @@ def test_quantise_blocks(N, K, dtype, st, fmt):
 
 # ------------------------------------------------------------------ products
 
-SIZES = [(1, 1, 16), (1, 100, 256), (2, 33, 144), (13, 4096, 2048), (16, 130, 128), (17, 63, 272), (64, 64, 128),
+SIZES = [(1, 1, 16), (1, 100, 256), (2, 33, 144), (4, 8200, 400), (16, 16400, 2064), (13, 4096, 2048), (16, 130, 128), (17, 63, 272), (64, 64, 128),
          (65, 129, 400), (200, 1000, 1040), (257, 260, 4096), (391, 1001, 1936), (700, 2304, 640)]
 
 
@@ -265,7 +265,8 @@ def test_product_extreme_scales():
 # ------------------------------------------------------------------ the layer and its gradients
 
 @pytest.mark.parametrize("st", [F32, E8M0])
-@pytest.mark.parametrize("T,N,K", [(1, 256, 512), (7, 1000, 4096), (16, 48, 144), (100, 333, 1040), (600, 512, 256)])
+@pytest.mark.parametrize("T,N,K", [(1, 256, 512), (7, 1000, 4096), (16, 48, 144), (100, 333, 1040), (600, 512, 256), (13, 4096, 16384),
+                                   (5, 8200, 144), (3, 16500, 272), (2, 16, 16)])
 def test_linear_equals_its_parts(T, N, K, st):
     step("linear", T, N, K, st)
     x = rows_like(T * K, T, K).cuda()
