@@ -247,7 +247,7 @@ rtq_status rtq_fp8_linear(const void* x, rtq_dtype xt, int64_t T, const void* w_
         g.workspace = left > 0 ? ws : nullptr;
         g.ws_bytes = left;
         hipStream_t s = static_cast<hipStream_t>(stream);
-        if (!keep && rtq::fp8_small_linear_takes(T))
+        if (!keep && rtq::fp8_small_linear_takes(T, K))
             return hip_status(rtq::launch_fp8_small_linear(g, x, xt == RTQ_BF16, s), "fp8 product launch");
         return quantize_then_gemm(q, g, s);
     });

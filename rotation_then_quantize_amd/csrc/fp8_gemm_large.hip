@@ -362,6 +362,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
                 }
         }
     }
+    wait_vmcnt<0>();   // nothing is still writing LDS when the workgroup's next tiles, or another workgroup, use it
 }
 
 template <bool kTrans, bool kE5M2, bool kE8M0>

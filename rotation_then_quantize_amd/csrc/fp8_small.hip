@@ -4,7 +4,9 @@
 // weight rows and the whole reduction, its 8 waves the blocks of 128 in turn; each wave loads its weight
 // fragments straight into registers (a block's 16 rows are 16 runs of 128 bytes, in two 16-byte loads a
 // lane) several blocks ahead, multiplies each with the block of the activations (16 x 16 x 128, the tokens
-// padded to 16) and scales the sums in fp32.  The waves' sums meet in LDS, in a fixed order.
+// padded to 16) and scales the sums in fp32.  The waves' sums meet in LDS, in a fixed order.  More rows per
+// workgroup and few units in flight stream best (16384 x 4096 weights: 16.3 us with 64 rows and one unit of 8
+// KB a wave beside the one in use, 17.9 us with two; 25 us with 32 rows, 29.6 us with 16).
 //
 // kX quantises the activations on the way: a lane holds 32 elements of its token's block, the four lanes
 // of a token share the maximum, and the codes are the matrix instruction's operand as they stand.  Every
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(64 * kWaves)
 fp8_small_kernel(SmallParams sp) {
     const Fp8GemmParams& p = sp.g;
     __shared__ __attribute__((aligned(16))) v4f s_sum[kWaves][kRT][64];
-    constexpr int kAhead = kRT == 4 ? 2 : 4;   // blocks in flight
+    constexpr int kAhead = kRT == 4 ? 1 : 2;   // units in flight beside the one in use
     constexpr int kScaleSize = kE8M0 ? 1 : 4;
     constexpr int kElem = kX == kCodes ? 1 : (kX == kBF16 ? 2 : 4);
     const int tid = threadIdx.x, lane = tid & 63;
@@ -148,15 +150,22 @@ fp8_small_kernel(SmallParams sp) {
             for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(d[r], s, acc[i][r]);
         }
     };
-    // the wave's blocks: wave, wave + 8, ... (past the last one a unit is all zeros)
+    // The wave's blocks: wave + 8 j, j over turns from a place of the workgroup's own (rows a power of two
+    // apart share memory channels: workgroups at the same place of their rows would crowd them).  Past the
+    // last turn a unit is all zeros.  (Workgroup b runs on XCD b % 8, so b / 8 differs within an XCD.)
+    const int turns = (blocks + kWaves - 1) / kWaves, start = static_cast<int>(blockIdx.x / 8) % turns;
+    auto block = [&](int t) {
+        const int j = t + start;
+        return t < turns ? wave + kWaves * (j < turns ? j : j - turns) : blocks;
+    };
     Unit<kRT, kX> u[kAhead];
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) load(u[q], wave + q * kWaves);
-    for (int kb = wave; kb < blocks; kb += kAhead * kWaves) {
+    for (int q = 0; q < kAhead; ++q) load(u[q], block(q));
+    for (int t = 0; t < turns; t += kAhead) {
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
             multiply(u[q]);
-            load(u[q], kb + (q + kAhead) * kWaves);
+            load(u[q], block(t + q + kAhead));
         }
     }
 #pragma unroll
@@ -205,7 +214,10 @@ hipError_t launch(const SmallParams& p, hipStream_t stream) {
 }  // namespace
 
 bool fp8_small_takes(int64_t M) { return M <= kTokens; }
-bool fp8_small_linear_takes(int64_t M) { return M <= kTokens; }
+// Every workgroup quantises all M R elements again: beyond about 2^16 of them that takes longer than a
+// launch of its own (13 x 16384, 4096 rows: 25.8 us so, 23 us with the quantiser's launch; 16 x 4096, 16384
+// rows: 19.0 and 20 us).
+bool fp8_small_linear_takes(int64_t M, int R) { return M <= kTokens && M * R <= 65536; }
 
 hipError_t launch_fp8_small(const fp8::Fp8GemmParams& g, bool e5m2, hipStream_t stream) {
     const SmallParams p{g, nullptr};

@@ -52,6 +52,23 @@ __device__ __forceinline__ v2i read_tr8(uint32_t lds_addr) {
     return __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_v2i>(lds_addr));
 }
 
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+// 4 x 16 16-bit elements transposed: the 16 lanes of a group give the addresses of 4 elements each, four
+// lanes to a row; lane i of the group gets element i of the rows, first row first.
+__device__ __forceinline__ v2i read_tr16(uint32_t lds_addr) {
+    return __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s>(lds_addr)));
+}
+
+// Two 16 x 16 x 32 bf16 products, 16 elements of the reduction a lane; layout as below.
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ v4f mfma_bf16(const v8i& x, const v8i& y, v4f c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, v4i{x[0], x[1], x[2], x[3]}),
+                                                __builtin_bit_cast(v8bf, v4i{y[0], y[1], y[2], y[3]}), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, v4i{x[4], x[5], x[6], x[7]}),
+                                                   __builtin_bit_cast(v8bf, v4i{y[4], y[5], y[6], y[7]}), c, 0, 0, 0);
+}
+
 // 16 x 16 x 128 product of e4m3 (first operand: weights) and e4m3 or e5m2 codes, 32 codes of one row a
 // lane.  Lane l of the result holds column l % 16 (second operand's row), rows 4 (l / 16) .. +4.
 template <bool kE5M2>

@@ -15,6 +15,7 @@
 
 #include "fp8_internal.h"
 #include "fp8_tile.h"
+#include "fp8_wgrad.h"
 #include "rtq_internal.h"
 
 namespace rtq {
@@ -22,41 +23,9 @@ namespace {
 
 using namespace fp8;
 
-typedef short v4s __attribute__((ext_vector_type(4)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) v4s* lds_v4s;
-
 constexpr int kTile = 64;
 constexpr int BT = 32;        // tokens per LDS stage: one 16 x 16 x 32 matrix instruction
 constexpr int kRow = kTile * 2;   // bytes of an LDS row (bf16)
-
-struct WgradParams {
-    const uint16_t* dy;
-    const uint8_t* x;
-    const void* x_scale;
-    int64_t T;
-    int N, K;
-    int tiles_n, tiles_k;
-    int split;
-    void* dw;
-    bool dw_bf16, accumulate;
-};
-
-// Four consecutive values at element `at` of dw.
-__device__ __forceinline__ void put4(void* dw, bool bf16, bool accumulate, int64_t at, v4f v) {
-    if (bf16) {
-        uint2* q = reinterpret_cast<uint2*>(static_cast<uint16_t*>(dw) + at);
-        if (accumulate) {
-            const uint2 o = *q;
-            v += v4f{bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y)};
-        }
-        *q = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    } else {
-        v4f* q = reinterpret_cast<v4f*>(static_cast<float*>(dw) + at);
-        if (accumulate) v += *q;
-        *q = v;
-    }
-}
 
 template <bool kE8M0>
 __global__ void __launch_bounds__(256)
@@ -91,9 +60,7 @@ fp8_wgrad_kernel(WgradParams p) {
         for (int h = 0; h < 2; ++h) {
             const int r = 8 * g + 4 * h + (l15 >> 2);
             const int chunk = (c0 / 8 + ((lane & 3) >> 1)) ^ ((r & 3) << 1);
-            const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                reinterpret_cast<lds_v4s>(base + static_cast<uint32_t>(r * kRow + (chunk << 4) + (lane & 1) * 8)));
-            f[h] = __builtin_bit_cast(v2i, x);
+            f[h] = read_tr16(base + static_cast<uint32_t>(r * kRow + (chunk << 4) + (lane & 1) * 8));
         }
         return __builtin_bit_cast(v8bf, v4i{f[0].x, f[0].y, f[1].x, f[1].y});
     };
@@ -137,7 +104,7 @@ fp8_wgrad_kernel(WgradParams p) {
             // K is a multiple of 16: four columns are all in or all out
             const int n = n0 + wn * 32 + j * 16 + l15, k = k0 + wk * 32 + i * 16 + 4 * g;
             if (n < p.N && k < p.K)
-                put4(dw, p.split == 1 && p.dw_bf16, p.split == 1 && p.accumulate, static_cast<int64_t>(n) * p.K + k,
+                wgrad_put4(dw, p.split == 1 && p.dw_bf16, p.split == 1 && p.accumulate, static_cast<int64_t>(n) * p.K + k,
                      acc[i][j]);
         }
 }
@@ -149,7 +116,7 @@ wgrad_reduce_kernel(const float* __restrict__ part, int split, int64_t n, void* 
     if (i >= n) return;   // n is a multiple of 16
     v4f s = *reinterpret_cast<const v4f*>(part + i);
     for (int k = 1; k < split; ++k) s += *reinterpret_cast<const v4f*>(part + k * n + i);
-    put4(dw, bf16, accumulate, i, s);
+    wgrad_put4(dw, bf16, accumulate, i, s);
 }
 
 int choose_split(int64_t tiles, int64_t stages) {
@@ -163,6 +130,7 @@ int64_t tiles_of(int N, int K) { return static_cast<int64_t>((N + kTile - 1) / k
 }  // namespace
 
 size_t fp8_wgrad_workspace_bytes(int64_t T, int N, int K) {
+    if (wgrad_large_takes(T, N, K)) return 0;
     const int split = choose_split(tiles_of(N, K), (T + BT - 1) / BT);
     return split > 1 ? static_cast<size_t>(split) * N * K * sizeof(float) : 0;
 }
@@ -175,15 +143,17 @@ hipError_t launch_fp8_wgrad(const Fp8WgradArgs& g, hipStream_t stream) {
     p.T = g.T;
     p.N = g.N;
     p.K = g.K;
+    p.dw = g.dw;
+    p.dw_bf16 = g.dw_bf16;
+    p.accumulate = g.accumulate;
+    if (wgrad_large_takes(g.T, g.N, g.K)) return launch_wgrad_large(p, g.e8m0, stream);
     p.tiles_n = (g.N + kTile - 1) / kTile;
     p.tiles_k = (g.K + kTile - 1) / kTile;
     const int64_t tiles = tiles_of(g.N, g.K);
     p.split = choose_split(tiles, (g.T + BT - 1) / BT);
     const int64_t n = static_cast<int64_t>(g.N) * g.K;
     if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(p.split) * n * sizeof(float)) p.split = 1;
-    p.dw = p.split > 1 ? g.workspace : g.dw;
-    p.dw_bf16 = g.dw_bf16;
-    p.accumulate = g.accumulate;
+    if (p.split > 1) p.dw = g.workspace;
     if (g.e8m0)
         fp8_wgrad_kernel<true><<<static_cast<unsigned>(tiles * p.split), 256, 0, stream>>>(p);
     else

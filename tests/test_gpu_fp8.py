@@ -312,6 +312,26 @@ def test_wgrad_exact(T, N, K, st):
         assert same(dw, (ref + start.cpu().double()).float().to(dtype))
 
 
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N,K", [(65, 2568, 2576), (130, 4096, 4112), (333, 2600, 3600), (1000, 2824, 2560), (64, 4096, 4096)])
+def test_large_wgrad_exact(T, N, K, st):
+    """Outputs of many 256 x 256 tiles: whole rounds of them, halves, two to many stages of tokens."""
+    step("large wgrad", T, N, K, st)
+    dy = torch.randint(-4, 5, (T, N), generator=gen(T)).to(BF16).cuda()
+    x, sx = int_codes(K, T, K).cuda(), pow2_scales(9, groups(K), T, -2, 2).to(st).cuda()
+    xv = x.double() * sx.double().t().repeat_interleave(128, 1)[:, :K]
+    ref = dy.double().t().contiguous() @ xv
+    for dtype in (F32, BF16):
+        dw = torch.full((N + 1, K), 7.0, dtype=dtype, device="cuda")
+        rtq.fp8_wgrad(dy, x, sx, dw[:N])
+        assert torch.equal(dw[:N].double(), ref.float().to(dtype).double())
+        assert (dw[N] == 7.0).all()
+        start = torch.randint(-8, 9, (N, K), generator=gen(2)).to(dtype).cuda()
+        dw = start.clone()
+        rtq.fp8_wgrad(dy, x, sx, dw, accumulate=True)
+        assert torch.equal(dw.double(), (ref + start.double()).float().to(dtype).double())
+
+
 def test_wgrad_without_rows_writes_zeros():
     step("wgrad T=0")
     dy, x, sx = torch.empty(0, 16, dtype=BF16, device="cuda"), *empty_rows(0, 32)
