@@ -411,41 +411,36 @@ def _operand(t, name: str, types: dict, shape=None, like=None) -> int:
     return code
 
 
-class _Launch:
-    """The device and stream of one call, and its workspace."""
+def _call(like, stream, fn, *args):
+    """fn(*args, stream) on the device of `like`, on `stream` or that device's current one."""
+    torch = _torch()
+    index = like.get_device()
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device == like.device:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
+    if index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != RTQ_OK:
+        raise RtqError(status, last_error())
 
-    def __init__(self, like, stream):
-        if stream is not None and stream.device != like.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
-        self._like = like
-        self._user_stream = stream
 
-    def __enter__(self):
-        cuda = _torch().cuda
-        index = self._like.get_device()
-        self._guard = None
-        if index != cuda.current_device():
-            self._guard = cuda.device(index)
-            self._guard.__enter__()
-        stream = cuda.current_stream(index) if self._user_stream is None else self._user_stream
-        self.stream = stream.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-    def workspace(self, given, need: int):
-        """(pointer, bytes) of the caller's workspace, or of a temporary one of `need` bytes."""
-        if given is None:
-            if need == 0:
-                return 0, 0
-            given = self._ws = _stream_local_workspace(_torch(), need, self._like.device, self._user_stream)
-        elif given.get_device() != self._like.get_device():
-            raise ValueError(f"workspace is on {given.device}, expected {self._like.device}")
-        elif not given.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        return given.data_ptr(), given.numel() * given.element_size()
+def _workspace(given, like, stream, query, *sizes):
+    """The caller's workspace, or a temporary one of the queried size for the call's stream."""
+    if given is None:
+        with _torch().cuda.device(like.device):
+            need = query(*sizes)
+        return _stream_local_workspace(_torch(), need, like.device, stream)
+    if given.get_device() != like.get_device():
+        raise ValueError(f"workspace is on {given.device}, expected {like.device}")
+    if not given.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return given
 
 
 def fp8_quantize(x, codes, scale, blocks: bool = False, stream=None):
@@ -456,9 +451,8 @@ def fp8_quantize(x, codes, scale, blocks: bool = False, stream=None):
     ct = _operand(codes, "codes", _types()[1], x.shape, x)
     st = _operand(scale, "scale", _types()[3],
                   (fp8_groups(rows), fp8_groups(d)) if blocks else (fp8_groups(d), rows), x)
-    with _Launch(x, stream) as go:
-        _check(load_library().rtq_fp8_quantize(_ptr(x), xt, rows, d, RTQ_FP8_BLOCKS if blocks else RTQ_FP8_ROWS,
-                                               _ptr(codes), ct, _ptr(scale), st, go.stream))
+    _call(x, stream, load_library().rtq_fp8_quantize, _ptr(x), xt, rows, d,
+          RTQ_FP8_BLOCKS if blocks else RTQ_FP8_ROWS, _ptr(codes), ct, _ptr(scale), st)
     return codes, scale
 
 
@@ -469,9 +463,8 @@ def fp8_dequantize(codes, scale, y, blocks: bool = False, stream=None):
     st = _operand(scale, "scale", _types()[3],
                   (fp8_groups(rows), fp8_groups(d)) if blocks else (fp8_groups(d), rows), codes)
     yt = _operand(y, "y", _types()[0], codes.shape, codes)
-    with _Launch(codes, stream) as go:
-        _check(load_library().rtq_fp8_dequantize(_ptr(codes), ct, _ptr(scale), st, rows, d,
-                                                 RTQ_FP8_BLOCKS if blocks else RTQ_FP8_ROWS, _ptr(y), yt, go.stream))
+    _call(codes, stream, load_library().rtq_fp8_dequantize, _ptr(codes), ct, _ptr(scale), st, rows, d,
+          RTQ_FP8_BLOCKS if blocks else RTQ_FP8_ROWS, _ptr(y), yt)
     return y
 
 
@@ -499,10 +492,9 @@ def fp8_qgemm(a_codes, a_scale, w_codes, w_scale, y, workspace=None, stream=None
     _operand(a_scale, "a_scale", _types()[3], (fp8_groups(K), T), a_codes)
     _same_scale(a_scale, "a_scale", w_scale)
     yt = _operand(y, "y", _types()[0], (T, N), a_codes)
-    with _Launch(a_codes, stream) as go:
-        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_qgemm_workspace(T, N, K))
-        _check(load_library().rtq_fp8_qgemm(_ptr(a_codes), at, _ptr(a_scale), T, _ptr(w_codes), _ptr(w_scale), st, N, K,
-                                            _ptr(y), yt, ws, nbytes, go.stream))
+    ws = _workspace(workspace, a_codes, stream, fp8_qgemm_workspace, T, N, K)
+    _call(a_codes, stream, load_library().rtq_fp8_qgemm, _ptr(a_codes), at, _ptr(a_scale), T, _ptr(w_codes),
+          _ptr(w_scale), st, N, K, _ptr(y), yt, _ptr(ws), ws.numel() * ws.element_size())
     return y
 
 
@@ -518,10 +510,9 @@ def fp8_dgrad(g_codes, g_scale, w_codes, w_scale, dx, workspace=None, stream=Non
     _operand(g_scale, "g_scale", _types()[3], (fp8_groups(N), T), g_codes)
     _same_scale(g_scale, "g_scale", w_scale)
     dxt = _operand(dx, "dx", _types()[0], (T, K), g_codes)
-    with _Launch(g_codes, stream) as go:
-        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_dgrad_workspace(T, N, K))
-        _check(load_library().rtq_fp8_dgrad(_ptr(g_codes), gt, _ptr(g_scale), T, _ptr(w_codes), _ptr(w_scale), st, N, K,
-                                            _ptr(dx), dxt, ws, nbytes, go.stream))
+    ws = _workspace(workspace, g_codes, stream, fp8_dgrad_workspace, T, N, K)
+    _call(g_codes, stream, load_library().rtq_fp8_dgrad, _ptr(g_codes), gt, _ptr(g_scale), T, _ptr(w_codes),
+          _ptr(w_scale), st, N, K, _ptr(dx), dxt, _ptr(ws), ws.numel() * ws.element_size())
     return dx
 
 
@@ -542,10 +533,9 @@ def fp8_linear(x, w_codes, w_scale, y, x_codes=None, x_scale=None, workspace=Non
         _operand(x_codes, "x_codes", _types()[2], (T, K), x)
         _operand(x_scale, "x_scale", _types()[3], (fp8_groups(K), T), x)
         _same_scale(x_scale, "x_scale", w_scale)
-    with _Launch(x, stream) as go:
-        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_linear_workspace(T, N, K))
-        _check(load_library().rtq_fp8_linear(_ptr(x), xt, T, _ptr(w_codes), _ptr(w_scale), st, N, K, _ptr(x_codes),
-                                             _ptr(x_scale), _ptr(y), yt, ws, nbytes, go.stream))
+    ws = _workspace(workspace, x, stream, fp8_linear_workspace, T, N, K)
+    _call(x, stream, load_library().rtq_fp8_linear, _ptr(x), xt, T, _ptr(w_codes), _ptr(w_scale), st, N, K,
+          _ptr(x_codes), _ptr(x_scale), _ptr(y), yt, _ptr(ws), ws.numel() * ws.element_size())
     return y
 
 
@@ -564,10 +554,9 @@ def fp8_linear_dgrad(dy, w_codes, w_scale, dx, grad_dtype=None, workspace=None, 
     grad_dtype = torch.float8_e5m2 if grad_dtype is None else grad_dtype
     if grad_dtype not in _types()[1]:
         raise TypeError(f"grad_dtype: unsupported dtype {grad_dtype}")
-    with _Launch(dy, stream) as go:
-        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_linear_dgrad_workspace(T, N, K))
-        _check(load_library().rtq_fp8_linear_dgrad(_ptr(dy), dyt, _types()[1][grad_dtype], T, _ptr(w_codes),
-                                                   _ptr(w_scale), st, N, K, _ptr(dx), dxt, ws, nbytes, go.stream))
+    ws = _workspace(workspace, dy, stream, fp8_linear_dgrad_workspace, T, N, K)
+    _call(dy, stream, load_library().rtq_fp8_linear_dgrad, _ptr(dy), dyt, _types()[1][grad_dtype], T, _ptr(w_codes),
+          _ptr(w_scale), st, N, K, _ptr(dx), dxt, _ptr(ws), ws.numel() * ws.element_size())
     return dx
 
 
@@ -585,10 +574,9 @@ def fp8_wgrad(dy, x_codes, x_scale, dw, accumulate: bool = False, workspace=None
     K = x_codes.shape[1]
     st = _operand(x_scale, "x_scale", _types()[3], (fp8_groups(K), T), dy)
     dwt = _operand(dw, "dw", _types()[0], (N, K), dy)
-    with _Launch(dy, stream) as go:
-        ws, nbytes = go.workspace(workspace, 0 if workspace is not None else fp8_wgrad_workspace(T, N, K))
-        _check(load_library().rtq_fp8_wgrad(_ptr(dy), T, _ptr(x_codes), _ptr(x_scale), st, N, K, _ptr(dw), dwt,
-                                            1 if accumulate else 0, ws, nbytes, go.stream))
+    ws = _workspace(workspace, dy, stream, fp8_wgrad_workspace, T, N, K)
+    _call(dy, stream, load_library().rtq_fp8_wgrad, _ptr(dy), T, _ptr(x_codes), _ptr(x_scale), st, N, K, _ptr(dw),
+          dwt, 1 if accumulate else 0, _ptr(ws), ws.numel() * ws.element_size())
     return dw
 
 
@@ -607,9 +595,8 @@ def act_fp8_forward(h, act: int, h_codes, h_scale, y=None, y_codes=None, y_scale
     else:
         _operand(y_codes, "y_codes", e4m3, h.shape, h)
         _operand(y_scale, "y_scale", {h_scale.dtype: st}, (fp8_groups(d), rows), h)
-    with _Launch(h, stream) as go:
-        _check(load_library().rtq_act_fp8_forward(_ptr(h), ht, rows, d, act, _ptr(h_codes), _ptr(h_scale), _ptr(y),
-                                                  _ptr(y_codes), _ptr(y_scale), st, go.stream))
+    _call(h, stream, load_library().rtq_act_fp8_forward, _ptr(h), ht, rows, d, act, _ptr(h_codes), _ptr(h_scale),
+          _ptr(y), _ptr(y_codes), _ptr(y_scale), st)
     return y if y is not None else (y_codes, y_scale)
 
 
@@ -620,7 +607,6 @@ def act_fp8_backward(dy, h_codes, h_scale, act: int, dh, stream=None):
     _operand(h_codes, "h_codes", _types()[2], dy.shape, dy)
     st = _operand(h_scale, "h_scale", _types()[3], (fp8_groups(d), rows), dy)
     _operand(dh, "dh", {dy.dtype: dyt}, dy.shape, dy)
-    with _Launch(dy, stream) as go:
-        _check(load_library().rtq_act_fp8_backward(_ptr(dy), dyt, _ptr(h_codes), _ptr(h_scale), st, rows, d, act,
-                                                   _ptr(dh), go.stream))
+    _call(dy, stream, load_library().rtq_act_fp8_backward, _ptr(dy), dyt, _ptr(h_codes), _ptr(h_scale), st, rows, d,
+          act, _ptr(dh))
     return dh

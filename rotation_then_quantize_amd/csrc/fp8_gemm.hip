@@ -13,6 +13,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cstdlib>
+#include <type_traits>
 
 #include "fp8_internal.h"
 #include "fp8_tile.h"
@@ -23,28 +25,16 @@ namespace {
 
 using namespace fp8;
 
-// Four consecutive outputs of row m from column n.
-__device__ __forceinline__ void store4(void* y, bool bf16, int64_t M, int64_t N, int64_t m, int64_t n, const v4f& v) {
-    if (m >= M || n >= N) return;
-    const int64_t at = m * N + n;
-    if (n + 4 <= N && N % 4 == 0) {
-        if (bf16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        else
-            *reinterpret_cast<v4f*>(static_cast<float*>(y) + at) = v;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i < N) {
-            if (bf16)
-                static_cast<uint16_t*>(y)[at + i] = static_cast<uint16_t>(pack_bf16x2(v[i], 0.0f));
-            else
-                static_cast<float*>(y)[at + i] = v[i];
-        }
-    }
-}
+constexpr int kTable = 32;   // blocks whose scales are in LDS
 
+template <int BM, int BN, int kSlots>
+constexpr int tile_lds() { return kSlots * (BM + BN) * BK + kTable * BM * static_cast<int>(sizeof(float)); }
+
+// A tile of BM x BN outputs, a ring of kSlots LDS stages of one block of the reduction each, loaded kSlots
+// stages ahead (tiles this small are bound by the loads' latency, not by their products); a block's fragments
+// are read while the block before it is multiplied.  The rows' scales
+// times the weight's, of kTable blocks at a time, are put into LDS beforehand: loads of scales among the
+// stages' would make every wait for one a wait for the stages behind it.
 template <int BM, int BN, int kWavesM, int kWavesN, int kSlots, bool kTrans, bool kE5M2, bool kE8M0>
 __global__ void __launch_bounds__(64 * kWavesM * kWavesN)
 fp8_gemm_kernel(Fp8GemmParams p) {
@@ -54,16 +44,21 @@ fp8_gemm_kernel(Fp8GemmParams p) {
     constexpr int kABytes = BM * BK, kWBytes = BN * BK, kStage = kABytes + kWBytes;
     constexpr int kALoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves;   // 1 KB loads per wave
     constexpr int kChunks = BN / 16;                                      // kTrans: 16-byte chunks per LDS row
-    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "whole loads per wave");
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && BN <= kFp8Block, "whole loads per wave, one weight scale");
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+    float* table = reinterpret_cast<float*>(lds + kSlots * kStage);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / kWavesN, wn = wave % kWavesN;
     const int g = lane >> 4, l15 = lane & 15;
 
-    const int tile = static_cast<int>(blockIdx.x) / p.split, part = static_cast<int>(blockIdx.x) % p.split;
+    // 8 contiguous ranges of tiles and their parts, one per XCD (workgroup b runs on XCD b % 8)
+    const int total = p.tiles_m * p.tiles_n * p.split, per = (total + 7) / 8;
+    const int local = static_cast<int>(blockIdx.x) / 8, lin = static_cast<int>(blockIdx.x) % 8 * per + local;
+    if (local >= per || lin >= total) return;
+    const int tile = lin / p.split, part = lin % p.split;
     const int64_t m0 = static_cast<int64_t>(tile % p.tiles_m) * BM, n0 = static_cast<int64_t>(tile / p.tiles_m) * BN;
     const int blocks = (p.R + BK - 1) / BK;
     const int kb0 = static_cast<int>(static_cast<int64_t>(blocks) * part / p.split);
@@ -76,9 +71,7 @@ fp8_gemm_kernel(Fp8GemmParams p) {
 
     // LDS rows of 128 bytes, chunk c (16 bytes) of row r at chunk c ^ ((r >> 1) & 7); lane group g holds
     // chunks g and g + 4 of its row, which makes the 16-byte reads free of bank conflicts (see the large
-    // kernel).  Transposed weights: rows of BN bytes (one n), chunk c of row r at c ^ row_swizzle(r): 8 rows
-    // of one chunk touch all banks once.
-    auto row_swizzle = [](int row) { return (row * BN / 256) & (kChunks - 1); };
+    // kernel).  Transposed weights: rows of BN bytes.
     auto issue = [&](int kb) {
         const uint32_t slot = lds_base + static_cast<uint32_t>(((kb - kb0) % kSlots) * kStage);
 #pragma unroll
@@ -98,7 +91,7 @@ fp8_gemm_kernel(Fp8GemmParams p) {
             uint32_t off;
             if constexpr (kTrans) {
                 const int row = (64 / kChunks) * (q * kWaves + wave) + lane / kChunks;
-                off = static_cast<uint32_t>(row * static_cast<int>(p.N) + (((lane % kChunks) ^ row_swizzle(row)) << 4));
+                off = static_cast<uint32_t>(row * static_cast<int>(p.N) + (((lane % kChunks) ^ tr_swizzle<BN>(row)) << 4));
             } else {
                 const int row = 8 * (q * kWaves + wave) + (lane >> 3);
                 const int col = kb * BK + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
@@ -107,19 +100,27 @@ fp8_gemm_kernel(Fp8GemmParams p) {
             load_to_lds(rsw, off, slot + static_cast<uint32_t>(kABytes + (q * kWaves + wave) * 1024));
         }
     };
+    const int64_t wblock = n0 / kFp8Block;
+    auto fill = [&](int c0) {   // the table of blocks c0 ..; row r of wave-row wm at [block][wm][r % 16][r / 16]
+#pragma unroll 4
+        for (int e = tid; e < kTable * BM; e += 64 * kWaves) {
+            const int kb = min(c0 + e / BM, blocks - 1), r = e % BM;
+            const int64_t m = min<int64_t>(m0 + r, p.M - 1);
+            table[e / BM * BM + (r / WM * 16 + (r & 15)) * TM + (r % WM >> 4)] =
+                load_scale<kE8M0>(p.a_scale, kb * p.M + m) * load_scale<kE8M0>(p.w_scale, wblock * p.w_out_stride + kb * p.w_red_stride);
+        }
+    };
     const uint32_t f0 = static_cast<uint32_t>(l15 * BK + ((g ^ (l15 >> 1)) << 4));
     const uint32_t f1 = static_cast<uint32_t>(l15 * BK + (((g + 4) ^ (l15 >> 1)) << 4));
     auto read_frag = [&](const uint8_t* base) {
         const v4i x = *reinterpret_cast<const v4i*>(base + f0), y = *reinterpret_cast<const v4i*>(base + f1);
         return v8i{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
     };
+    const int tr_row = 16 * g + (l15 >> 1);
+    const uint32_t tr0 = static_cast<uint32_t>(tr_row * BN + (lane & 1) * 8);
     auto read_frag_tr = [&](uint32_t base, int chunk) {
-        v2i r[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int row = 64 * (q >> 1) + 16 * g + 8 * (q & 1) + (l15 >> 1);
-            r[q] = read_tr8(base + static_cast<uint32_t>(row * BN + ((chunk ^ row_swizzle(row)) << 4) + (lane & 1) * 8));
-        }
+        const uint32_t at = base + tr0 + static_cast<uint32_t>((chunk ^ tr_swizzle<BN>(tr_row)) << 4);
+        const v2i r[4] = {read_tr8(at), read_tr8(at + 8 * BN), read_tr8(at + 64 * BN), read_tr8(at + 72 * BN)};
         return v8i{r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
     };
 
@@ -129,47 +130,69 @@ fp8_gemm_kernel(Fp8GemmParams p) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    int64_t mi[TM];   // the lane's row of each row tile, kept inside the array
-#pragma unroll
-    for (int i = 0; i < TM; ++i) mi[i] = min<int64_t>(m0 + wm * WM + i * 16 + l15, p.M - 1);
-    const int64_t wblock = min<int64_t>((n0 + wn * WN) / kFp8Block, (p.N - 1) / kFp8Block);
-
-#pragma unroll
-    for (int s = 0; s < kSlots - 1; ++s)
-        if (kb0 + s < kb1) issue(kb0 + s);
     constexpr int kLoads = kALoads + kWLoads;
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const float sw = load_scale<kE8M0>(p.w_scale, wblock * p.w_out_stride + kb * p.w_red_stride);
-        float s[TM];
+    v8i fa[2][TM], fw[2][TN];
+    float sc[2][TM];
+    // Block kb from the fragments and scales of set P, while those of block kb + 1 are read into the other.
+    auto read = [&](auto set, int kb) {
+        constexpr int P = decltype(set)::value;
+        const int slot = ((kb - kb0) % kSlots) * kStage;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) s[i] = load_scale<kE8M0>(p.a_scale, kb * p.M + mi[i]) * sw;
-        // block kb has landed (later blocks may be in flight), in every wave; block kb - 1 is read
-        if (kSlots > 2 && kb + kSlots - 2 < kb1)
+        for (int j = 0; j < TN; ++j) {
+            if constexpr (kTrans)
+                fw[P][j] = read_frag_tr(lds_base + static_cast<uint32_t>(slot + kABytes), (wn * WN + j * 16) / 16);
+            else
+                fw[P][j] = read_frag(lds + slot + kABytes + (wn * WN + j * 16) * BK);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            fa[P][i] = read_frag(lds + slot + (wm * WM + i * 16) * BK);
+            sc[P][i] = table[(kb - kb0) % kTable * BM + (wm * 16 + l15) * TM + i];
+        }
+    };
+    auto block = [&](auto set, int kb) {
+        constexpr int P = decltype(set)::value;
+        lds_done();   // this wave's fragments of block kb are in registers
+        // block kb + 1 has landed (later ones may be in flight), in every wave; block kb's slot is free
+        if (kb + kSlots - 1 < kb1)
             wait_vmcnt<(kSlots - 2) * kLoads>();
         else
             wait_vmcnt<0>();
         barrier();
-        if (kb + kSlots - 1 < kb1) issue(kb + kSlots - 1);
-        const int slot = ((kb - kb0) % kSlots) * kStage;
-        v8i fa[TM], fw[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            if constexpr (kTrans)
-                fw[j] = read_frag_tr(lds_base + static_cast<uint32_t>(slot + kABytes), (wn * WN + j * 16) / 16);
-            else
-                fw[j] = read_frag(lds + slot + kABytes + (wn * WN + j * 16) * BK);
+        if (kb + kSlots < kb1) issue(kb + kSlots);
+        if (kb + 1 < kb1) {
+            if ((kb + 1 - kb0) % kTable == 0) {   // (every wave has read the last scales of the old table)
+                fill(kb + 1);
+                lds_done();
+                barrier();
+            }
+            read(std::integral_constant<int, 1 - P>{}, kb + 1);
         }
-#pragma unroll
-        for (int i = 0; i < TM; ++i) fa[i] = read_frag(lds + slot + (wm * WM + i * 16) * BK);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                const v4f d = mfma<kE5M2>(fw[j], fa[i], v4f{0.f, 0.f, 0.f, 0.f});
+                const v4f d = mfma<kE5M2>(fw[P][j], fa[P][i], v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s[i], acc[i][j][r]);
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], sc[P][i], acc[i][j][r]);
             }
-        lds_done();   // the fragments are in registers before the barrier that lets the slot be refilled
+    };
+    constexpr auto P0 = std::integral_constant<int, 0>{};
+    constexpr auto P1 = std::integral_constant<int, 1>{};
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+        if (kb0 + s < kb1) issue(kb0 + s);
+    fill(kb0);
+    if (kb0 + kSlots - 1 < kb1)
+        wait_vmcnt<(kSlots - 1) * kLoads>();
+    else
+        wait_vmcnt<0>();
+    lds_done();
+    barrier();
+    read(P0, kb0);
+    for (int kb = kb0; kb < kb1; kb += 2) {
+        block(P0, kb);
+        if (kb + 1 < kb1) block(P1, kb + 1);
     }
     void* y = p.y;
     if (p.split > 1) y = static_cast<float*>(p.y) + static_cast<int64_t>(part) * p.M * p.N;
@@ -205,47 +228,59 @@ fp8_reduce_kernel(const float* __restrict__ part, int split, int64_t n, void* __
     }
 }
 
-constexpr int kTile = 64;   // the small tile's rows and columns
-constexpr int kMaxSplit = 16;
+// How a product runs.
+enum Form : int { kSmall, kTile64, kTile128, kLarge };
+struct Plan {
+    Form form;
+    int split;   // ranges of the reduction per tile, summed by a second kernel
+};
 
-// Ranges of the reduction per tile: enough workgroups for two per CU, each at least four blocks long.
-int choose_split(int64_t tiles, int blocks) {
-    const int64_t want = 2 * 256;
-    if (tiles >= want) return 1;
-    const int64_t s = std::min<int64_t>(want / tiles, blocks / 4);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplit)));
+Plan plan(int64_t M, int64_t N, int R, bool trans) {
+    if (fp8_small_takes(M, N, R, trans)) return {kSmall, 1};
+    auto tiles = [&](int64_t t) { return (M + t - 1) / t * ((N + t - 1) / t); };
+    const int blocks = static_cast<int>(fp8_groups(R));
+    const char* f = getenv("FORM");
+    const int form = f ? atoi(f) : (tiles(256) >= 96 && blocks > 1 ? kLarge : kTile64);
+    if (form == kLarge) return {kLarge, 1};
+    const int64_t n = tiles(form == kTile128 ? 128 : 64), want = form == kTile128 ? 256 : 512;
+    int split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want / n, blocks / 4, 16})));
+    if (getenv("SPLIT")) split = atoi(getenv("SPLIT"));
+    return {static_cast<Form>(form), split};
 }
 
-// (the large kernel's loads run two stages ahead, so it takes reductions of at least two blocks)
-bool use_large(int64_t M, int64_t N, int R) { return R > BK && ((M + 255) / 256) * ((N + 255) / 256) >= 96; }
-
-template <bool kTrans, bool kE5M2>
-hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
-    constexpr int kSlots = 4;
-    constexpr size_t lds = static_cast<size_t>(kSlots) * 2 * kTile * BK;
-    auto kernel = g.e8m0 ? fp8_gemm_kernel<kTile, kTile, 2, 2, kSlots, kTrans, kE5M2, true>
-                         : fp8_gemm_kernel<kTile, kTile, 2, 2, kSlots, kTrans, kE5M2, false>;
+template <int BT, int kWavesM, int kWavesN, int kSlots, bool kTrans, bool kE5M2>
+hipError_t launch_tiles(Fp8GemmParams p, const Fp8GemmArgs& g, int split, hipStream_t stream) {
+    auto kernel = g.e8m0 ? fp8_gemm_kernel<BT, BT, kWavesM, kWavesN, kSlots, kTrans, kE5M2, true>
+                         : fp8_gemm_kernel<BT, BT, kWavesM, kWavesN, kSlots, kTrans, kE5M2, false>;
+    constexpr int threads = 64 * kWavesM * kWavesN, lds = tile_lds<BT, BT, kSlots>();
     int per_cu = 0;
-    hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), 256, lds, &per_cu);
+    hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), threads, lds, &per_cu);
     if (e != hipSuccess) return e;
-    Fp8GemmParams p = fp8_gemm_params(g);
-    if (!kTrans && fp8_small_takes(g.M)) return launch_fp8_small(p, kE5M2, stream);
-    if (use_large(g.M, g.N, g.R)) {
-        return launch_fp8_gemm_large(p, kTrans, kE5M2, stream);
-    }
-    p.tiles_m = static_cast<int>((g.M + kTile - 1) / kTile);
-    p.tiles_n = static_cast<int>((g.N + kTile - 1) / kTile);
-    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-    p.split = choose_split(tiles, static_cast<int>(fp8_groups(g.R)));
-    if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(p.split) * g.M * g.N * sizeof(float)) p.split = 1;
-    p.y = p.split > 1 ? g.workspace : g.y;
-    kernel<<<static_cast<unsigned>(tiles * p.split), 256, lds, stream>>>(p);
+    p.tiles_m = static_cast<int>((g.M + BT - 1) / BT);
+    p.tiles_n = static_cast<int>((g.N + BT - 1) / BT);
+    p.split = split;
+    if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(split) * g.M * g.N * sizeof(float)) p.split = 1;
+    if (p.split > 1) p.y = g.workspace;
+    const int64_t total = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.split;
+    kernel<<<static_cast<unsigned>((total + 7) / 8 * 8), threads, lds, stream>>>(p);
     e = hipGetLastError();
     if (e != hipSuccess || p.split == 1) return e;
     const int64_t n = g.M * g.N;
     fp8_reduce_kernel<<<static_cast<unsigned>((n + 1023) / 1024), 256, 0, stream>>>(static_cast<const float*>(g.workspace),
                                                                                     p.split, n, g.y, g.y_bf16);
     return hipGetLastError();
+}
+
+template <bool kTrans, bool kE5M2>
+hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
+    const Fp8GemmParams p = fp8_gemm_params(g);
+    const Plan how = plan(g.M, g.N, g.R, kTrans);
+    switch (how.form) {
+        case kSmall: return launch_fp8_small(p, kTrans, kE5M2, stream);
+        case kLarge: return launch_fp8_gemm_large(p, kTrans, kE5M2, stream);
+        case kTile128: return launch_tiles<128, 2, 4, 4, kTrans, kE5M2>(p, g, how.split, stream);
+        default: return launch_tiles<64, 2, 2, 4, kTrans, kE5M2>(p, g, how.split, stream);
+    }
 }
 
 }  // namespace
@@ -269,9 +304,8 @@ fp8::Fp8GemmParams fp8_gemm_params(const Fp8GemmArgs& g) {
 }
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int R, bool trans) {
-    if ((!trans && fp8_small_takes(M)) || use_large(M, N, R)) return 0;
-    const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-    const int split = choose_split(tiles, static_cast<int>(fp8_groups(R)));
+    if (M == 0) return 0;
+    const int split = plan(M, N, R, trans).split;
     return split > 1 ? static_cast<size_t>(split) * M * N * sizeof(float) : 0;
 }
 

@@ -69,6 +69,19 @@ __device__ __forceinline__ v4f mfma_bf16(const v8i& x, const v8i& y, v4f c) {
                                                    __builtin_bit_cast(v8bf, v4i{y[4], y[5], y[6], y[7]}), c, 0, 0, 0);
 }
 
+// Where transposed weights sit in LDS rows of kBytes (one n of the block): chunk c (16 bytes) of row r at
+// c ^ tr_swizzle(r), so that a transposing read's 8 rows of one chunk, and those of the next lane group 16
+// rows further on, touch all banks once.
+template <int kBytes>
+__device__ __forceinline__ int tr_swizzle(int row) {
+    static_assert(kBytes == 16 || kBytes == 32 || kBytes == 64 || kBytes == 128 || kBytes == 256, "row bytes");
+    if constexpr (kBytes == 256) return (row & 7) | ((row >> 4) & 1) << 3;
+    if constexpr (kBytes == 128) return ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
+    if constexpr (kBytes == 64) return ((row >> 2) & 1) | ((row >> 4) & 1) << 1;
+    if constexpr (kBytes == 32) return (row >> 4) & 1;
+    return 0;
+}
+
 // 16 x 16 x 128 product of e4m3 (first operand: weights) and e4m3 or e5m2 codes, 32 codes of one row a
 // lane.  Lane l of the result holds column l % 16 (second operand's row), rows 4 (l / 16) .. +4.
 template <bool kE5M2>
@@ -81,6 +94,28 @@ __device__ __forceinline__ v4f mfma(const v8i& w, const v8i& a, v4f c) {
 template <bool kE5M2, int kByte>
 __device__ __forceinline__ v4f mfma_scaled(const v8i& w, const v8i& a, v4f c, int scales) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, kE5M2 ? 1 : 0, kByte + 1, scales, kByte, scales);
+}
+
+// Four consecutive outputs of row m from column n.
+__device__ __forceinline__ void store4(void* y, bool bf16, int64_t M, int64_t N, int64_t m, int64_t n, const v4f& v) {
+    if (m >= M || n >= N) return;
+    const int64_t at = m * N + n;
+    if (n + 4 <= N && N % 4 == 0) {
+        if (bf16)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        else
+            *reinterpret_cast<v4f*>(static_cast<float*>(y) + at) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i < N) {
+            if (bf16)
+                static_cast<uint16_t*>(y)[at + i] = static_cast<uint16_t>(pack_bf16x2(v[i], 0.0f));
+            else
+                static_cast<float*>(y)[at + i] = v[i];
+        }
+    }
 }
 
 // Kernel arguments of a product: out[m][n] = sum over the reduction r of a[m][r] w[n][r] (or w[r][n]).
@@ -102,9 +137,10 @@ struct Fp8GemmParams {
 
 struct Fp8GemmArgs;
 fp8::Fp8GemmParams fp8_gemm_params(const Fp8GemmArgs& g);
-// The product for at most 16 rows (weights [N][R]): from codes, or quantising the rows on the way.
-bool fp8_small_takes(int64_t M);
-hipError_t launch_fp8_small(const fp8::Fp8GemmParams& g, bool e5m2, hipStream_t stream);
+// The product for a few rows or a small output (fp8_small.hip), from codes.
+bool fp8_small_takes(int64_t M, int64_t N, int R, bool trans);
+hipError_t launch_fp8_small(const fp8::Fp8GemmParams& g, bool trans, bool e5m2, hipStream_t stream);
+// Tiles of 256 x 256; reductions of at least two blocks.
 hipError_t launch_fp8_gemm_large(const fp8::Fp8GemmParams& g, bool trans, bool e5m2, hipStream_t stream);
 
 }  // namespace rtq
