@@ -13,7 +13,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <cstdlib>
 #include <type_traits>
 
 #include "fp8_internal.h"
@@ -235,17 +234,25 @@ struct Plan {
     int split;   // ranges of the reduction per tile, summed by a second kernel
 };
 
+// Measured at a reduction of 4096 (M x 4096 outputs, us):
+//              M = 64      128      256      512      1000     1500     2048
+//   64 x 64    16.6        16.9     17.4     20.8     38.0     54.3      -
+//   128 x 128  24.1        25.5     25.9     26.6     28.8     50.6      -
+//   256 x 256   -           -        -        -       35       35        38
+// A tile costs its chain of stages as long as each CU has one (128: one workgroup per CU, 64: two), so the
+// largest tile whose workgroups fit at once is taken.  Splitting the reduction shortens the chain of the 64
+// x 64 tiles where CUs are idle (M = 64: 11.4 us in four, M = 128: 13.6 in two); below 12 blocks a part the
+// second kernel costs what it saves.
 Plan plan(int64_t M, int64_t N, int R, bool trans) {
     if (fp8_small_takes(M, N, R, trans)) return {kSmall, 1};
     auto tiles = [&](int64_t t) { return (M + t - 1) / t * ((N + t - 1) / t); };
     const int blocks = static_cast<int>(fp8_groups(R));
-    const char* f = getenv("FORM");
-    const int form = f ? atoi(f) : (tiles(256) >= 96 && blocks > 1 ? kLarge : kTile64);
-    if (form == kLarge) return {kLarge, 1};
-    const int64_t n = tiles(form == kTile128 ? 128 : 64), want = form == kTile128 ? 256 : 512;
-    int split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want / n, blocks / 4, 16})));
-    if (getenv("SPLIT")) split = atoi(getenv("SPLIT"));
-    return {static_cast<Form>(form), split};
+    const int64_t cus = device_cu_count();
+    if (tiles(64) > 2 * cus) {
+        if (tiles(128) <= cus) return {kTile128, 1};
+        if (blocks > 1) return {kLarge, 1};   // (its loads run two stages ahead)
+    }
+    return {kTile64, static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({cus / tiles(64), blocks / 12, 16})))};
 }
 
 template <int BT, int kWavesM, int kWavesN, int kSlots, bool kTrans, bool kE5M2>
