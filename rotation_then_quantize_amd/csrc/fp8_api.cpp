@@ -247,7 +247,7 @@ rtq_status rtq_fp8_linear(const void* x, rtq_dtype xt, int64_t T, const void* w_
         g.workspace = left > 0 ? ws : nullptr;
         g.ws_bytes = left;
         hipStream_t s = static_cast<hipStream_t>(stream);
-        if (rtq::fp8_small_linear_takes(T, N, K, false, xt == RTQ_BF16 ? 2 : 4))
+        if (rtq::fp8_small_linear_takes(T, N, K, false))
             return hip_status(rtq::launch_fp8_small_linear(g, x, xt == RTQ_BF16, keep ? x_codes : nullptr,
                                                            keep ? x_scale : nullptr, s), "fp8 product launch");
         return quantize_then_gemm(q, g, s);
@@ -282,7 +282,7 @@ rtq_status rtq_fp8_linear_dgrad(const void* dy, rtq_dtype dyt, rtq_dtype gt, int
         g.workspace = ws_bytes > need ? ws + need : nullptr;
         g.ws_bytes = ws_bytes - need;
         hipStream_t s = static_cast<hipStream_t>(stream);
-        if (rtq::fp8_small_linear_takes(T, K, N, true, dyt == RTQ_BF16 ? 2 : 4))
+        if (rtq::fp8_small_linear_takes(T, K, N, true))
             return hip_status(rtq::launch_fp8_small_linear(g, dy, dyt == RTQ_BF16, nullptr, nullptr, s), "fp8 dgrad launch");
         return quantize_then_gemm(q, g, s);
     });

@@ -88,8 +88,8 @@ struct Fp8GemmArgs {
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream);
 // The layer for a few rows or a small output in one launch: x [M][R] (fp32 or bf16) is quantised on the way
 // to row groups of g's format (g.a and g.a_scale are not used), which go to keep and keep_scale if those
-// are given.  Takes what fp8_small_linear_takes says (elem: bytes of an element of x).
-bool fp8_small_linear_takes(int64_t M, int64_t N, int R, bool trans, int elem);
+// are given.  Takes what fp8_small_linear_takes says.
+bool fp8_small_linear_takes(int64_t M, int64_t N, int R, bool trans);
 hipError_t launch_fp8_small_linear(const Fp8GemmArgs& g, const void* x, bool x_bf16, void* keep, void* keep_scale,
                                    hipStream_t stream);
 // Workspace bytes launch_fp8_gemm can use for these sizes (0: none).

@@ -310,23 +310,25 @@ hipError_t launch_x(const SmallParams& p, bool x_bf16, hipStream_t stream) {
     return x_bf16 ? launch<kBF16, kE5M2, kTrans>(p, stream) : launch<kF32, kE5M2, kTrans>(p, stream);
 }
 
-// Bytes that the workgroups of an output of many rows read, each its own rows and columns.
-int64_t small_bytes(int64_t M, int64_t N, int64_t R, int elem) {
-    return (M + 31) / 32 * ((N + 63) / 64) * R * (32 * elem + 64);
+// More than 16 rows: an output whose workgroups all run at once, and at most two turns of the waves through
+// the reduction.  (Layer, 391 x 1936, 1001 columns: 11.6 us, 14.0 through the quantiser and shared tiles; 200
+// x 2048, 1024: 10.9 and 12.6; but 300 x 1024, 2048, 320 workgroups: 18.7 and 10.3; 40 x 4096, 2048: 16.3 and
+// 14.3.)
+bool fits(int64_t M, int64_t N, int R) {
+    return R <= 2048 && (M + 31) / 32 * ((N + 63) / 64) <= device_cu_count();
 }
-constexpr int64_t kMostBytes = int64_t{16} << 20;
 
 }  // namespace
 
 bool fp8_small_takes(int64_t M, int64_t N, int R, bool trans) {
-    return M <= 16 ? !trans || N * R <= kMostBytes : small_bytes(M, N, R, 1) <= kMostBytes;
+    if (M <= 16) return !trans || N * R <= int64_t{16} << 20;
+    return fits(M, N, R);
 }
-// Every workgroup quantises its rows again: beyond about 2^16 elements of one that takes longer than a launch
-// of its own (13 x 16384, 4096 columns: 25.8 us so, 23 us with the quantiser's launch; 16 x 4096, 16384
-// columns: 19.0 and 20 us).
-bool fp8_small_linear_takes(int64_t M, int64_t N, int R, bool trans, int elem) {
-    if (M <= 16) return M * R <= 65536 && fp8_small_takes(M, N, R, trans);
-    return R <= 4096 && small_bytes(M, N, R, elem) <= kMostBytes;
+// Every workgroup quantises its rows again: of few tokens, beyond about 2^16 elements that takes longer than
+// a launch of its own (13 x 16384, 4096 columns: 25.8 us so, 23 us with the quantiser's launch; 16 x 4096,
+// 16384 columns: 19.0 and 20 us).
+bool fp8_small_linear_takes(int64_t M, int64_t N, int R, bool trans) {
+    return fp8_small_takes(M, N, R, trans) && (M > 16 || M * R <= 65536);
 }
 
 hipError_t launch_fp8_small(const fp8::Fp8GemmParams& g, bool trans, bool e5m2, hipStream_t stream) {

@@ -4,10 +4,13 @@
 //   dw[n][k] = sum_t dy[t][n] * x^[t][k],   x^[t][k] = sx[k / 128][t] qx[t][k]
 //
 // The scale varies along the reduction (t), so it cannot be taken out of the sum: the codes are decoded
-// to bf16 on their way into LDS (exact for power-of-two scales, as rtq_fp8_quantize writes them: a code
-// has at most 4 significant bits; one rounding to bf16 for general scales) and multiplied with dy as it
-// is, summed in fp32.  Both operands have the reduction as their row index; the transposing LDS read
-// gives each lane consecutive t of one column.
+// to bf16 in LDS (exact for power-of-two scales, as rtq_fp8_quantize writes them: a code has at most 4
+// significant bits; one rounding to bf16 for general scales) and multiplied with dy as it is, summed in
+// fp32.  Both operands have the reduction as their row index; the transposing LDS read gives each lane
+// consecutive t of one column.
+//
+// This file: 128 x 128 tiles, one per workgroup, for outputs of few tiles, which are bound by the latency of
+// each workgroup's chain of stages.  Outputs of many tiles: fp8_wgrad_large.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -23,89 +26,145 @@ namespace {
 
 using namespace fp8;
 
-constexpr int kTile = 64;
-constexpr int BT = 32;        // tokens per LDS stage: one 16 x 16 x 32 matrix instruction
-constexpr int kRow = kTile * 2;   // bytes of an LDS row (bf16)
+constexpr int kTile = 128;        // rows n and columns k: one scale a token
+constexpr int BT = 64;            // tokens per LDS stage
+constexpr int kWavesN = 2, kWavesK = 4, kWaves = kWavesN * kWavesK, kThreads = 64 * kWaves;
+constexpr int WN = kTile / kWavesN, WK = kTile / kWavesK, TN = WN / 16, TK = WK / 16;
+constexpr int kSlots = 4;         // stages of dy and of codes in LDS
+constexpr int kRow = kTile * 2;   // LDS bytes of a token's dy, or of its decoded input
+constexpr int kDy = BT * kRow, kRaw = BT * kTile, kStage = kDy + kRaw;
+constexpr int kTable = 1024;      // tokens whose scales are in LDS
+constexpr int kLds = kSlots * kStage + 2 * BT * kRow + kTable * static_cast<int>(sizeof(float));
 
+// The stages of dy and of the codes are loaded kSlots stages ahead, straight into LDS; the codes of stage s + 1
+// are decoded into a bf16 copy (two of them in turn) while stage s is multiplied.
 template <bool kE8M0>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
 fp8_wgrad_kernel(WgradParams p) {
-    __shared__ __attribute__((aligned(16))) uint8_t s_dy[BT * kRow];
-    __shared__ __attribute__((aligned(16))) uint8_t s_x[BT * kRow];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+    constexpr int kDecoded = kSlots * kStage;
+    float* table = reinterpret_cast<float*>(lds + kDecoded + 2 * BT * kRow);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave / kWavesK, wk = wave % kWavesK;
     const int g = lane >> 4, l15 = lane & 15;
-    const int wk = wave >> 1, wn = wave & 1;   // 32 columns of k and 32 rows of n per wave
-    const int tile = static_cast<int>(blockIdx.x) / p.split, part = static_cast<int>(blockIdx.x) % p.split;
+
+    // 8 contiguous ranges of tiles and their parts, one per XCD (workgroup b runs on XCD b % 8)
+    const int total = p.tiles_n * p.tiles_k * p.split, per = (total + 7) / 8;
+    const int local = static_cast<int>(blockIdx.x) / 8, lin = static_cast<int>(blockIdx.x) % 8 * per + local;
+    if (local >= per || lin >= total) return;
+    const int tile = lin / p.split, part = lin % p.split;
     const int n0 = tile / p.tiles_k * kTile, k0 = tile % p.tiles_k * kTile;
     const int64_t stages = (p.T + BT - 1) / BT;
-    const int64_t s0 = stages * part / p.split, s1 = stages * (part + 1) / p.split;
+    const int64_t s0 = stages * part / p.split;
+    const int nt = static_cast<int>(stages * (part + 1) / p.split - s0);
 
-    // thread: row tid / 8 of the stage, 8 columns from 8 (tid % 8); chunk c (16 bytes) of row r sits at
-    // c ^ (2 (r & 3)), so that the 4 rows x 32 bytes of a transposing read touch different banks
-    const int row = tid >> 3, col = (tid & 7) * 8;
-    const uint32_t put = static_cast<uint32_t>(row * kRow + (((tid & 7) ^ ((row & 3) << 1)) << 4));
-    const int64_t xs_row = static_cast<int64_t>(min(k0 + col, p.K - 1) / kFp8Block) * p.T;
-    const uint32_t base_dy = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_dy));
-    const uint32_t base_x = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_x));
-
-    v4f acc[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-
-    auto read = [&](uint32_t base, int c0) {   // 8 t of column c0 + l15: t = 8 g .. 8 g + 7
-        v2i f[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = 8 * g + 4 * h + (l15 >> 2);
-            const int chunk = (c0 / 8 + ((lane & 3) >> 1)) ^ ((r & 3) << 1);
-            f[h] = read_tr16(base + static_cast<uint32_t>(r * kRow + (chunk << 4) + (lane & 1) * 8));
-        }
-        return __builtin_bit_cast(v8bf, v4i{f[0].x, f[0].y, f[1].x, f[1].y});
+    // dy: 4 rows of 256 bytes a load; the 32-byte unit u (16 columns) of row t at u ^ (t & 7).  Codes: 8 rows
+    // of 128 bytes a load.
+    const int d_row = 4 * wave + (lane >> 4);
+    const uint32_t d_off = static_cast<uint32_t>(d_row) * static_cast<uint32_t>(p.N) * 2u +
+                           static_cast<uint32_t>(((lane & 15) ^ ((d_row & 7) << 1)) << 4);
+    const uint32_t x_off = static_cast<uint32_t>(8 * wave + (lane >> 3)) * static_cast<uint32_t>(p.K) + static_cast<uint32_t>((lane & 7) * 16);
+    auto issue = [&](int s) {
+        const int64_t t0 = (s0 + s) * BT;
+        const int rows = static_cast<int>(min<int64_t>(BT, p.T - t0));
+        const v4i rd = make_rsrc(p.dy + t0 * p.N + n0, (static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.N) - static_cast<uint32_t>(n0)) * 2u);
+        const v4i rx = make_rsrc(p.x + t0 * p.K + k0, static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.K) - static_cast<uint32_t>(k0));
+        const uint32_t slot = lds_base + static_cast<uint32_t>(s % kSlots * kStage + wave * 1024);
+        load_to_lds(rd, d_off, slot);
+        load_to_lds(rd, d_off + 64u * static_cast<uint32_t>(p.N), slot + kWaves * 1024);
+        load_to_lds(rx, x_off, slot + kDy);
     };
-    for (int64_t s = s0; s < s1; ++s) {
-        const int64_t t = s * BT + row;
-        uint4 d{0u, 0u, 0u, 0u};
-        uint2 q{0u, 0u};
-        float sc = 0.0f;
-        if (t < p.T) {
-            if (n0 + col < p.N) d = *reinterpret_cast<const uint4*>(p.dy + t * p.N + n0 + col);
-            if (k0 + col < p.K) q = *reinterpret_cast<const uint2*>(p.x + t * p.K + k0 + col);
-            sc = load_scale<kE8M0>(p.x_scale, xs_row + t);
+    constexpr int kLoads = 3;
+    const int64_t xs = static_cast<int64_t>(k0 / kFp8Block) * p.T;
+    auto fill = [&](int s) {   // the scales of the stages s ..
+#pragma unroll
+        for (int e = tid; e < kTable; e += kThreads)
+            table[e] = load_scale<kE8M0>(p.x_scale, xs + min<int64_t>((s0 + s) * BT + e, p.T - 1));
+    };
+    const int x_row = tid >> 3;
+    auto decode = [&](int s) {   // 16 codes a thread
+        const v4i q = *reinterpret_cast<const v4i*>(lds + s % kSlots * kStage + kDy + tid * 16);
+        const float sc = table[s * BT % kTable + x_row];
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float v[4];
+            decode4<false>(static_cast<uint32_t>(q[e]), v);
+            w[2 * e] = pack_bf16x2(v[0] * sc, v[1] * sc);
+            w[2 * e + 1] = pack_bf16x2(v[2] * sc, v[3] * sc);
         }
-        float v[8];
-        decode4<false>(q.x, v);
-        decode4<false>(q.y, v + 4);
-        uint4 x{pack_bf16x2(v[0] * sc, v[1] * sc), pack_bf16x2(v[2] * sc, v[3] * sc),
-                pack_bf16x2(v[4] * sc, v[5] * sc), pack_bf16x2(v[6] * sc, v[7] * sc)};
-        __syncthreads();
-        *reinterpret_cast<uint4*>(s_dy + put) = d;
-        *reinterpret_cast<uint4*>(s_x + put) = x;
-        __syncthreads();
-        v8bf fx[2], fd[2];
+        uint8_t* at = lds + kDecoded + (s & 1) * BT * kRow + x_row * kRow + (((tid & 7) ^ (x_row & 7)) << 5);
+        *reinterpret_cast<uint4*>(at) = uint4{w[0], w[1], w[2], w[3]};
+        *reinterpret_cast<uint4*>(at + 16) = uint4{w[4], w[5], w[6], w[7]};
+    };
+    // Fragments: lane group g holds tokens 16 q + 4 g + (0..3), q = 0..3, of its column.
+    const int r4 = l15 >> 2, swz = 4 * (g & 1) + r4;
+    const uint32_t d0 = lds_base + static_cast<uint32_t>((4 * g + r4) * kRow + (((TN * wn) ^ swz) << 5) + (l15 & 3) * 8);
+    const uint32_t x0 = lds_base + static_cast<uint32_t>(kDecoded + (4 * g + r4) * kRow + (((TK * wk) ^ swz) << 5) + (l15 & 3) * 8);
+    auto frag = [&](uint32_t at) {
+        const v2i r[4] = {read_tr16(at), read_tr16(at + 16 * kRow), read_tr16(at + 32 * kRow), read_tr16(at + 48 * kRow)};
+        return v8i{r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
+    };
+
+    v4f acc[TK][TN];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            fx[i] = read(base_x, wk * 32 + i * 16);
-            fd[i] = read(base_dy, wn * 32 + i * 16);
+    for (int j = 0; j < TK; ++j)
+#pragma unroll
+        for (int i = 0; i < TN; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (nt > 0) {
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+            if (s < nt) issue(s);
+        fill(0);
+        if (nt > kSlots - 1)
+            wait_vmcnt<(kSlots - 1) * kLoads>();
+        else
+            wait_vmcnt<0>();
+        lds_done();
+        barrier();   // stage 0 and the scales, in every wave
+        decode(0);
+    }
+    for (int s = 0; s < nt; ++s) {
+        lds_done();   // this wave's part of the decoded stage s is written, its fragments of stage s - 1 are read
+        // stage s + 1 has landed (later ones may be in flight), in every wave
+        if (s + kSlots - 1 < nt)
+            wait_vmcnt<(kSlots - 3) * kLoads>();
+        else
+            wait_vmcnt<0>();
+        barrier();
+        if (s > 0 && s + kSlots - 1 < nt) issue(s + kSlots - 1);   // into the slot of stage s - 1
+        if (s + 1 < nt) {
+            if ((s + 1) * BT % kTable == 0) {   // (every wave has decoded the last stage of the old table)
+                fill(s + 1);
+                lds_done();
+                barrier();
+            }
+            decode(s + 1);
         }
+        const uint32_t dy = d0 + static_cast<uint32_t>(s % kSlots * kStage), x = x0 + static_cast<uint32_t>((s & 1) * BT * kRow);
+        v8i fx[TK], fd[TN];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < TK; ++j) fx[j] = frag(x ^ static_cast<uint32_t>(j << 5));
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[i], fd[j], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < TN; ++i) fd[i] = frag(dy ^ static_cast<uint32_t>(i << 5));
+#pragma unroll
+        for (int j = 0; j < TK; ++j)
+#pragma unroll
+            for (int i = 0; i < TN; ++i) acc[j][i] = mfma_bf16(fx[j], fd[i], acc[j][i]);
     }
     void* dw = p.dw;
     if (p.split > 1) dw = static_cast<float*>(p.dw) + static_cast<int64_t>(part) * p.N * p.K;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < TK; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int i = 0; i < TN; ++i) {
             // K is a multiple of 16: four columns are all in or all out
-            const int n = n0 + wn * 32 + j * 16 + l15, k = k0 + wk * 32 + i * 16 + 4 * g;
+            const int n = n0 + wn * WN + i * 16 + l15, k = k0 + wk * WK + j * 16 + 4 * g;
             if (n < p.N && k < p.K)
                 wgrad_put4(dw, p.split == 1 && p.dw_bf16, p.split == 1 && p.accumulate, static_cast<int64_t>(n) * p.K + k,
-                     acc[i][j]);
+                           acc[j][i]);
         }
 }
 
@@ -119,19 +178,18 @@ wgrad_reduce_kernel(const float* __restrict__ part, int split, int64_t n, void* 
     wgrad_put4(dw, bf16, accumulate, i, s);
 }
 
-int choose_split(int64_t tiles, int64_t stages) {
-    const int64_t want = 2 * 256;
-    if (tiles >= want) return 1;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want / tiles, stages / 4, 16})));
-}
-
 int64_t tiles_of(int N, int K) { return static_cast<int64_t>((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile); }
+
+// Ranges of the tokens per tile: a workgroup for each CU, each at least eight stages long.
+int choose_split(int64_t tiles, int64_t T) {
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({device_cu_count() / tiles, (T + BT - 1) / BT / 8, 16})));
+}
 
 }  // namespace
 
 size_t fp8_wgrad_workspace_bytes(int64_t T, int N, int K) {
     if (wgrad_large_takes(T, N, K)) return 0;
-    const int split = choose_split(tiles_of(N, K), (T + BT - 1) / BT);
+    const int split = choose_split(tiles_of(N, K), T);
     return split > 1 ? static_cast<size_t>(split) * N * K * sizeof(float) : 0;
 }
 
@@ -143,22 +201,24 @@ hipError_t launch_fp8_wgrad(const Fp8WgradArgs& g, hipStream_t stream) {
     p.T = g.T;
     p.N = g.N;
     p.K = g.K;
+    p.split = 1;
     p.dw = g.dw;
     p.dw_bf16 = g.dw_bf16;
     p.accumulate = g.accumulate;
     if (wgrad_large_takes(g.T, g.N, g.K)) return launch_wgrad_large(p, g.e8m0, stream);
+    auto kernel = g.e8m0 ? fp8_wgrad_kernel<true> : fp8_wgrad_kernel<false>;
+    int per_cu = 0;
+    hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), kThreads, kLds, &per_cu);
+    if (e != hipSuccess) return e;
     p.tiles_n = (g.N + kTile - 1) / kTile;
     p.tiles_k = (g.K + kTile - 1) / kTile;
-    const int64_t tiles = tiles_of(g.N, g.K);
-    p.split = choose_split(tiles, (g.T + BT - 1) / BT);
+    p.split = choose_split(tiles_of(g.N, g.K), g.T);
     const int64_t n = static_cast<int64_t>(g.N) * g.K;
     if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(p.split) * n * sizeof(float)) p.split = 1;
     if (p.split > 1) p.dw = g.workspace;
-    if (g.e8m0)
-        fp8_wgrad_kernel<true><<<static_cast<unsigned>(tiles * p.split), 256, 0, stream>>>(p);
-    else
-        fp8_wgrad_kernel<false><<<static_cast<unsigned>(tiles * p.split), 256, 0, stream>>>(p);
-    hipError_t e = hipGetLastError();
+    const int64_t total = tiles_of(g.N, g.K) * p.split;
+    kernel<<<static_cast<unsigned>((total + 7) / 8 * 8), kThreads, kLds, stream>>>(p);
+    e = hipGetLastError();
     if (e != hipSuccess || p.split == 1) return e;
     wgrad_reduce_kernel<<<static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, stream>>>(
         static_cast<const float*>(g.workspace), p.split, n, g.dw, g.dw_bf16, g.accumulate);

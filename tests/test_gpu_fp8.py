@@ -293,7 +293,7 @@ def test_linear_equals_its_parts(T, N, K, st):
 
 
 @pytest.mark.parametrize("st", [F32, E8M0])
-@pytest.mark.parametrize("T,N,K", [(1, 8, 16), (3, 40, 144), (31, 136, 128), (64, 64, 64), (517, 264, 1040), (1500, 72, 272)])
+@pytest.mark.parametrize("T,N,K", [(1, 8, 16), (3, 40, 144), (31, 136, 128), (64, 64, 64), (517, 264, 1040), (1500, 72, 272), (4200, 136, 400), (129, 8, 16), (65, 640, 656)])
 def test_wgrad_exact(T, N, K, st):
     """Whole-number operands: every product and sum is exact in fp32."""
     step("wgrad", T, N, K, st)
