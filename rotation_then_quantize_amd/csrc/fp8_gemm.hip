@@ -24,7 +24,7 @@ namespace {
 
 using namespace fp8;
 
-constexpr int kTable = 32;   // blocks whose scales are in LDS
+constexpr int kTable = 32;   // blocks whose scales are in LDS (an even number)
 
 template <int BM, int BN, int kSlots>
 constexpr int tile_lds() { return kSlots * (BM + BN) * BK + kTable * BM * static_cast<int>(sizeof(float)); }
@@ -65,6 +65,7 @@ fp8_gemm_kernel(Fp8GemmParams p) {
 
     const int rows_a = static_cast<int>(min<int64_t>(BM, p.M - m0));
     const int rows_w = static_cast<int>(min<int64_t>(BN, p.N - n0));
+    const int end = min(p.R, kb1 * BK);   // of this part of the reduction: loads past it give zeros
     const v4i rsa = make_rsrc(p.a + m0 * p.R, static_cast<uint32_t>(rows_a) * static_cast<uint32_t>(p.R));
     v4i rsw = make_rsrc(p.w + (kTrans ? 0 : n0 * p.R), static_cast<uint32_t>(rows_w) * static_cast<uint32_t>(p.R));
 
@@ -77,13 +78,13 @@ fp8_gemm_kernel(Fp8GemmParams p) {
         for (int q = 0; q < kALoads; ++q) {
             const int row = 8 * (q * kWaves + wave) + (lane >> 3);
             const int col = kb * BK + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
-            load_to_lds(rsa, col < p.R ? static_cast<uint32_t>(row * p.R + col) : kOob,
+            load_to_lds(rsa, col < end ? static_cast<uint32_t>(row * p.R + col) : kOob,
                         slot + static_cast<uint32_t>((q * kWaves + wave) * 1024));
         }
         if constexpr (kTrans) {
-            const int rows = min(BK, p.R - kb * BK);
+            const int rows = min(BK, end - kb * BK);
             rsw = make_rsrc(p.w + static_cast<int64_t>(kb) * BK * p.N + n0,
-                            static_cast<uint32_t>(rows * p.N - n0));
+                            rows > 0 ? static_cast<uint32_t>(rows * p.N - n0) : 0u);
         }
 #pragma unroll
         for (int q = 0; q < kWLoads; ++q) {
@@ -94,7 +95,7 @@ fp8_gemm_kernel(Fp8GemmParams p) {
             } else {
                 const int row = 8 * (q * kWaves + wave) + (lane >> 3);
                 const int col = kb * BK + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
-                off = col < p.R ? static_cast<uint32_t>(row * p.R + col) : kOob;
+                off = col < end ? static_cast<uint32_t>(row * p.R + col) : kOob;
             }
             load_to_lds(rsw, off, slot + static_cast<uint32_t>(kABytes + (q * kWaves + wave) * 1024));
         }
@@ -132,7 +133,11 @@ fp8_gemm_kernel(Fp8GemmParams p) {
     constexpr int kLoads = kALoads + kWLoads;
     v8i fa[2][TM], fw[2][TN];
     float sc[2][TM];
-    // Block kb from the fragments and scales of set P, while those of block kb + 1 are read into the other.
+    auto read_scales = [&](auto set, int kb) {
+        constexpr int P = decltype(set)::value;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sc[P][i] = table[(kb - kb0) % kTable * BM + (wm * 16 + l15) * TM + i];
+    };
     auto read = [&](auto set, int kb) {
         constexpr int P = decltype(set)::value;
         const int slot = ((kb - kb0) % kSlots) * kStage;
@@ -144,29 +149,19 @@ fp8_gemm_kernel(Fp8GemmParams p) {
                 fw[P][j] = read_frag(lds + slot + kABytes + (wn * WN + j * 16) * BK);
         }
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            fa[P][i] = read_frag(lds + slot + (wm * WM + i * 16) * BK);
-            sc[P][i] = table[(kb - kb0) % kTable * BM + (wm * 16 + l15) * TM + i];
-        }
+        for (int i = 0; i < TM; ++i) fa[P][i] = read_frag(lds + slot + (wm * WM + i * 16) * BK);
+        read_scales(set, kb);
     };
+    // Block kb from the fragments and scales of set P, while those of block kb + 1 are read into the other.
+    // Nothing here is conditional: with a branch the compiler would wait for all of the reads before the
+    // products.  Past the last block zeros are loaded, and what is read is not used.
     auto block = [&](auto set, int kb) {
         constexpr int P = decltype(set)::value;
-        lds_done();   // this wave's fragments of block kb are in registers
-        // block kb + 1 has landed (later ones may be in flight), in every wave; block kb's slot is free
-        if (kb + kSlots - 1 < kb1)
-            wait_vmcnt<(kSlots - 2) * kLoads>();
-        else
-            wait_vmcnt<0>();
-        barrier();
-        if (kb + kSlots < kb1) issue(kb + kSlots);
-        if (kb + 1 < kb1) {
-            if ((kb + 1 - kb0) % kTable == 0) {   // (every wave has read the last scales of the old table)
-                fill(kb + 1);
-                lds_done();
-                barrier();
-            }
-            read(std::integral_constant<int, 1 - P>{}, kb + 1);
-        }
+        lds_done();                            // this wave's fragments of block kb are in registers
+        wait_vmcnt<(kSlots - 2) * kLoads>();   // block kb + 1 has landed (later ones may be in flight) ...
+        barrier();                             // ... in every wave; block kb's slot is free
+        issue(kb + kSlots);
+        read(std::integral_constant<int, 1 - P>{}, kb + 1);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -179,20 +174,30 @@ fp8_gemm_kernel(Fp8GemmParams p) {
     constexpr auto P0 = std::integral_constant<int, 0>{};
     constexpr auto P1 = std::integral_constant<int, 1>{};
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s)
-        if (kb0 + s < kb1) issue(kb0 + s);
+    for (int s = 0; s < kSlots; ++s) issue(kb0 + s);
     fill(kb0);
-    if (kb0 + kSlots - 1 < kb1)
-        wait_vmcnt<(kSlots - 1) * kLoads>();
-    else
-        wait_vmcnt<0>();
+    wait_vmcnt<(kSlots - 1) * kLoads>();
     lds_done();
     barrier();
     read(P0, kb0);
-    for (int kb = kb0; kb < kb1; kb += 2) {
-        block(P0, kb);
-        if (kb + 1 < kb1) block(P1, kb + 1);
+    for (int c0 = kb0; c0 < kb1; c0 += kTable) {
+        if (c0 != kb0) {   // the next blocks' scales, once every wave has read the last of the old ones
+            lds_done();
+            barrier();
+            fill(c0);
+            lds_done();
+            barrier();
+            read_scales(P0, c0);
+        }
+        const int c1 = min(c0 + kTable, kb1);
+        int kb = c0;
+        for (; kb + 1 < c1; kb += 2) {
+            block(P0, kb);
+            block(P1, kb + 1);
+        }
+        if (kb < c1) block(P0, kb);
     }
+    wait_vmcnt<0>();   // nothing is still writing this workgroup's LDS when another one gets it
     void* y = p.y;
     if (p.split > 1) y = static_cast<float*>(p.y) + static_cast<int64_t>(part) * p.M * p.N;
 #pragma unroll

@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8_internal.h"
 #include "fp8_tile.h"
@@ -33,11 +34,12 @@ constexpr int WN = kTile / kWavesN, WK = kTile / kWavesK, TN = WN / 16, TK = WK 
 constexpr int kSlots = 4;         // stages of dy and of codes in LDS
 constexpr int kRow = kTile * 2;   // LDS bytes of a token's dy, or of its decoded input
 constexpr int kDy = BT * kRow, kRaw = BT * kTile, kStage = kDy + kRaw;
-constexpr int kTable = 1024;      // tokens whose scales are in LDS
-constexpr int kLds = kSlots * kStage + 2 * BT * kRow + kTable * static_cast<int>(sizeof(float));
+constexpr int kTable = 1024;      // tokens whose scales are in LDS, and those of two stages more
+constexpr int kLds = kSlots * kStage + 2 * BT * kRow + (kTable + 2 * BT) * static_cast<int>(sizeof(float));
 
-// The stages of dy and of the codes are loaded kSlots stages ahead, straight into LDS; the codes of stage s + 1
-// are decoded into a bf16 copy (two of them in turn) while stage s is multiplied.
+// The stages of dy and of the codes are loaded kSlots stages ahead, straight into LDS; while stage s is
+// multiplied, the codes of stage s + 2 are decoded into a bf16 copy (two of them in turn) and the fragments of
+// stage s + 1 are read.
 template <bool kE8M0>
 __global__ void __launch_bounds__(kThreads)
 fp8_wgrad_kernel(WgradParams p) {
@@ -60,6 +62,7 @@ fp8_wgrad_kernel(WgradParams p) {
     const int64_t s0 = stages * part / p.split;
     const int nt = static_cast<int>(stages * (part + 1) / p.split - s0);
 
+    const int64_t end = min<int64_t>(p.T, (s0 + nt) * BT);   // loads past this part's tokens give zeros
     // dy: 4 rows of 256 bytes a load; the 32-byte unit u (16 columns) of row t at u ^ (t & 7).  Codes: 8 rows
     // of 128 bytes a load.
     const int d_row = 4 * wave + (lane >> 4);
@@ -68,9 +71,10 @@ fp8_wgrad_kernel(WgradParams p) {
     const uint32_t x_off = static_cast<uint32_t>(8 * wave + (lane >> 3)) * static_cast<uint32_t>(p.K) + static_cast<uint32_t>((lane & 7) * 16);
     auto issue = [&](int s) {
         const int64_t t0 = (s0 + s) * BT;
-        const int rows = static_cast<int>(min<int64_t>(BT, p.T - t0));
-        const v4i rd = make_rsrc(p.dy + t0 * p.N + n0, (static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.N) - static_cast<uint32_t>(n0)) * 2u);
-        const v4i rx = make_rsrc(p.x + t0 * p.K + k0, static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.K) - static_cast<uint32_t>(k0));
+        const int rows = static_cast<int>(max<int64_t>(0, min<int64_t>(BT, end - t0)));
+        const uint32_t mask = rows > 0 ? ~0u : 0u;
+        const v4i rd = make_rsrc(p.dy + t0 * p.N + n0, ((static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.N) - static_cast<uint32_t>(n0)) * 2u) & mask);
+        const v4i rx = make_rsrc(p.x + t0 * p.K + k0, (static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.K) - static_cast<uint32_t>(k0)) & mask);
         const uint32_t slot = lds_base + static_cast<uint32_t>(s % kSlots * kStage + wave * 1024);
         load_to_lds(rd, d_off, slot);
         load_to_lds(rd, d_off + 64u * static_cast<uint32_t>(p.N), slot + kWaves * 1024);
@@ -80,13 +84,17 @@ fp8_wgrad_kernel(WgradParams p) {
     const int64_t xs = static_cast<int64_t>(k0 / kFp8Block) * p.T;
     auto fill = [&](int s) {   // the scales of the stages s ..
 #pragma unroll
-        for (int e = tid; e < kTable; e += kThreads)
+        for (int e = tid; e < kTable + 2 * BT; e += kThreads)
             table[e] = load_scale<kE8M0>(p.x_scale, xs + min<int64_t>((s0 + s) * BT + e, p.T - 1));
     };
     const int x_row = tid >> 3;
-    auto decode = [&](int s) {   // 16 codes a thread
-        const v4i q = *reinterpret_cast<const v4i*>(lds + s % kSlots * kStage + kDy + tid * 16);
-        const float sc = table[s * BT % kTable + x_row];
+    v4i q;      // 16 codes a thread
+    float sc;   // and their token's scale; the table begins with stage `first`
+    auto read_codes = [&](int s, int first) {
+        q = *reinterpret_cast<const v4i*>(lds + s % kSlots * kStage + kDy + tid * 16);
+        sc = table[(s - first) * BT + x_row];
+    };
+    auto decode = [&](int s) {
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -113,46 +121,66 @@ fp8_wgrad_kernel(WgradParams p) {
     for (int j = 0; j < TK; ++j)
 #pragma unroll
         for (int i = 0; i < TN; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (nt > 0) {
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-            if (s < nt) issue(s);
-        fill(0);
-        if (nt > kSlots - 1)
-            wait_vmcnt<(kSlots - 1) * kLoads>();
-        else
-            wait_vmcnt<0>();
-        lds_done();
-        barrier();   // stage 0 and the scales, in every wave
-        decode(0);
-    }
-    for (int s = 0; s < nt; ++s) {
-        lds_done();   // this wave's part of the decoded stage s is written, its fragments of stage s - 1 are read
-        // stage s + 1 has landed (later ones may be in flight), in every wave
-        if (s + kSlots - 1 < nt)
-            wait_vmcnt<(kSlots - 3) * kLoads>();
-        else
-            wait_vmcnt<0>();
-        barrier();
-        if (s > 0 && s + kSlots - 1 < nt) issue(s + kSlots - 1);   // into the slot of stage s - 1
-        if (s + 1 < nt) {
-            if ((s + 1) * BT % kTable == 0) {   // (every wave has decoded the last stage of the old table)
-                fill(s + 1);
-                lds_done();
-                barrier();
-            }
-            decode(s + 1);
-        }
+    v8i fx[2][TK], fd[2][TN];
+    auto read = [&](auto set, int s) {
+        constexpr int P = decltype(set)::value;
         const uint32_t dy = d0 + static_cast<uint32_t>(s % kSlots * kStage), x = x0 + static_cast<uint32_t>((s & 1) * BT * kRow);
-        v8i fx[TK], fd[TN];
 #pragma unroll
-        for (int j = 0; j < TK; ++j) fx[j] = frag(x ^ static_cast<uint32_t>(j << 5));
+        for (int j = 0; j < TK; ++j) fx[P][j] = frag(x ^ static_cast<uint32_t>(j << 5));
 #pragma unroll
-        for (int i = 0; i < TN; ++i) fd[i] = frag(dy ^ static_cast<uint32_t>(i << 5));
+        for (int i = 0; i < TN; ++i) fd[P][i] = frag(dy ^ static_cast<uint32_t>(i << 5));
+    };
+    // Stage s from the fragments of set P, while those of stage s + 1 are read and stage s + 2 is decoded.
+    // Nothing here is conditional (see the products); past the last stage zeros are loaded and decoded.
+    auto stage = [&](auto set, int s, int first) {
+        constexpr int P = decltype(set)::value;
+        lds_done();              // this wave's part of the decoded stage s + 1 is written, its fragments of stage s are read
+        wait_vmcnt<kLoads>();    // stage s + 2 has landed (the next one may be in flight) ...
+        barrier();               // ... in every wave; stage s's slot and decoded copy are free
+        issue(s + kSlots);
+        read_codes(s + 2, first);   // before the fragments: it is needed first
+        read(std::integral_constant<int, 1 - P>{}, s + 1);
 #pragma unroll
         for (int j = 0; j < TK; ++j)
 #pragma unroll
-            for (int i = 0; i < TN; ++i) acc[j][i] = mfma_bf16(fx[j], fd[i], acc[j][i]);
+            for (int i = 0; i < TN; ++i) acc[j][i] = mfma_bf16(fx[P][j], fd[P][i], acc[j][i]);
+        decode(s + 2);
+    };
+    constexpr auto P0 = std::integral_constant<int, 0>{};
+    constexpr auto P1 = std::integral_constant<int, 1>{};
+    if (nt > 0) {
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) issue(s);
+        fill(0);
+        wait_vmcnt<(kSlots - 2) * kLoads>();
+        lds_done();
+        barrier();   // stages 0 and 1 and the scales, in every wave
+        read_codes(0, 0);
+        decode(0);
+        read_codes(1, 0);
+        decode(1);
+        lds_done();
+        barrier();
+        read(P0, 0);
+        // The table holds the scales of kTable / BT stages; stage s decodes stage s + 2.
+        constexpr int kPer = kTable / BT;
+        for (int c = 0; c < nt; c += kPer) {
+            if (c > 0) {   // once every wave has decoded the last of the old ones
+                lds_done();
+                barrier();
+                fill(c);
+                lds_done();
+                barrier();
+            }
+            const int c1 = min(c + kPer, nt);
+            int s = c;
+            for (; s + 1 < c1; s += 2) {
+                stage(P0, s, c);
+                stage(P1, s + 1, c);
+            }
+            if (s < c1) stage(P0, s, c);
+        }
+        wait_vmcnt<0>();   // nothing is still writing this workgroup's LDS when another one gets it
     }
     void* dw = p.dw;
     if (p.split > 1) dw = static_cast<float*>(p.dw) + static_cast<int64_t>(part) * p.N * p.K;
