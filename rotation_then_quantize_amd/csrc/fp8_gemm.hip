@@ -31,9 +31,10 @@ constexpr int tile_lds() { return kSlots * (BM + BN) * BK + kTable * BM * static
 
 // A tile of BM x BN outputs, a ring of kSlots LDS stages of one block of the reduction each, loaded kSlots
 // stages ahead (tiles this small are bound by the loads' latency, not by their products); a block's fragments
-// are read while the block before it is multiplied.  The rows' scales
-// times the weight's, of kTable blocks at a time, are put into LDS beforehand: loads of scales among the
-// stages' would make every wait for one a wait for the stages behind it.
+// are read while the block before it is multiplied (with branches in that stage, which made the compiler wait
+// for the reads first, 512 x 4096 x 4096 took 20.8 us instead of 18.4).  The rows' scales times the weight's,
+// of kTable blocks at a time, are put into LDS beforehand: loads of scales among the stages' would make every
+// wait for one a wait for the stages behind it.
 template <int BM, int BN, int kWavesM, int kWavesN, int kSlots, bool kTrans, bool kE5M2, bool kE8M0>
 __global__ void __launch_bounds__(64 * kWavesM * kWavesN)
 fp8_gemm_kernel(Fp8GemmParams p) {
@@ -42,7 +43,6 @@ fp8_gemm_kernel(Fp8GemmParams p) {
     constexpr int TM = WM / 16, TN = WN / 16;
     constexpr int kABytes = BM * BK, kWBytes = BN * BK, kStage = kABytes + kWBytes;
     constexpr int kALoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves;   // 1 KB loads per wave
-    constexpr int kChunks = BN / 16;                                      // kTrans: 16-byte chunks per LDS row
     static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && BN <= kFp8Block, "whole loads per wave, one weight scale");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
@@ -90,6 +90,7 @@ fp8_gemm_kernel(Fp8GemmParams p) {
         for (int q = 0; q < kWLoads; ++q) {
             uint32_t off;
             if constexpr (kTrans) {
+                constexpr int kChunks = BN / 16;   // 16-byte chunks of an LDS row
                 const int row = (64 / kChunks) * (q * kWaves + wave) + lane / kChunks;
                 off = static_cast<uint32_t>(row * static_cast<int>(p.N) + (((lane % kChunks) ^ tr_swizzle<BN>(row)) << 4));
             } else {
@@ -240,14 +241,15 @@ struct Plan {
 };
 
 // Measured at a reduction of 4096 (M x 4096 outputs, us):
-//              M = 64      128      256      512      1000     1500     2048
-//   64 x 64    16.6        16.9     17.4     20.8     38.0     54.3      -
-//   128 x 128  24.1        25.5     25.9     26.6     28.8     50.6      -
-//   256 x 256   -           -        -        -       35       35        38
+//              M = 64      128      256      512      768      1000     1500     2048
+//   64 x 64    13.0        13.4     14.0     17.8     29.0     34.7     51.9     75.6
+//   128 x 128  19.9        21.1     21.4     22.2     23.2     24.3     42.9     49.3
+//   256 x 256  32.5        33.1     33.1     33.4     33.5     33.4     34.8     38.9
 // A tile costs its chain of stages as long as each CU has one (128: one workgroup per CU, 64: two), so the
 // largest tile whose workgroups fit at once is taken.  Splitting the reduction shortens the chain of the 64
-// x 64 tiles where CUs are idle (M = 64: 11.4 us in four, M = 128: 13.6 in two); below 12 blocks a part the
-// second kernel costs what it saves.
+// x 64 tiles: in as many parts as give each CU one workgroup (M = 64: 13.0 to 11.7 us in two, M = 128: 13.4
+// to 12.7 in two), or two where the parts stay long (M = 128, reduction of 16384: 45.0, in two 28.2, in four
+// 22.9; of 4096: 12.7, 12.8); below 12 blocks a part the second kernel costs what it saves.
 Plan plan(int64_t M, int64_t N, int R, bool trans) {
     if (fp8_small_takes(M, N, R, trans)) return {kSmall, 1};
     auto tiles = [&](int64_t t) { return (M + t - 1) / t * ((N + t - 1) / t); };
@@ -257,7 +259,8 @@ Plan plan(int64_t M, int64_t N, int R, bool trans) {
         if (tiles(128) <= cus) return {kTile128, 1};
         if (blocks > 1) return {kLarge, 1};   // (its loads run two stages ahead)
     }
-    return {kTile64, static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({cus / tiles(64), blocks / 12, 16})))};
+    const int64_t one = std::min<int64_t>(cus / tiles(64), blocks / 12), two = std::min<int64_t>(2 * cus / tiles(64), blocks / 32);
+    return {kTile64, static_cast<int>(std::clamp<int64_t>(std::max(one, two), 1, 16))};
 }
 
 template <int BT, int kWavesM, int kWavesN, int kSlots, bool kTrans, bool kE5M2>

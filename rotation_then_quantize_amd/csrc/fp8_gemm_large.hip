@@ -1,4 +1,4 @@
-// fp8_gemm_large.hip -- the 8-bit product for outputs of many tiles: 256 x 256 (or 128 x 128) outputs per
+// fp8_gemm_large.hip -- the 8-bit product for outputs of many tiles: 256 x 256 outputs per
 // workgroup.
 //
 // A workgroup of 8 waves (two per SIMD) owns 256 x 256 outputs, each wave 128 x 64 of them as 8 x 4
@@ -36,20 +36,13 @@ namespace {
 using namespace fp8;
 
 constexpr int kXcds = 8;
-constexpr int kWavesM = 2;
-
-// A workgroup's tile of kM x kN outputs: waves of (kM / 2) x 64.
-template <int kM, int kN>
-struct Tile {
-    static constexpr int kRows = kM, BN = kN;
-    static constexpr int kWavesN = BN / 64, kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
-    static constexpr int kBlocks = BN / BK;                                            // weight scales across
-    static constexpr int kRing = 2 * (kRows + BN) * BK;
-    static constexpr int kScaleBytes = 2 * kBlocks * kRows * static_cast<int>(sizeof(float));   // [slot][column block][row]
-    static constexpr int kStageOut = kWaves * 16 * 128;                                // epilogue: 16 rows x 128 bytes a wave
-    static constexpr int kLds = kRing + kScaleBytes + kStageOut;
-};
-using Large = Tile<256, 256>;    // one workgroup per CU
+constexpr int kTileM = 256, BN = 256;
+constexpr int kWavesM = 2, kWavesN = 4, kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
+constexpr int kBlocks = BN / BK;                                                            // weight scales across
+constexpr int kRing = 2 * (kTileM + BN) * BK;
+constexpr int kScaleBytes = 2 * kBlocks * kTileM * static_cast<int>(sizeof(float));         // [slot][column block][row]
+constexpr int kStageOut = kWaves * 16 * 128;                                                // epilogue: 16 rows x 128 bytes a wave
+constexpr int kLds = kRing + kScaleBytes + kStageOut;
 
 // Tile index within the XCD-ordered sequence -> (tile_m, tile_n), in bands of 8 N-tiles.
 __device__ __forceinline__ void tile_of(int lin, int tiles_m, int tiles_n, int* tm, int* tn) {
@@ -77,16 +70,14 @@ struct LargeParams {
     int full;      // tiles [0, full) are taken whole; the rest as two halves of their rows
 };
 
-// Tiles of BM rows: G's, or halves of them.
-template <typename G, int BM, bool kTrans, bool kE5M2, bool kE8M0>
+// Tiles of BM rows: kTileM, or half of that.
+template <int BM, bool kTrans, bool kE5M2, bool kE8M0>
 __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds, int first, int end, int stride) {
-    constexpr int BN = G::BN, kWavesN = G::kWavesN, kWaves = G::kWaves, kMaxM = G::kRows, kRing = G::kRing;
-    constexpr int kScaleBytes = G::kScaleBytes, kBlocks = G::kBlocks;
     constexpr int WM = BM / kWavesM, TM = WM / 16, WN = BN / kWavesN, TN = WN / 16;
-    static_assert(TN == 4 && (BN == 256 || BN == 128), "the transposing read's addresses");
+    static_assert(TN == 4, "the transposing read's addresses");
     constexpr int kABytes = BM * BK, kStage = kABytes + BN * BK;
     constexpr int kALoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves;   // 1 KB loads per wave
-    constexpr int kHalves = kMaxM / BM;                                   // tiles of BM rows per tile of G
+    constexpr int kHalves = kTileM / BM;                                  // tiles of BM rows per whole tile
     static_assert(TM % 2 == 0 && TM >= 4, "row tiles");
     const Fp8GemmParams& p = lp.g;
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
@@ -102,7 +93,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     auto place = [&](int lin, int64_t* m0, int64_t* n0) {
         int tm, tn;
         tile_of(lin / kHalves, p.tiles_m, p.tiles_n, &tm, &tn);
-        *m0 = static_cast<int64_t>(tm) * kMaxM + (lin % kHalves) * BM;
+        *m0 = static_cast<int64_t>(tm) * kTileM + (lin % kHalves) * BM;
         *n0 = static_cast<int64_t>(tn) * BN;
     };
     // The loads run two stages ahead of the products, over the ends of tiles: their own tile and block.
@@ -143,7 +134,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     // The stage's scales: thread t holds row t % BM's scale and, for its wave's column block, the
     // weight's, until they are written to LDS (with 128 rows, threads 256.. write the same again).
     const int s_row = tid % WM, s_cb = tid / BM % kBlocks;
-    const int s_at = s_cb * kMaxM + ((tid % BM / WM) * 16 + (s_row & 15)) * TM + (s_row >> 4);
+    const int s_at = s_cb * kTileM + ((tid % BM / WM) * 16 + (s_row & 15)) * TM + (s_row >> 4);
     constexpr int kScaleSize = kE8M0 ? 1 : 4;
     uint32_t r_a = 0u, r_w = 0u;   // as loaded: converting them here would wait for the loads just issued
     auto load_scales = [&]() {
@@ -156,9 +147,9 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     };
     auto write_scales = [&](int slot) {
         if constexpr (kE8M0)   // both bytes, for the matrix instruction
-            reinterpret_cast<uint16_t*>(s_scale)[slot * kBlocks * kMaxM + s_at] = static_cast<uint16_t>(r_a | r_w << 8);
+            reinterpret_cast<uint16_t*>(s_scale)[slot * kBlocks * kTileM + s_at] = static_cast<uint16_t>(r_a | r_w << 8);
         else
-            s_scale[slot * kBlocks * kMaxM + s_at] = __uint_as_float(r_a) * __uint_as_float(r_w);
+            s_scale[slot * kBlocks * kTileM + s_at] = __uint_as_float(r_a) * __uint_as_float(r_w);
     };
     auto issue = [&](int slot) {   // the cursor's stage, and the cursor moves on
         const int kb = c_kb;
@@ -208,14 +199,14 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     v4f d[TN];
     float sc[TM], s_last = 0.f;
     uint32_t eb[TM / 2], eb_next[TM / 2];
-    const int s_mine = (wn / 2) * kMaxM + (wm * 16 + l15) * TM;
+    const int s_mine = (wn / 2) * kTileM + (wm * 16 + l15) * TM;
     auto read_scales = [&](int slot) {
         if constexpr (kE8M0) {
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(s_scale) + slot * kBlocks * kMaxM + s_mine);
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(s_scale) + slot * kBlocks * kTileM + s_mine);
 #pragma unroll
             for (int i = 0; i < TM / 2; ++i) eb_next[i] = q[i];
         } else {
-            const v4f* q = reinterpret_cast<const v4f*>(s_scale + slot * kBlocks * kMaxM + s_mine);
+            const v4f* q = reinterpret_cast<const v4f*>(s_scale + slot * kBlocks * kTileM + s_mine);
 #pragma unroll
             for (int i = 0; i < TM / 4; ++i) {
                 const v4f x = q[i];
@@ -375,46 +366,38 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     wait_vmcnt<0>();   // nothing is still writing LDS when the workgroup's next tiles, or another workgroup, use it
 }
 
-template <typename G, bool kTrans, bool kE5M2, bool kE8M0>
-__global__ void __launch_bounds__(G::kThreads, 1)
+template <bool kTrans, bool kE5M2, bool kE8M0>
+__global__ void __launch_bounds__(kThreads, 1)
 fp8_gemm_large_kernel(LargeParams p) {
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     // Tiles are split into 8 contiguous ranges, one per XCD (block b runs on XCD b % 8); the blocks of an
     // XCD walk their range together, in bands of 8 N-tiles, and share operand panels in that L2.
     const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds, stride = gridDim.x / kXcds;
     const int per = (p.full + kXcds - 1) / kXcds;
-    large_tiles<G, G::kRows, kTrans, kE5M2, kE8M0>(p, lds, xcd * per + local, min((xcd + 1) * per, p.full), stride);
-    if constexpr (G::kRows == 256) {
-        const int rest = 2 * (p.g.tiles_m * p.g.tiles_n - p.full), rper = (rest + kXcds - 1) / kXcds;
-        if (rest > 0) {
-            __syncthreads();
-            const int r0 = 2 * p.full;
-            large_tiles<G, 128, kTrans, kE5M2, kE8M0>(p, lds, r0 + xcd * rper + local, r0 + min((xcd + 1) * rper, rest), stride);
-        }
+    large_tiles<kTileM, kTrans, kE5M2, kE8M0>(p, lds, xcd * per + local, min((xcd + 1) * per, p.full), stride);
+    const int rest = 2 * (p.g.tiles_m * p.g.tiles_n - p.full), rper = (rest + kXcds - 1) / kXcds;
+    if (rest > 0) {
+        __syncthreads();
+        const int r0 = 2 * p.full;
+        large_tiles<kTileM / 2, kTrans, kE5M2, kE8M0>(p, lds, r0 + xcd * rper + local, r0 + min((xcd + 1) * rper, rest), stride);
     }
 }
 
-template <typename G, bool kTrans, bool kE5M2, bool kE8M0>
+template <bool kTrans, bool kE5M2, bool kE8M0>
 hipError_t launch(const Fp8GemmParams& g, hipStream_t stream) {
-    auto kernel = fp8_gemm_large_kernel<G, kTrans, kE5M2, kE8M0>;
+    auto kernel = fp8_gemm_large_kernel<kTrans, kE5M2, kE8M0>;
     int per_cu = 0;
-    hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), G::kThreads, G::kLds, &per_cu);
+    hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), kThreads, kLds, &per_cu);
     if (e != hipSuccess) return e;
     LargeParams p{};
     p.g = g;
-    p.g.tiles_m = static_cast<int>((g.M + G::kRows - 1) / G::kRows);
-    p.g.tiles_n = static_cast<int>((g.N + G::BN - 1) / G::BN);
+    p.g.tiles_m = static_cast<int>((g.M + kTileM - 1) / kTileM);
+    p.g.tiles_n = static_cast<int>((g.N + BN - 1) / BN);
     const int cus = std::max(kXcds, device_cu_count() / kXcds * kXcds);
-    const int total = p.g.tiles_m * p.g.tiles_n;
-    if constexpr (G::kRows == 256) {
-        // whole rounds of 256-row tiles; a remainder that fills at most half a round goes as 128-row halves
-        const int rest = total % cus;
-        p.full = rest > 0 && rest <= cus / 2 ? total - rest : total;
-        kernel<<<cus, G::kThreads, G::kLds, stream>>>(p);
-    } else {
-        p.full = total;
-        kernel<<<std::min(2 * cus, (total + kXcds - 1) / kXcds * kXcds), G::kThreads, G::kLds, stream>>>(p);
-    }
+    // whole rounds of whole tiles; a remainder that fills at most half a round goes as halves of 128 rows
+    const int total = p.g.tiles_m * p.g.tiles_n, rest = total % cus;
+    p.full = rest > 0 && rest <= cus / 2 ? total - rest : total;
+    kernel<<<cus, kThreads, kLds, stream>>>(p);
     return hipGetLastError();
 }
 
@@ -423,7 +406,7 @@ hipError_t launch(const Fp8GemmParams& g, hipStream_t stream) {
 hipError_t launch_fp8_gemm_large(const Fp8GemmParams& g, bool trans, bool e5m2, hipStream_t stream) {
     auto pick = [&](auto t, auto f) {
         constexpr bool kT = decltype(t)::value, kF = decltype(f)::value;
-        return g.e8m0 ? launch<Large, kT, kF, true>(g, stream) : launch<Large, kT, kF, false>(g, stream);
+        return g.e8m0 ? launch<kT, kF, true>(g, stream) : launch<kT, kF, false>(g, stream);
     };
     constexpr auto yes = std::true_type{};
     constexpr auto no = std::false_type{};

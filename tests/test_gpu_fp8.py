@@ -208,6 +208,32 @@ def test_large_products_exact(T, N, R, fmt, st, trans):
         assert (y[T] == 7.0).all()
 
 
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("T,N,R", [(1000, 4000, 400), (990, 4096, 4176), (64, 4096, 4096), (300, 512, 8240), (40, 1008, 16400),
+                                   (512, 4096, 5008), (128, 4096, 16400), (300, 640, 2048), (9, 4096, 2064), (3, 16400, 1040),
+                                   (16, 1040, 8208), (1, 4096, 4096)])
+def test_product_forms_exact(T, N, R, trans, st):
+    """Tiles of 64 and of 128, whole and split reductions, more blocks than a table of scales holds, few rows.
+    Codes to 4 and two scales of 1/2 to 2: products are whole quarters up to 64, so every sum is at most 2^20.01
+    and a multiple of 1/4, exact in fp32."""
+    step("product forms", T, N, R, trans, st)
+    a, w = int_codes(T + R, T, R).cuda(), int_codes(N + 1, R if trans else N, N if trans else R).cuda()
+    sa = pow2_scales(3, groups(R), T, -1, 1).to(st).cuda()
+    sw = pow2_scales(4, groups(w.shape[0]), groups(w.shape[1]), -1, 1).to(st).cuda()
+    av = a.double() * sa.double().t().repeat_interleave(128, 1)[:, :R]
+    wv = w.double() * sw.double().repeat_interleave(128, 0)[:w.shape[0]].repeat_interleave(128, 1)[:, :w.shape[1]]
+    ref = av @ (wv if trans else wv.t().contiguous())
+    call, size = (rtq.fp8_dgrad, rtq.fp8_dgrad_workspace) if trans else (rtq.fp8_qgemm, rtq.fp8_qgemm_workspace)
+    need = size(T, *((R, N) if trans else (N, R)))
+    for dtype in (F32, BF16):
+        y = torch.full((T + 1, N), 7.0, dtype=dtype, device="cuda")
+        ws = torch.zeros(need + 64, dtype=torch.uint8, device="cuda")
+        call(a, sa, w, sw, y[:T], workspace=ws[:need] if need else ws)
+        assert torch.equal(y[:T].double(), ref.float().to(dtype).double())
+        assert (y[T] == 7.0).all() and not ws[need:].any()      # nothing past the size asked for
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 300, 2048), (16, 512, 4096), (100, 333, 1040), (300, 512, 2064)])
 def test_product_general(T, N, K):
     """General fp32 scales and codes over the whole range."""
@@ -541,6 +567,44 @@ def test_rotation_cancels_between_quantised_operands():
     y = torch.empty(T, N, dtype=BF16, device="cuda")
     rtq.fp8_linear(xr, *_quantised(wr), y)
     assert rel(y, x.cpu().double() @ w.cpu().double().T) < 0.06
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N,K", [(1024, 1920, 1920), (1025, 1920, 2000), (1090, 2000, 1920), (2500, 2048, 2048), (2113, 1928, 2032)])
+def test_wgrad_many_tokens_exact(T, N, K, st):
+    """More tokens in one part than a table of scales holds, one stage and many past it."""
+    step("wgrad many tokens", T, N, K, st)
+    dy = torch.randint(-4, 5, (T, N), generator=gen(T)).to(BF16).cuda()
+    x, sx = int_codes(K, T, K).cuda(), pow2_scales(9, groups(K), T, -2, 2).to(st).cuda()
+    ref = dy.double().t().contiguous() @ (x.double() * sx.double().t().repeat_interleave(128, 1)[:, :K])
+    dw = torch.full((N + 1, K), 7.0, device="cuda")
+    rtq.fp8_wgrad(dy, x, sx, dw[:N])
+    assert torch.equal(dw[:N].double(), ref) and (dw[N] == 7.0).all()
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N,K", [(130, 528, 1040), (391, 1000, 1936), (33, 2064, 272), (512, 256, 2048)])
+def test_direct_layer_keeps_the_codes(T, N, K, st):
+    """The layers that quantise on the way, at more than 16 rows: what they keep is what the quantiser writes, and
+    the gradient's two code types."""
+    step("direct layer", T, N, K, st)
+    x = rows_like(T * K, T, K).cuda()
+    wq, ws = _quantised((torch.randn(N, K, generator=gen(N)) * 0.05).bfloat16().cuda(), st)
+    codes, scale = empty_rows(T, K, st=st)
+    rtq.fp8_quantize(x, codes, scale)
+    c2, s2 = empty_rows(T, K, st=st)
+    y = torch.empty(T, N, device="cuda")
+    rtq.fp8_linear(x, wq, ws, y, x_codes=c2, x_scale=s2)
+    assert same(c2, codes) and same(s2.float(), scale.float())
+    assert rel(y, row_values(codes, scale) @ block_values(wq, ws).T) <= GENERAL
+    g = rows_like(7, T, (N + 15) // 16 * 16).cuda()[:, :N // 16 * 16].contiguous()
+    wg, wgs = _quantised((torch.randn(g.shape[1], K, generator=gen(N)) * 0.05).bfloat16().cuda(), st)
+    for fmt in (E4M3, E5M2):
+        gc, gs = empty_rows(T, g.shape[1], fmt, st)
+        rtq.fp8_quantize(g, gc, gs)
+        dx = torch.empty(T, K, device="cuda")
+        rtq.fp8_linear_dgrad(g, wg, wgs, dx, grad_dtype=fmt)
+        assert rel(dx, row_values(gc, gs) @ block_values(wg, wgs)) <= GENERAL
 
 
 def test_captured_step_replays():
