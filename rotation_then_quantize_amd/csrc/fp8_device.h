@@ -8,6 +8,15 @@
 namespace rtq {
 namespace fp8 {
 
+// A launch of more work-items than a grid's first dimension holds (2^32) goes over two; each kernel returns in
+// the workgroups past its last.  The first dimension is a multiple of 8, the number of XCDs.
+inline dim3 grid_of(int64_t blocks) {
+    constexpr int64_t kMost = 1 << 22;
+    return blocks <= kMost ? dim3(static_cast<unsigned>(blocks)) : dim3(kMost, static_cast<unsigned>((blocks + kMost - 1) / kMost));
+}
+__device__ __forceinline__ int64_t block_index() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
+
+
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));

@@ -55,7 +55,7 @@ fp8_gemm_kernel(Fp8GemmParams p) {
 
     // 8 contiguous ranges of tiles and their parts, one per XCD (workgroup b runs on XCD b % 8)
     const int total = p.tiles_m * p.tiles_n * p.split, per = (total + 7) / 8;
-    const int local = static_cast<int>(blockIdx.x) / 8, lin = static_cast<int>(blockIdx.x) % 8 * per + local;
+    const int b = static_cast<int>(block_index()), local = b / 8, lin = b % 8 * per + local;
     if (local >= per || lin >= total) return;
     const int tile = lin / p.split, part = lin % p.split;
     const int64_t m0 = static_cast<int64_t>(tile % p.tiles_m) * BM, n0 = static_cast<int64_t>(tile / p.tiles_m) * BN;
@@ -277,7 +277,7 @@ hipError_t launch_tiles(Fp8GemmParams p, const Fp8GemmArgs& g, int split, hipStr
     if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(split) * g.M * g.N * sizeof(float)) p.split = 1;
     if (p.split > 1) p.y = g.workspace;
     const int64_t total = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.split;
-    kernel<<<static_cast<unsigned>((total + 7) / 8 * 8), threads, lds, stream>>>(p);
+    kernel<<<grid_of((total + 7) / 8 * 8), threads, lds, stream>>>(p);
     e = hipGetLastError();
     if (e != hipSuccess || p.split == 1) return e;
     const int64_t n = g.M * g.N;

@@ -92,7 +92,7 @@ template <bool kBF16, bool kE5M2, int kAct, int kY, int kRows>
 __global__ void __launch_bounds__(kThreads)
 fp8_rows_kernel(const void* __restrict__ x, int64_t rows, int d, int col_waves, RowsOut o) {
     const int lane = threadIdx.x & 63;
-    const int64_t wave = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
+    const int64_t wave = block_index() * (kThreads / 64) + (threadIdx.x >> 6);
     const int64_t r0 = wave / col_waves * kRows;
     const int c = static_cast<int>(wave % col_waves) * kWaveCols + lane * 8;
     if (r0 >= rows) return;
@@ -137,23 +137,24 @@ fp8_rows_kernel(const void* __restrict__ x, int64_t rows, int d, int col_waves, 
     }
 }
 
-// Rows per wave: 16 fill the run of scales a wave stores (64 bytes of fp32), but leave few waves
-// when there are few rows; then 4, or 1.
+// Rows per wave: two loads in flight for each lane, and many waves (4608 rows, us:
+//                            1        2        4        8        16
+//   quantise 4096 columns   14.2     13.3     13.4     14.2     16.4
+//   quantise 16384          45.1     40.9     41.9     45.2     47.2
+//   GELU (tanh) 16384       69.1     68.2     69.8     77.5     84.5
+// at 40.9 and 68.2 us 5.5 TB/s: more rows fill a cache line of scales, but even out worse over the CUs).  One
+// where there are fewer waves than the CUs have SIMDs for twice over.
 template <bool kBF16, bool kE5M2, int kAct, int kY>
 hipError_t launch_rows(const void* x, int64_t rows, int d, const RowsOut& o, hipStream_t stream) {
     const int col_waves = (d + kWaveCols - 1) / kWaveCols;
-    auto blocks = [&](int per) {
-        return static_cast<unsigned>(((rows + per - 1) / per * col_waves + kThreads / 64 - 1) / (kThreads / 64));
+    auto go = [&](auto per) {
+        constexpr int kRows = decltype(per)::value;
+        const int64_t waves = (rows + kRows - 1) / kRows * col_waves;
+        fp8_rows_kernel<kBF16, kE5M2, kAct, kY, kRows>
+            <<<grid_of((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(x, rows, d, col_waves, o);
+        return hipGetLastError();
     };
-    const int64_t units = rows * col_waves;
-    const dim3 block(kThreads);
-    if (units >= 16 * 2048)
-        fp8_rows_kernel<kBF16, kE5M2, kAct, kY, 16><<<blocks(16), block, 0, stream>>>(x, rows, d, col_waves, o);
-    else if (units >= 4 * 1024)
-        fp8_rows_kernel<kBF16, kE5M2, kAct, kY, 4><<<blocks(4), block, 0, stream>>>(x, rows, d, col_waves, o);
-    else
-        fp8_rows_kernel<kBF16, kE5M2, kAct, kY, 1><<<blocks(1), block, 0, stream>>>(x, rows, d, col_waves, o);
-    return hipGetLastError();
+    return rows * col_waves >= 2048 ? go(std::integral_constant<int, 2>{}) : go(std::integral_constant<int, 1>{});
 }
 
 // A workgroup takes one 128 x 128 block of a weight: 16 lanes a row, 8 elements a lane, 16 rows a pass.
@@ -164,8 +165,9 @@ fp8_blocks_kernel(const void* __restrict__ x, int64_t rows, int d, void* __restr
     constexpr int kPass = kThreads / 16;
     __shared__ uint32_t s_max[kThreads / 64];
     const int groups = (d + kFp8Block - 1) / kFp8Block;
-    const int64_t br = blockIdx.x / groups;
-    const int bc = static_cast<int>(blockIdx.x % groups);
+    const int64_t br = block_index() / groups;
+    const int bc = static_cast<int>(block_index() % groups);
+    if (br * kFp8Block >= rows) return;
     const int64_t r0 = br * kFp8Block + threadIdx.x / 16;
     const int c = bc * kFp8Block + (threadIdx.x % 16) * 8;
     Row8<kBF16> in8[kFp8Block / kPass];
@@ -204,14 +206,15 @@ fp8_blocks_kernel(const void* __restrict__ x, int64_t rows, int d, void* __restr
     if (threadIdx.x == 0) store_scale(scale, e8m0, br * groups + bc, e);
 }
 
-// Elementwise passes over codes: a thread takes 8 elements of kElemRows rows.
-constexpr int kElemRows = 4;
+// Elementwise passes over codes: a thread takes 8 elements of kElemRows rows (the gradient of GELU at 2304 x 4096:
+// 11.1 us with one, 12.4 with two, 13.5 with four; at 4608 x 16384 73.3, 71.6, 73.5).
+constexpr int kElemRows = 2;
 
 template <bool kE5M2, bool kBF16, bool kE8M0>
 __global__ void __launch_bounds__(kThreads)
 fp8_dequant_kernel(const uint8_t* __restrict__ codes, const void* __restrict__ scale, bool blocks,
                    int64_t rows, int d, int64_t units, void* __restrict__ y) {
-    const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t u = block_index() * kThreads + threadIdx.x;
     if (u >= units) return;
     const int per_row = d / 8;
     const int c = static_cast<int>(u % per_row) * 8;
@@ -243,7 +246,7 @@ template <bool kBF16, int kAct, bool kE8M0>
 __global__ void __launch_bounds__(kThreads)
 act_backward_kernel(const void* dy, const uint8_t* __restrict__ codes, const void* __restrict__ scale,
                     int64_t rows, int d, int64_t units, void* dh) {   // dh may be dy
-    const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t u = block_index() * kThreads + threadIdx.x;
     if (u >= units) return;
     const int per_row = d / 8;
     const int c = static_cast<int>(u % per_row) * 8;
@@ -274,7 +277,7 @@ act_backward_kernel(const void* dy, const uint8_t* __restrict__ codes, const voi
 }
 
 int64_t elem_units(int64_t rows, int d) { return (rows + kElemRows - 1) / kElemRows * (d / 8); }
-unsigned elem_blocks(int64_t units) { return static_cast<unsigned>((units + kThreads - 1) / kThreads); }
+dim3 elem_blocks(int64_t units) { return grid_of((units + kThreads - 1) / kThreads); }
 
 template <bool kBF16, int kAct>
 hipError_t act_forward(const ActForwardArgs& a, hipStream_t stream) {
@@ -306,7 +309,7 @@ hipError_t launch_fp8_quantize_rows(const Fp8QuantArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_fp8_quantize_blocks(const Fp8QuantArgs& a, hipStream_t stream) {
-    const unsigned grid = static_cast<unsigned>(fp8_groups(a.rows) * fp8_groups(a.d));
+    const dim3 grid = grid_of(fp8_groups(a.rows) * fp8_groups(a.d));
     auto go = [&](auto kernel) {
         kernel<<<grid, kThreads, 0, stream>>>(a.x, a.rows, a.d, a.codes, a.scale, a.e8m0);
         return hipGetLastError();

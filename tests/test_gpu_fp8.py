@@ -86,7 +86,7 @@ def test_quantise_rows(T, d, dtype, st, fmt):
 
 @pytest.mark.parametrize("T,d", [(8300, 2064), (4300, 512)])
 def test_quantise_rows_many(T, d):
-    """The variants for many rows (16 and 4 rows a wave) against the one-row form of the same rows."""
+    """Many rows (two a wave) against the one-row form of the same rows."""
     step("quantise rows", T, d)
     x = rows_like(5, T, d).cuda()
     codes, scale = empty_rows(T, d)
@@ -681,3 +681,30 @@ def test_offsets_past_32_bits():
     rtq.fp8_qgemm(a, sa, w, sw, x)
     assert same(x[-3:], (a[-3:].cpu().double() @ w.cpu().double().T).bfloat16())
     assert not x[:-3].any()
+
+
+def test_launches_of_more_than_2_32_work_items():
+    """More rows than one dimension of a launch holds threads for."""
+    torch.cuda.empty_cache()
+    T, d = (1 << 29) + 37, 16
+    step("many narrow rows")
+    x = torch.zeros(T, d, dtype=BF16, device="cuda")
+    tail = rows_like(3, 5, d)
+    x[-5:] = tail.cuda()
+    codes, scale = empty_rows(T, d)
+    codes.view(torch.uint8).fill_(9)
+    rtq.fp8_quantize(x, codes, scale)
+    q, s = quantise(tail, E4M3)
+    assert same(codes[-5:], q) and same(scale[:, -5:], s)
+    assert not codes[:-5].view(torch.uint8).any() and (scale[:, :-5] == 1.0).all()
+    del x, scale
+    step("many narrow tiles")
+    T = (1 << 30) + 70
+    codes = torch.zeros(T, d, dtype=torch.uint8, device="cuda").view(E4M3)
+    a = int_codes(1, 5, d)
+    codes[-5:] = a.cuda()
+    w, sw = int_codes(2, 8, d), torch.ones(1, 1, device="cuda")
+    y = torch.full((T, 8), 7.0, dtype=BF16, device="cuda")
+    rtq.fp8_qgemm(codes, torch.ones(1, T, device="cuda"), w.cuda(), sw, y)
+    assert same(y[-5:], (a.double() @ w.double().T).bfloat16())
+    assert not y[:-5].any()
