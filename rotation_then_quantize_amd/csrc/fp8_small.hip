@@ -234,7 +234,7 @@ fp8_small_kernel(SmallParams sp) {
     // The wave's blocks: wave + 8 j, j over turns from a place of the workgroup's own (rows a power of two
     // apart share memory channels: workgroups at the same place of their rows would crowd them).  Past the
     // last turn a unit is all zeros.
-    const int turns = (blocks + kWaves - 1) / kWaves, start = local % turns;
+    const int turns = (blocks + kWaves - 1) / kWaves, start = static_cast<int>(blockIdx.x) % turns;
     auto block = [&](int t) {
         const int j = t + start;
         return t < turns ? wave + kWaves * (j < turns ? j : j - turns) : blocks;
