@@ -14,8 +14,9 @@
 // scales where they are kept.
 //
 // A few tokens (kTT = 1) are bound by the weights' bytes.  More columns per workgroup and few units in flight
-// stream best (16384 x 4096 weights: 16.3 us with 64 columns and one unit of 8 KB a wave beside the one in
-// use, 17.9 us with two; 25 us with 32 columns, 29.6 us with 16).  Small outputs are bound by latency: one
+// stream best (16384 x 4096 weights: 15.0 us, 4.5 TB/s, with 64 columns and one unit of 8 KB a wave beside
+// the one in use; when all XCDs began at the same place of their rows 16.3 so, 17.9 with two units, 25 with 32
+// columns, 29.6 with 16).  Small outputs are bound by latency: one
 // launch, one chain of loads, products and sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -231,9 +232,10 @@ fp8_small_kernel(SmallParams sp) {
         }
         if constexpr (kTrans) lds_done();   // the weights are in registers before the slot is filled again
     };
-    // The wave's blocks: wave + 8 j, j over turns from a place of the workgroup's own (rows a power of two
-    // apart share memory channels: workgroups at the same place of their rows would crowd them).  Past the
-    // last turn a unit is all zeros.
+    // The wave's blocks: wave + 8 j, j over turns from a place of the workgroup's own: rows a power of two
+    // apart share memory channels, and workgroups at the same place of their rows would crowd them (13 x 16384,
+    // 4096 columns, product alone: 16.5 us; 22 with the same place in all XCDs).  Past the last turn a unit is
+    // all zeros.
     const int turns = (blocks + kWaves - 1) / kWaves, start = static_cast<int>(blockIdx.x) % turns;
     auto block = [&](int t) {
         const int j = t + start;
@@ -325,8 +327,8 @@ bool fp8_small_takes(int64_t M, int64_t N, int R, bool trans) {
     return fits(M, N, R);
 }
 // Every workgroup quantises its rows again: of few tokens, beyond about 2^16 elements that takes longer than
-// a launch of its own (13 x 16384, 4096 columns: 25.8 us so, 23 us with the quantiser's launch; 16 x 4096,
-// 16384 columns: 19.0 and 20 us).
+// a launch of its own (4096 columns, 13 x 16384: 24.8 us so, 20.7 with the quantiser's launch, 5 x 16384: 22.8
+// and 18.1; 16384 columns, 16 x 4096: 17.4 and 20).
 bool fp8_small_linear_takes(int64_t M, int64_t N, int R, bool trans) {
     return fp8_small_takes(M, N, R, trans) && (M > 16 || M * R <= 65536);
 }
