@@ -304,7 +304,8 @@ size_t rtq_rotated_qlinear_asym_workspace(int64_t T, int32_t d);
  *   - blocks (weights [N][K]): one scale for each 128 x 128 block, the last ones possibly smaller.
  *     Stored row-major: scale[ceil(N / 128)][ceil(K / 128)].
  *   - scales are F32 (any value; non-finite ones spread as in fp32 arithmetic) or E8M0, one type for
- *     both operands of a product.  Scale arrays are 16-byte aligned like every device pointer here.
+ *     both operands of a product.  The product of the two scales of a block must itself be an fp32 number
+ *     (below 2^128).  Scale arrays are 16-byte aligned like every device pointer here.
  *   - The quantiser's rule for a block: with m its largest finite magnitude, the scale is the smallest
  *     power of two s >= 2^-120 with m <= 448 s (E4M3) or m <= 57344 s (E5M2), and 1 when m = 0; a code
  *     is x / s (exact) rounded to nearest, ties to even.  NaN stays NaN; an infinity becomes NaN in

@@ -271,6 +271,30 @@ def test_product_spreads_non_finite_values_only_along_their_row_and_column():
     assert same(y[keep][:, cols], clean[keep][:, cols])
 
 
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("T,N,R", [(5, 208, 528), (70, 208, 528), (200, 4096, 1040), (1000, 4000, 400), (4100, 1488, 272)])
+def test_not_a_number_scales(T, N, R, trans, st):
+    """In every form: one row's and one weight block's scale."""
+    step("NaN scales", T, N, R, trans, st)
+    a, w = int_codes(1, T, R).cuda(), int_codes(2, R if trans else N, N if trans else R).cuda()
+    sa = torch.ones(groups(R), T, device="cuda").to(st)
+    sw = torch.ones(groups(w.shape[0]), groups(w.shape[1]), device="cuda").to(st)
+    call = rtq.fp8_dgrad if trans else rtq.fp8_qgemm
+    clean = torch.empty(T, N, device="cuda")
+    call(a, sa, w, sw, clean)
+    for s, at in ((sa, (1, 3)), (sw, (1, 0) if trans else (0, 1))):     # the second block of the reduction
+        if st == E8M0:
+            s.view(torch.uint8)[at] = 255
+        else:
+            s[at] = float("nan")
+    y = torch.empty(T, N, device="cuda")
+    call(a, sa, w, sw, y)
+    assert torch.isnan(y[3]).all() and torch.isnan(y[:, :128]).all()
+    rest = [t for t in range(T) if t != 3]
+    assert torch.equal(y[rest][:, 128:], clean[rest][:, 128:])
+
+
 def test_product_extreme_scales():
     """Scales at both ends of their range, zero and the smallest E8M0 byte."""
     step("product extreme scales")
