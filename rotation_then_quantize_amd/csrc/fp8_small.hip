@@ -296,9 +296,11 @@ hipError_t launch_form(const SmallParams& p, hipStream_t stream) {
         if ((p.g.M + 31) / 32 * ((p.g.N + 63) / 64) >= cus / 2) return launch_tile<2, 4, kX, kE5M2, kE8M0, kTrans>(p, stream);
         return launch_tile<2, 2, kX, kE5M2, kE8M0, kTrans>(p, stream);
     }
-    // columns per workgroup: as many as leave a workgroup for each CU (each repeats the activations' part)
-    if (tiles >= 4 * cus) return launch_tile<1, 4, kX, kE5M2, kE8M0, kTrans>(p, stream);
-    if (tiles >= 2 * cus) return launch_tile<1, 2, kX, kE5M2, kE8M0, kTrans>(p, stream);
+    // Columns per workgroup: as few as leave no CU with two (each repeats the activations' part, and a CU with two
+    // takes twice as long as the others: layers of one token, 4096 long, 4608 columns 8.5 us with 32, 10.5 with
+    // 16; 9216 columns 11.6 with 64, 14.8 with 32).
+    if (tiles > 2 * cus) return launch_tile<1, 4, kX, kE5M2, kE8M0, kTrans>(p, stream);
+    if (tiles > cus) return launch_tile<1, 2, kX, kE5M2, kE8M0, kTrans>(p, stream);
     return launch_tile<1, 1, kX, kE5M2, kE8M0, kTrans>(p, stream);
 }
 
