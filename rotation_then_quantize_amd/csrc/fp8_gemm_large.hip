@@ -20,6 +20,10 @@
 //
 // Persistent: one workgroup per CU walks its tiles.  The stages of all its tiles are one stream: the last
 // stages of a tile load the first ones of the next, and its epilogue runs with those in LDS.
+//
+// 4608 x 4096, 16384 columns: fp32 scales 284 us (2180 TFLOP/s), E8M0 250-263 us (2350-2470 TFLOP/s).  The
+// matrix instructions are busy 53-58% of the time, at 1.7-1.9 GHz: the card's power sets the clock, and fewer
+// clocks in the same kernel (no bank conflicts, 3% fewer) did not shorten it.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -394,7 +398,8 @@ hipError_t launch(const Fp8GemmParams& g, hipStream_t stream) {
     p.g.tiles_m = static_cast<int>((g.M + kTileM - 1) / kTileM);
     p.g.tiles_n = static_cast<int>((g.N + BN - 1) / BN);
     const int cus = std::max(kXcds, device_cu_count() / kXcds * kXcds);
-    // whole rounds of whole tiles; a remainder that fills at most half a round goes as halves of 128 rows
+    // whole rounds of whole tiles; a remainder that fills at most half a round goes as halves of 128 rows (4608 x
+    // 4096 x 4096, a round and an eighth: 90 us, 105 without)
     const int total = p.g.tiles_m * p.g.tiles_n, rest = total % cus;
     p.full = rest > 0 && rest <= cus / 2 ? total - rest : total;
     kernel<<<cus, kThreads, kLds, stream>>>(p);
