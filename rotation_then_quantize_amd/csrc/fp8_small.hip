@@ -159,11 +159,11 @@ fp8_small_kernel(SmallParams sp) {
             }
         }
         const uint32_t x0 = o0 == kOob ? kOob : xoff + o0 * kElem, x1 = o1 == kOob ? kOob : xoff + o1 * kElem;
-        const int kc = min(kb, blocks - 1);   // past the end everything else is zero
+        const int kc = min(kb, blocks - 1), some = kb < blocks ? kScaleSize : 0;   // past the end all reads as zeros
         const __amdgpu_buffer_rsrc_t rsa = resource(static_cast<const uint8_t*>(p.a_scale) + (static_cast<int64_t>(kc) * p.M + m0) * kScaleSize,
-                                                    rows * kScaleSize);
+                                                    rows * some);
         const __amdgpu_buffer_rsrc_t rsw = resource(static_cast<const uint8_t*>(p.w_scale) +
-                                                        (n0 / BK * p.w_out_stride + kc * p.w_red_stride) * kScaleSize, kScaleSize);
+                                                        (n0 / BK * p.w_out_stride + kc * p.w_red_stride) * kScaleSize, some);
 #pragma unroll
         for (int t = 0; t < kTT; ++t) {
             const uint32_t row = static_cast<uint32_t>(16 * t) * static_cast<uint32_t>(R * kElem);

@@ -82,10 +82,14 @@ fp8_wgrad_kernel(WgradParams p) {
     };
     constexpr int kLoads = 3;
     const int64_t xs = static_cast<int64_t>(k0 / kFp8Block) * p.T;
-    auto fill = [&](int s) {   // the scales of the stages s ..
+    auto fill = [&](int s) {   // the scales of the stages s .., zeros past the last token (an infinite one times the
+                               // zeros there would be none)
 #pragma unroll
-        for (int e = tid; e < kTable + 2 * BT; e += kThreads)
-            table[e] = load_scale<kE8M0>(p.x_scale, xs + min<int64_t>((s0 + s) * BT + e, p.T - 1));
+        for (int e = tid; e < kTable + 2 * BT; e += kThreads) {
+            const int64_t t = (s0 + s) * BT + e;
+            const float v = load_scale<kE8M0>(p.x_scale, xs + min<int64_t>(t, p.T - 1));
+            table[e] = t < p.T ? v : 0.0f;
+        }
     };
     const int x_row = tid >> 3;
     v4i q;      // 16 codes a thread

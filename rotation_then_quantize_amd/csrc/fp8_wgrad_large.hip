@@ -104,9 +104,12 @@ __device__ __forceinline__ void large_tiles(const WgradParams& p, uint8_t* lds, 
     const uint32_t x_put = static_cast<uint32_t>(kOp + x_row * kRow + (((tid & 15) ^ (x_row & 7)) << 5));
     v4i x_codes[2];
     uint32_t x_scale[2];
+    int x_rows = 0;   // tokens that there are among the stage's: past them the scale is taken as 0 (the last token's may be
+                      // infinite, and times the zeros there would be none)
     auto issue = [&](int slot) {   // the cursor's stage, and the cursor moves on
         const int64_t t0 = static_cast<int64_t>(c_t) * BT;
         const int rows = static_cast<int>(min<int64_t>(BT, p.T - t0));
+        x_rows = rows;
         const uint32_t dy_bytes = (static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.N) - static_cast<uint32_t>(c_n0)) * 2u;
         const uint32_t x_bytes = static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.K) - static_cast<uint32_t>(c_k0);
         const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
@@ -130,7 +133,8 @@ __device__ __forceinline__ void large_tiles(const WgradParams& p, uint8_t* lds, 
     auto decode = [&](int slot) {   // the codes that issue loaded last
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float s = kE8M0 ? e8m0_value(x_scale[h]) : __uint_as_float(x_scale[h]);
+            const float raw = kE8M0 ? e8m0_value(x_scale[h]) : __uint_as_float(x_scale[h]);
+            const float s = x_row + 32 * h < x_rows ? raw : 0.0f;
             uint32_t w[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {

@@ -295,6 +295,29 @@ def test_not_a_number_scales(T, N, R, trans, st):
     assert torch.equal(y[rest][:, 128:], clean[rest][:, 128:])
 
 
+@pytest.mark.parametrize("T,N,R", [(5, 200, 144), (5, 200, 1040), (16, 4200, 400), (40, 200, 1040), (300, 200, 4112), (4100, 1488, 272)])
+def test_infinite_scale_of_the_last_block(T, N, R):
+    """Nothing that fills a block, a stage or a turn meets the infinite scale: sums of positive products stay infinite."""
+    step("infinite scale", T, N, R)
+    a, w = torch.ones(T, R, device="cuda").to(E4M3), torch.ones(N, R, device="cuda").to(E4M3)
+    sa, sw = torch.ones(groups(R), T, device="cuda"), torch.ones(groups(N), groups(R), device="cuda")
+    sa[-1, T - 1] = float("inf")
+    y = torch.empty(T, N, device="cuda")
+    rtq.fp8_qgemm(a, sa, w, sw, y)
+    assert (y[T - 1] == float("inf")).all() and (y[:T - 1] == float(R)).all()
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 16, 32), (65, 64, 272), (130, 64, 144), (333, 4096, 4112)])
+def test_wgrad_infinite_scale_of_the_last_token(T, N, K):
+    step("wgrad infinite scale", T, N, K)
+    dy, x = torch.ones(T, N, dtype=BF16, device="cuda"), torch.ones(T, K, device="cuda").to(E4M3)
+    sx = torch.ones(groups(K), T, device="cuda")
+    sx[0, T - 1] = float("inf")
+    dw = torch.empty(N, K, device="cuda")
+    rtq.fp8_wgrad(dy, x, sx, dw)
+    assert (dw[:, :128] == float("inf")).all() and (dw[:, 128:] == float(T)).all()
+
+
 def test_product_extreme_scales():
     """Scales at both ends of their range, zero and the smallest E8M0 byte."""
     step("product extreme scales")
