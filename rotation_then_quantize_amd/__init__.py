@@ -404,10 +404,12 @@ def _operand(t, name: str, types: dict, shape=None, like=None) -> int:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {'two dimensions' if shape is None else tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if like is not None and t.get_device() != like.get_device():
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if like is None or like is t:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+    elif t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be a GPU tensor" if not t.is_cuda else
+                         f"{name} is on {t.device}, expected {like.device}")
     return code
 
 
@@ -421,7 +423,7 @@ def _call(like, stream, fn, *args):
         handle = stream.cuda_stream
     else:
         raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -433,9 +435,13 @@ def _call(like, stream, fn, *args):
 def _workspace(given, like, stream, query, *sizes):
     """The caller's workspace, or a temporary one of the queried size for the call's stream."""
     if given is None:
-        with _torch().cuda.device(like.device):
+        torch = _torch()
+        if like.get_device() == torch._C._cuda_getDevice():
             need = query(*sizes)
-        return _stream_local_workspace(_torch(), need, like.device, stream)
+        else:
+            with torch.cuda.device(like.device):
+                need = query(*sizes)
+        return _stream_local_workspace(torch, need, like.device, stream)
     if given.get_device() != like.get_device():
         raise ValueError(f"workspace is on {given.device}, expected {like.device}")
     if not given.is_contiguous():
