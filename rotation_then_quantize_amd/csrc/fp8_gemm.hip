@@ -212,24 +212,23 @@ fp8_gemm_kernel(Fp8GemmParams p) {
 // y = the sum of the split partials, in order (the result does not depend on which finished first).
 __global__ void __launch_bounds__(256)
 fp8_reduce_kernel(const float* __restrict__ part, int split, int64_t n, void* __restrict__ y, bool y_bf16) {
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (i >= n) return;
-    if (i + 4 <= n && n % 4 == 0) {
-        v4f s = *reinterpret_cast<const v4f*>(part + i);
-        for (int k = 1; k < split; ++k) s += *reinterpret_cast<const v4f*>(part + k * n + i);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * 1024;
+    if (n % 4 == 0) {
+        const int64_t i = first + threadIdx.x * 4;
+        if (i >= n) return;
+        const v4f s = sum_parts<v4f>(part + i, split, n);
         if (y_bf16)
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + i) = uint2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
         else
             *reinterpret_cast<v4f*>(static_cast<float*>(y) + i) = s;
         return;
     }
-    for (int64_t e = i; e < min(i + 4, n); ++e) {
-        float s = part[e];
-        for (int k = 1; k < split; ++k) s += part[k * n + e];
+    for (int64_t i = first + threadIdx.x; i < min(first + 1024, n); i += 256) {
+        const float s = sum_parts<float>(part + i, split, n);
         if (y_bf16)
-            static_cast<uint16_t*>(y)[e] = static_cast<uint16_t>(pack_bf16x2(s, 0.0f));
+            static_cast<uint16_t*>(y)[i] = static_cast<uint16_t>(pack_bf16x2(s, 0.0f));
         else
-            static_cast<float*>(y)[e] = s;
+            static_cast<float*>(y)[i] = s;
     }
 }
 
@@ -247,9 +246,11 @@ struct Plan {
 //   256 x 256  32.5        33.1     33.1     33.4     33.5     33.4     34.8     38.9
 // A tile costs its chain of stages as long as each CU has one (128: one workgroup per CU, 64: two), so the
 // largest tile whose workgroups fit at once is taken.  Splitting the reduction shortens the chain of the 64
-// x 64 tiles: in as many parts as give each CU one workgroup (M = 64: 13.0 to 11.7 us in two, M = 128: 13.4
-// to 12.7 in two), or two where the parts stay long (M = 128, reduction of 16384: 45.0, in two 28.2, in four
-// 22.9; of 4096: 12.7, 12.8); below 12 blocks a part the second kernel costs what it saves.
+// x 64 tiles: in as many parts as give each CU one workgroup (64 x 1024 outputs, 4096 long: 12.3 us whole, 10.1
+// in two parts, 8.0 in five; M = 128: 13.4 and 12.4 in two), or two where the parts stay long (M = 128,
+// reduction of 16384: 45.0, in two 28.2, in four 22.9; of 4096: 12.4, 12.7).  The second kernel loads four
+// parts beside the first at once, so five of them cost little more than two (8656 long, 23 x 697: 11.7 in five
+// parts, 12.9 in eleven; 2064 long, 64 x 512: 8.5 whole, 9.4 in two).
 Plan plan(int64_t M, int64_t N, int R, bool trans) {
     if (fp8_small_takes(M, N, R, trans)) return {kSmall, 1};
     auto tiles = [&](int64_t t) { return (M + t - 1) / t * ((N + t - 1) / t); };
@@ -259,7 +260,8 @@ Plan plan(int64_t M, int64_t N, int R, bool trans) {
         if (tiles(128) <= cus) return {kTile128, 1};
         if (blocks > 1) return {kLarge, 1};   // (its loads run two stages ahead)
     }
-    const int64_t one = std::min<int64_t>(cus / tiles(64), blocks / 12), two = std::min<int64_t>(2 * cus / tiles(64), blocks / 32);
+    const int parts = blocks >= 30 ? std::max(5, blocks / 12) : blocks / 12;
+    const int64_t one = std::min<int64_t>(cus / tiles(64), parts), two = std::min<int64_t>(2 * cus / tiles(64), blocks / 32);
     return {kTile64, static_cast<int>(std::clamp<int64_t>(std::max(one, two), 1, 16))};
 }
 

@@ -205,9 +205,7 @@ __global__ void __launch_bounds__(256)
 wgrad_reduce_kernel(const float* __restrict__ part, int split, int64_t n, void* __restrict__ dw, bool bf16, bool accumulate) {
     const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
     if (i >= n) return;   // n is a multiple of 16
-    v4f s = *reinterpret_cast<const v4f*>(part + i);
-    for (int k = 1; k < split; ++k) s += *reinterpret_cast<const v4f*>(part + k * n + i);
-    wgrad_put4(dw, bf16, accumulate, i, s);
+    wgrad_put4(dw, bf16, accumulate, i, sum_parts<v4f>(part + i, split, n));
 }
 
 int64_t tiles_of(int N, int K) { return static_cast<int64_t>((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile); }
