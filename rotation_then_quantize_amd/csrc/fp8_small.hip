@@ -328,11 +328,12 @@ bool fp8_small_takes(int64_t M, int64_t N, int R, bool trans) {
     if (M <= 16) return !trans || N * R <= int64_t{16} << 20;
     return fits(M, N, R);
 }
-// Every workgroup quantises its rows again: of few tokens, beyond about 2^16 elements that takes longer than
-// a launch of its own (4096 columns, 13 x 16384: 24.8 us so, 20.7 with the quantiser's launch, 5 x 16384: 22.8
-// and 18.1; 16384 columns, 16 x 4096: 17.4 and 20).
+// Every workgroup quantises its rows again: of few tokens, along a long reduction that takes longer than a launch
+// of its own, the sooner the fewer columns a workgroup has (4096 columns, 1 x 4096: 7.2 us so, 9.2 with the
+// quantiser's launch, 16 x 6144: 12.2 and 11.0, 1 x 8192: 11.2 and 10.0, 2 x 32768: 41.0 and 33.2; 64 columns a
+// workgroup, 16384 columns, 2 x 6144: 22.2 and 24.1, 28672 columns, 1 x 8192: 45.1 and 46.1).
 bool fp8_small_linear_takes(int64_t M, int64_t N, int R, bool trans) {
-    return fp8_small_takes(M, N, R, trans) && (M > 16 || M * R <= 65536);
+    return fp8_small_takes(M, N, R, trans) && (M > 16 || R <= ((N + 15) / 16 > 2 * device_cu_count() ? 8192 : 4096));
 }
 
 hipError_t launch_fp8_small(const fp8::Fp8GemmParams& g, bool trans, bool e5m2, hipStream_t stream) {
