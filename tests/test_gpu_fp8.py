@@ -654,6 +654,29 @@ def test_direct_layer_keeps_the_codes(T, N, K, st):
         assert rel(dx, row_values(gc, gs) @ block_values(wg, wgs)) <= GENERAL
 
 
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,out,R", [(3, 8208, 8192), (3, 304, 5008), (16, 4112, 4096), (7, 9216, 1040), (1, 8208, 1936), (16, 4624, 2064)])
+def test_few_row_layers_and_gradients(T, out, R, st):
+    """Both sides of the rules for few rows: quantised on the way or before, one to four tiles of columns, forward and
+    transposed, against the quantiser's codes."""
+    step("few rows", T, out, R, st)
+    x = rows_like(T + R, T, R).cuda()
+    for trans in (False, True):
+        w, ws = _quantised((torch.randn(*((R, out) if trans else (out, R)), generator=gen(out)) * 0.05).bfloat16().cuda(), st)
+        wv = block_values(w, ws)
+        for fmt in (E4M3, E5M2) if trans else (E4M3,):
+            codes, scale = empty_rows(T, R, fmt, st)
+            rtq.fp8_quantize(x, codes, scale)
+            for dtype in (F32, BF16):
+                y = torch.full((T + 1, out), 7.0, dtype=dtype, device="cuda")
+                if trans:
+                    rtq.fp8_linear_dgrad(x, w, ws, y[:T], grad_dtype=fmt)
+                else:
+                    rtq.fp8_linear(x, w, ws, y[:T])
+                assert rel(y[:T], row_values(codes, scale) @ (wv if trans else wv.T)) <= GENERAL + (HALF_BF16 if dtype == BF16 else 0.0)
+                assert (y[T] == 7.0).all()
+
+
 def test_captured_step_replays():
     """A captured training step, replayed with new inputs in its buffers and eager work between the replays."""
     step("captured step")
