@@ -778,3 +778,50 @@ def test_launches_of_more_than_2_32_work_items():
     rtq.fp8_qgemm(codes, torch.ones(1, T, device="cuda"), w.cuda(), sw, y)
     assert same(y[-5:], (a.double() @ w.double().T).bfloat16())
     assert not y[:-5].any()
+
+
+def before_nans(t):
+    """A copy of t on the GPU whose buffer goes on with 64 KB of NaNs."""
+    bits = t.contiguous().view(torch.uint8).flatten()
+    nan = {E4M3: 0x7f, E5M2: 0x7f, E8M0: 0xff, BF16: 0xff, F32: 0xff}[t.dtype]
+    buffer = torch.full((bits.numel() + (1 << 16),), nan, dtype=torch.uint8, device="cuda")
+    buffer[:bits.numel()] = bits.cuda()
+    return buffer[:bits.numel()].view(t.dtype).view(t.shape)
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("T,N,R", [(1, 16, 144), (5, 208, 528), (13, 4112, 1040), (16, 8208, 272), (40, 208, 1040), (70, 528, 4112),
+                                   (1000, 4000, 400), (4100, 1488, 272)])
+def test_products_of_operands_with_nans_behind_them(T, N, R, trans, st):
+    """Every form, the last block and tile ragged: what lies behind an operand does not reach the product."""
+    step("NaNs behind", T, N, R, trans, st)
+    a, w = int_codes(T + R, T, R), int_codes(N + 1, R if trans else N, N if trans else R)
+    sa = pow2_scales(3, groups(R), T, -1, 1).to(st)
+    sw = pow2_scales(4, groups(w.shape[0]), groups(w.shape[1]), -1, 1).to(st)
+    av, wv = row_values(a, sa).cuda(), block_values(w, sw).cuda()
+    ref = av @ (wv if trans else wv.t().contiguous())
+    y = torch.empty(T, N, device="cuda")
+    (rtq.fp8_dgrad if trans else rtq.fp8_qgemm)(*[before_nans(t) for t in (a, sa, w, sw)], y)
+    assert torch.equal(y.double(), ref)
+    x = torch.randint(-8, 9, (T, R), generator=gen(5)).to(BF16)      # whole numbers: exact codes, any scale
+    q, s = quantise(x, E4M3)
+    ref = row_values(q, s).cuda() @ (wv if trans else wv.t().contiguous())
+    for dtype in (BF16, F32):
+        if trans:
+            rtq.fp8_linear_dgrad(before_nans(x.to(dtype)), before_nans(w), before_nans(sw), y, grad_dtype=E4M3)
+        else:
+            rtq.fp8_linear(before_nans(x.to(dtype)), before_nans(w), before_nans(sw), y)
+        assert torch.equal(y.double(), ref)
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N,K", [(1, 8, 16), (77, 136, 272), (517, 264, 1040), (65, 2568, 2576), (333, 2600, 3600)])
+def test_wgrad_of_operands_with_nans_behind_them(T, N, K, st):
+    step("wgrad NaNs behind", T, N, K, st)
+    dy = torch.randint(-4, 5, (T, N), generator=gen(T)).to(BF16)
+    x, sx = int_codes(K, T, K), pow2_scales(9, groups(K), T, -2, 2).to(st)
+    ref = dy.cuda().double().t().contiguous() @ row_values(x, sx).cuda()
+    dw = torch.empty(N, K, device="cuda")
+    rtq.fp8_wgrad(*[before_nans(t) for t in (dy, x, sx)], dw)
+    assert torch.equal(dw.double(), ref)
