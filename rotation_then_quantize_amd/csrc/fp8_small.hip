@@ -176,9 +176,9 @@ fp8_small_kernel(SmallParams sp) {
         }
         u.sw = load_raw<kE8M0>(rsw, 0u);
         if constexpr (kTrans) {   // last: the wait below counts on it
-            // in 32 bits (at most 2^27), which scalar instructions compute
-            const int bytes = max(0, max(0, min(BK, R - kb * BK)) * N - n0);
-            const v4i rt = make_rsrc(p.w + static_cast<int64_t>(kc) * BK * N + n0, static_cast<uint32_t>(bytes));
+            const int64_t n_rows = max(0, min(BK, R - kb * BK));
+            const int64_t bytes = n_rows * N - n0;
+            const v4i rt = make_rsrc(p.w + static_cast<int64_t>(kc) * BK * N + n0, bytes > 0 ? static_cast<uint32_t>(bytes) : 0u);
 #pragma unroll
             for (int q = 0; q < kDma; ++q) {
                 const int row = q * (64 / kRT) + w_row;

@@ -108,7 +108,7 @@ __device__ __forceinline__ void large_tiles(const WgradParams& p, uint8_t* lds, 
                       // infinite, and times the zeros there would be none)
     auto issue = [&](int slot) {   // the cursor's stage, and the cursor moves on
         const int64_t t0 = static_cast<int64_t>(c_t) * BT;
-        const int rows = min(BT, static_cast<int>(p.T - t0));   // (T < 2^31: in 32 bits, by scalar instructions)
+        const int rows = static_cast<int>(min<int64_t>(BT, p.T - t0));
         x_rows = rows;
         const uint32_t dy_bytes = (static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.N) - static_cast<uint32_t>(c_n0)) * 2u;
         const uint32_t x_bytes = static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.K) - static_cast<uint32_t>(c_k0);
