@@ -29,11 +29,11 @@ __device__ __forceinline__ v4i make_rsrc(const void* base, uint32_t bytes) {
 }
 
 // 16 bytes per lane from buffer offset voff to LDS address lds_addr + 16 * lane.
-// The descriptor may just have been written by a vector instruction (make_rsrc's v_readfirstlane): a memory
-// instruction reads a scalar register right only five wait states after that, and the compiler, which inserts
-// them for its own loads, does not look into this string.
+// Wait states, which the hardware does not check and the compiler inserts for its own loads only: one between the
+// write of M0 and the load, and five between a vector instruction that wrote the descriptor (make_rsrc's
+// v_readfirstlane) and the load.
 __device__ __forceinline__ void load_to_lds(v4i rsrc, uint32_t voff, uint32_t lds_addr) {
-    asm volatile("s_nop 3\n\ts_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(static_cast<int>(lds_addr))), "v"(voff), "s"(rsrc)
                  : "memory", "m0");

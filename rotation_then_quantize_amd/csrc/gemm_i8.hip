@@ -91,9 +91,10 @@ __device__ __forceinline__ v4i make_rsrc(const void* base, uint32_t bytes) {
     return r;
 }
 
-// 16 bytes per lane from buffer offset voff to LDS address lds_addr + 16 * lane.
+// 16 bytes per lane from buffer offset voff to LDS address lds_addr + 16 * lane.  One wait state must pass between
+// the write of M0 and the load; the compiler inserts none within inline assembly.
 __device__ __forceinline__ void load_to_lds(v4i rsrc, uint32_t voff, uint32_t lds_addr) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(static_cast<int>(lds_addr))), "v"(voff), "s"(rsrc)
                  : "memory", "m0");
@@ -119,7 +120,7 @@ __device__ __forceinline__ void wait_vmcnt() {
 
 // 4 bytes per lane from buffer offset voff to LDS address lds_addr + 4 * lane.
 __device__ __forceinline__ void load_to_lds4(v4i rsrc, uint32_t voff, uint32_t lds_addr) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(static_cast<int>(lds_addr))), "v"(voff), "s"(rsrc)
                  : "memory", "m0");

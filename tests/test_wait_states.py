@@ -4,7 +4,8 @@ The compiler inserts them for the instructions it chooses, but does not look int
 
   - a scalar register written by a vector instruction (v_readfirstlane, v_cmp, ..) is read by a memory
     instruction no sooner than 5 wait states later: a buffer descriptor's size or a base address read too early is
-    the old one, and the access may leave its array.
+    the old one, and the access may leave its array;
+  - M0 is written at least 1 wait state before a load to LDS, which takes its LDS address from it.
 
 An instruction is one wait state, s_nop n is n + 1.  The listing of each kernel in the built library is followed
 backwards from every memory instruction, over branches."""
@@ -21,7 +22,7 @@ OBJDUMP = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm", "bin", 
 MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
 VCC = 106      # register number of vcc
 VMEM = ("buffer_", "global_", "flat_", "scratch_")
-VALU_TO_VMEM = 5
+VALU_TO_VMEM, M0_TO_LDS = 5, 1
 
 
 def code_objects(library):
@@ -51,7 +52,7 @@ def scalars(operand):
 
 
 class Instr:
-    __slots__ = ("text", "name", "waits", "valu_writes", "before")
+    __slots__ = ("text", "name", "waits", "valu_writes", "writes_m0", "before")
 
     def __init__(self, text):
         self.text = text
@@ -63,12 +64,17 @@ class Instr:
             self.valu_writes = scalars(operands[0])
             if len(operands) > 1 and re.search(r"_co_|div_scale|mad_[ui]64", self.name):
                 self.valu_writes = self.valu_writes | scalars(operands[1])
+        self.writes_m0 = self.name.startswith("s_") and bool(operands) and operands[0] == "m0" and not self.name.startswith("s_cmp")
         self.before = []      # indexes of the instructions that may run right before this one
 
     @property
     def scalar_reads(self):
         words = re.split(r"[,\s]+", self.text)[1:]
         return set().union(*(scalars(w) for w in words)) if words else set()
+
+    @property
+    def to_lds(self):
+        return self.name.startswith("buffer_load") and self.text.endswith(" lds") or "_load_lds_" in self.name
 
 
 LINE = re.compile(r"^\t(\S[^/]*?)\s*// ([0-9A-F]+):(?:.*<([^>+]+)(?:\+0x([0-9a-f]+))?>)?")
@@ -126,6 +132,9 @@ def hazards(listing):
             r = reached(code, i, VALU_TO_VMEM, lambda c: c.valu_writes & reads) if reads else None
             if r:
                 found.append(f"{name}: '{r[0].text}', {r[1]} wait states before '{instr.text}'")
+            r = reached(code, i, M0_TO_LDS, lambda c: c.writes_m0) if instr.to_lds else None
+            if r:
+                found.append(f"{name}: '{r[0].text}', {r[1]} wait states before '{instr.text}'")
     return found
 
 
@@ -133,7 +142,7 @@ def test_the_check_sees_what_it_looks_for():
     listing = """
 0000000000001000 <k>:
 	v_readfirstlane_b32 s6, v0                                 // 000000001000: 7E0C0500
-	s_mov_b32 s9, s3                                           // 000000001004: BE890003
+	s_mov_b32 m0, s9                                           // 000000001004: BEFC0009
 	buffer_load_dwordx4 v1, s[4:7], 0 offen lds                // 000000001008: E05D1000 80010001
 	v_cmp_gt_i32_e32 vcc, 1, v2                                // 000000001010: 7D880481
 	s_nop 4                                                    // 000000001014: BF800004
@@ -146,8 +155,8 @@ def test_the_check_sees_what_it_looks_for():
 	s_endpgm                                                   // 000000001038: BF810000
 """
     found = hazards(listing)
-    assert len(found) == 2
-    assert "s6" in found[0] and "1 wait states" in found[0] and "s8" in found[1]
+    assert len(found) == 3
+    assert "s6" in found[0] and "1 wait states" in found[0] and "m0" in found[1] and "s8" in found[2]
 
 
 @pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
