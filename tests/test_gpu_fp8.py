@@ -825,3 +825,54 @@ def test_wgrad_of_operands_with_nans_behind_them(T, N, K, st):
     dw = torch.empty(N, K, device="cuda")
     rtq.fp8_wgrad(*[before_nans(t) for t in (dy, x, sx)], dw)
     assert torch.equal(dw.double(), ref)
+
+
+def _below_zero(T, d):
+    """Groups of 128 that lie wholly in [-8, -4], [-13, -8], [-4, 0] in turn."""
+    lo = torch.tensor([-8.0, -13.0, -4.0])[torch.arange(d) // 128 % 3]
+    hi = torch.tensor([-4.0, -8.0, 0.0])[torch.arange(d) // 128 % 3]
+    return lo + (hi - lo) * torch.rand(T, d, generator=gen(T + d))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,d", [(1, 384), (37, 784)])
+def test_gelu_below_zero(T, d, dtype):
+    """GELU (erf) keeps its relative accuracy where it is small.  y = h q, q the normal distribution's tail, which falls
+    as exp(-h^2 / 2): three roundings of that exponent (the constant's 2^-25, two products' 2^-24) cost at most
+    h^2 2^-23, the exponential, a reciprocal and some ten further operations at most 18 * 2^-23; then y's rounding."""
+    step("gelu below zero", T, d, dtype)
+    h = _below_zero(T, d).to(dtype)
+    codes, scale = empty_rows(T, d)
+    y = torch.empty(T, d, dtype=dtype, device="cuda")
+    rtq.act_fp8_forward(h.cuda(), ACTS["gelu"], codes, scale, y=y)
+    ref = act(h.double(), "gelu")
+    own = ref.abs() * (h.double() ** 2 + 18) * 2.0 ** -23 + 2.0 ** -126
+    tol = own + ref.abs() * (HALF_BF16 if dtype == BF16 else 2.0 ** -24)
+    assert ((y.cpu().double() - ref).abs() <= tol).all()
+    # as codes: half a step (2^-4) of y, or half the smallest code (2^-10) of a group whose scale follows y's size
+    yc, ys = empty_rows(T, d)
+    rtq.act_fp8_forward(h.cuda(), ACTS["gelu"], codes, scale, y_codes=yc, y_scale=ys)
+    top = torch.nn.functional.pad((ref.abs() + own), (0, groups(d) * 128 - d)).view(T, -1, 128).amax(2).t()
+    assert (ys.cpu().double() * 448.0 <= 2 * top * (1 + 2.0 ** -10)).all()      # the smallest power of two that holds it
+    small = (ys.cpu().double() * 2.0 ** -10).t().repeat_interleave(128, 1)[:, :d]
+    assert ((row_values(yc, ys) - ref).abs() <= own + (ref.abs() + own) * 2.0 ** -4 + small).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,d", [(1, 384), (37, 784)])
+def test_gelu_slope_below_zero(T, d, dtype):
+    """q + h phi(h): the first term as above, (h^2 + 18) 2^-23 of itself; the density has the same exponential, and two
+    products' roundings.  The terms have opposite signs below zero: the bound is on their sum of magnitudes, at most
+    (h^2 + 19) 2^-23 of it with the addition's rounding; a density below fp32's normal range may be 0."""
+    step("gelu slope below zero", T, d, dtype)
+    q, s = quantise(_below_zero(T, d), E4M3)
+    codes, scale = q.float().to(E4M3).cuda(), s.float().cuda()
+    hv = row_values(codes, scale)
+    dy = rows_like(T, T, d, dtype)
+    dh = torch.empty(T, d, dtype=dtype, device="cuda")
+    rtq.act_fp8_backward(dy.cuda(), codes, scale, ACTS["gelu"], dh)
+    want = dy.double() * slope(hv, "gelu")
+    first = 0.5 * torch.erfc(-hv / 2.0 ** 0.5)
+    second = hv.abs() * torch.exp(-0.5 * hv * hv) / (2 * torch.pi) ** 0.5
+    tol = dy.double().abs() * ((first + second) * (hv * hv + 19) * 2.0 ** -23 + 16 * 2.0 ** -126) + 2.0 ** -126
+    assert ((dh.cpu().double() - want).abs() <= tol + want.abs() * (HALF_BF16 if dtype == BF16 else 2.0 ** -23)).all()
