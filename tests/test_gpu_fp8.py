@@ -876,3 +876,109 @@ def test_gelu_slope_below_zero(T, d, dtype):
     second = hv.abs() * torch.exp(-0.5 * hv * hv) / (2 * torch.pi) ** 0.5
     tol = dy.double().abs() * ((first + second) * (hv * hv + 19) * 2.0 ** -23 + 16 * 2.0 ** -126) + 2.0 ** -126
     assert ((dh.cpu().double() - want).abs() <= tol + want.abs() * (HALF_BF16 if dtype == BF16 else 2.0 ** -23)).all()
+
+
+def _values(codes, scale, blocks=False):
+    """What codes stand for, on their device (float64)."""
+    s = scale.double()
+    s = s.repeat_interleave(128, 0)[:codes.shape[0]] if blocks else s.t()
+    return codes.double() * s.repeat_interleave(128, 1)[:, :codes.shape[1]]
+
+
+def _block_amax(v, dim):
+    """Largest magnitude of each 128 along a dimension, which comes last."""
+    v = v.abs().movedim(dim, 1)
+    return torch.nn.functional.pad(v, (0, groups(v.shape[1]) * 128 - v.shape[1])).view(v.shape[0], -1, 128).amax(2)
+
+
+# one size for each way a product runs: few rows, small, 64 tiles, split, 128 tiles, 256 tiles, long and 256 tiles
+FORMS = [(5, 208, 2064), (100, 336, 1040), (300, 512, 2064), (64, 4096, 4096), (1000, 4000, 400), (2500, 2800, 2064), (2500, 2800, 8208)]
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("T,N,R", FORMS)
+def test_general_operands_in_every_form(T, N, R, trans, fmt, st):
+    """Codes over the whole range and, in fp32, scales that are no powers of two.  In the 2-norm as above; in every
+    element: an instruction cuts each of 128 products at 2^-13 of the largest, 2^-6 of it in all, which is at most the
+    product of the block's largest factors.  (In fp32 sums, or E8M0 ones within the instruction at 2^-20 a block of the
+    running sum, which is at most 128 of those products: 2^-13 a block, 2^-6 over 128 blocks: 2^-5 together.)"""
+    step("general", T, N, R, trans, fmt, st)
+    x = rows_like(T + R, T, R).cuda()
+    w = (torch.randn(R if trans else N, N if trans else R, generator=gen(N)) * torch.exp(0.5 * torch.randn(1, generator=gen(3)))).cuda()
+    a, sa = empty_rows(T, R, fmt, st)
+    rtq.fp8_quantize(x, a, sa)
+    wq, sw = torch.empty(w.shape, dtype=E4M3, device="cuda"), torch.empty(groups(w.shape[0]), groups(w.shape[1]), dtype=st, device="cuda")
+    rtq.fp8_quantize(w, wq, sw, blocks=True)
+    if st == F32:
+        sa *= 0.75 + 0.5 * torch.rand(sa.shape, generator=gen(1)).cuda()
+        sw *= 0.75 + 0.5 * torch.rand(sw.shape, generator=gen(2)).cuda()
+    av, wv = _values(a, sa), _values(wq, sw, blocks=True)
+    ref = av @ (wv if trans else wv.t().contiguous())
+    each = _block_amax(av, 1) @ _block_amax(wv, 0 if trans else 1).t().contiguous()
+    for dtype in (F32, BF16):
+        y = torch.empty(T, N, dtype=dtype, device="cuda")
+        (rtq.fp8_dgrad if trans else rtq.fp8_qgemm)(a, sa, wq, sw, y)
+        out = HALF_BF16 if dtype == BF16 else 0.0
+        assert float((y.double() - ref).norm() / ref.norm()) <= GENERAL + out
+        assert ((y.double() - ref).abs() <= 2.0 ** -5 * each * (1 + out) + out * ref.abs()).all()
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N,R", [(4, 512, 2048), (64, 512, 2048), (1000, 4000, 2048), (2500, 2800, 2048)])
+def test_small_blocks_behind_a_large_one(T, N, R, st):
+    """Block sums of 1 behind one of 2^k: in fp32 every sum here is exact.  E8M0 blocks of the 256 x 256 tiles are added
+    by the instruction, which may cut off 2^-20 of the running sum in each of the 15 blocks."""
+    step("small blocks behind a large one", T, N, R, st)
+    a, w = torch.ones(T, R, device="cuda").to(E4M3), torch.ones(N, R, device="cuda").to(E4M3)
+    sw = torch.ones(groups(N), groups(R), device="cuda").to(st)
+    for k in (0, 10, 17, 20, 23):
+        sa = torch.full((groups(R), T), 2.0 ** -7, device="cuda")
+        sa[0] = 2.0 ** (k - 7)
+        y = torch.empty(T, N, device="cuda")
+        rtq.fp8_qgemm(a, sa.to(st), w, sw, y)
+        want = 2.0 ** k + 15
+        cut = 15 * 2.0 ** -20 * want if st == E8M0 and T * N > 1 << 22 else 0.0
+        assert ((y.double() - want).abs() <= cut).all()
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("T,N,R", [(5, 208, 272), (1000, 4000, 400), (4100, 1488, 272)])
+def test_extreme_scales_in_every_form(T, N, R, trans):
+    """Scales at both ends of their range, in fp32 and as E8M0 bytes; byte 0 is 2^-127."""
+    step("extreme scales", T, N, R, trans)
+    a, w = int_codes(1, T, R).cuda(), int_codes(2, R if trans else N, N if trans else R).cuda()
+    ref = a.double() @ (w.double() if trans else w.double().t().contiguous())
+    call = rtq.fp8_dgrad if trans else rtq.fp8_qgemm
+
+    def product(sa, sw, st):
+        s1 = torch.full((groups(R), T), sa, device="cuda").to(st)
+        s2 = torch.full((groups(w.shape[0]), groups(w.shape[1])), sw, device="cuda").to(st)
+        y = torch.empty(T, N, device="cuda")
+        call(a, s1, w, s2, y)
+        return y
+    for ea, ew in ((100, -100), (-120, 120), (-60, -60), (-127, 100), (100, -127), (60, 50), (-127, 127), (127, -127), (-40, -70)):
+        for st in (F32, E8M0):
+            assert torch.equal(product(2.0 ** ea, 2.0 ** ew, st).double(), ref * 2.0 ** (ea + ew)), (ea, ew, st)
+    assert not product(0.0, 1.0, F32).any()
+
+
+@pytest.mark.parametrize("T,N,K", [(200, 136, 272), (333, 2600, 3600), (1000, 2824, 2560)])
+def test_wgrad_general_scales_in_every_form(T, N, K):
+    """Sums of T products in fp32, and with general scales each term's decoded input rounded to bf16: in every element
+    2^-8 of the terms' magnitudes and (T + 1) 2^-22 for the sums."""
+    step("wgrad general scales", T, N, K)
+    dy = rows_like(3, T, N).cuda()
+    x, sx = empty_rows(T, K)
+    rtq.fp8_quantize(rows_like(4, T, K).cuda(), x, sx)
+    for general in (False, True):
+        if general:
+            sx *= 0.75 + 0.5 * torch.rand(sx.shape, generator=gen(1)).cuda()
+        xv, g = _values(x, sx), dy.double().t().contiguous()
+        ref, size = g @ xv, g.abs() @ xv.abs()
+        tol = ((2.0 ** -8 if general else 0.0) + (T + 1) * 2.0 ** -22) * size
+        for dtype in (F32, BF16):
+            dw = torch.empty(N, K, dtype=dtype, device="cuda")
+            rtq.fp8_wgrad(dy, x, sx, dw)
+            assert ((dw.double() - ref).abs() <= tol + (HALF_BF16 * (ref.abs() + tol) if dtype == BF16 else 0.0)).all()
