@@ -982,3 +982,72 @@ def test_wgrad_general_scales_in_every_form(T, N, K):
             dw = torch.empty(N, K, dtype=dtype, device="cuda")
             rtq.fp8_wgrad(dy, x, sx, dw)
             assert ((dw.double() - ref).abs() <= tol + (HALF_BF16 * (ref.abs() + tol) if dtype == BF16 else 0.0)).all()
+
+
+def test_row_passes_past_32_bits():
+    """Activations and their gradient, and codes read back, in the last rows of more than 2^31 elements."""
+    torch.cuda.empty_cache()
+    T, d = 140000, 16384
+    step("row passes past 2^31")
+    h = torch.zeros(T, d, dtype=BF16, device="cuda")
+    tail = rows_like(5, 3, d)
+    h[-3:] = tail.cuda()
+    codes, scale = empty_rows(T, d)
+    y = torch.full((T, d), 7.0, dtype=BF16, device="cuda")
+    rtq.act_fp8_forward(h, ACTS["silu"], codes, scale, y=y)
+    small, s1 = empty_rows(3, d)
+    want = torch.empty(3, d, dtype=BF16, device="cuda")
+    rtq.act_fp8_forward(tail.cuda(), ACTS["silu"], small, s1, y=want)       # checked against 64 bits elsewhere
+    assert same(y[-3:], want) and not y[:-3].any()
+    assert same(codes[-3:], small) and same(scale[:, -3:], s1)
+    step("read back past 2^31")
+    y.fill_(7.0)
+    rtq.fp8_dequantize(codes, scale, y)
+    assert same(y[-3:], row_values(small, s1).float().bfloat16()) and not y[:-3].any()
+    step("gradient past 2^31")
+    h[:] = 1.0
+    grad = rows_like(6, 3, d)
+    h[-3:] = grad.cuda()
+    rtq.act_fp8_backward(h, codes, scale, ACTS["silu"], y)
+    rtq.act_fp8_backward(grad.cuda(), small, s1, ACTS["silu"], want)
+    assert same(y[-3:], want) and (y[:-3] == 0.5).all()                     # the slope of SiLU at 0
+    step("weight blocks past 2^31")
+    w = y.fill_(0.0)
+    w[-3:] = tail.cuda()
+    q, s = quantise(torch.cat([torch.zeros(T % 128 - 3, d), tail.float()]), E4M3, blocks=True)      # the last row of blocks
+    bs = torch.empty(groups(T), groups(d), device="cuda")
+    rtq.fp8_quantize(w, codes, bs, blocks=True)
+    assert same(codes[-3:], q[-3:]) and same(bs[-1], s[0]) and (bs[:-1] == 1.0).all()
+
+
+@pytest.mark.parametrize("trans", [False, True])
+def test_large_products_past_32_bits(trans):
+    """256 x 256 tiles: more than 2^31 outputs, and more than 2^31 codes."""
+    torch.cuda.empty_cache()
+    for T, N, R in ((140000, 16384, 272), (140000, 272, 16384)):
+        step("large product past 2^31", T, N, R, trans)
+        a = torch.zeros(T, R, device="cuda", dtype=torch.uint8).view(E4M3)
+        tail = int_codes(1, 3, R)
+        a[-3:] = tail.cuda()
+        w = int_codes(2, R if trans else N, N if trans else R).cuda()
+        sa, sw = torch.ones(groups(R), T, device="cuda"), torch.ones(groups(w.shape[0]), groups(w.shape[1]), device="cuda")
+        y = torch.full((T, N), 7.0, dtype=BF16, device="cuda")
+        (rtq.fp8_dgrad if trans else rtq.fp8_qgemm)(a, sa, w, sw, y)
+        ref = tail.double().cuda() @ (w.double() if trans else w.double().t().contiguous())
+        assert same(y[-3:], ref.float().bfloat16()) and not y[:-3].any()
+        del a, y
+
+
+@pytest.mark.parametrize("T,N,K", [(64, 65544, 32784), (70, 65544, 32784), (270000, 8200, 144)])
+def test_wgrad_past_32_bits(T, N, K):
+    """Both kernels with more than 2^31 gradients, and with more than 2^31 output gradients."""
+    torch.cuda.empty_cache()
+    step("wgrad past 2^31", T, N, K)
+    dy = torch.zeros(T, N, dtype=BF16, device="cuda")
+    dy[-3:, -16:] = torch.randint(-4, 5, (3, 16), generator=gen(1)).to(BF16).cuda()
+    x = int_codes(K, 16, K).cuda().view(torch.uint8).repeat(-(-T // 16), 1)[:T].contiguous().view(E4M3)
+    sx = torch.ones(groups(K), T, device="cuda")
+    dw = torch.full((N, K), 7.0, dtype=BF16, device="cuda")
+    rtq.fp8_wgrad(dy, x, sx, dw)
+    ref = dy[-3:, -16:].double().t().contiguous() @ x[-3:].double()
+    assert same(dw[-16:], ref.float().bfloat16()) and not dw[:-16].any()
