@@ -1051,3 +1051,80 @@ def test_wgrad_past_32_bits(T, N, K):
     rtq.fp8_wgrad(dy, x, sx, dw)
     ref = dy[-3:, -16:].double().t().contiguous() @ x[-3:].double()
     assert same(dw[-16:], ref.float().bfloat16()) and not dw[:-16].any()
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N,R", [(5, 208, 528), (70, 208, 528), (200, 4096, 1040), (1000, 4000, 400), (4100, 1488, 272)])
+def test_infinite_gradient_codes(T, N, R, st):
+    """An infinite E5M2 code times positive weights, forward and transposed, in every form; and with its opposite: NaN."""
+    step("infinite codes", T, N, R, st)
+    for trans in (False, True):
+        a, w = torch.ones(T, R).to(E5M2), torch.ones(R if trans else N, N if trans else R, device="cuda").to(E4M3)
+        a[0, R - 1], a[T // 2, 1], a[T // 2, 2] = -float("inf"), float("inf"), -float("inf")
+        sa, sw = torch.ones(groups(R), T, device="cuda").to(st), torch.ones(groups(w.shape[0]), groups(w.shape[1]), device="cuda").to(st)
+        y = torch.empty(T, N, device="cuda")
+        (rtq.fp8_dgrad if trans else rtq.fp8_qgemm)(a.cuda(), sa, w, sw, y)
+        assert (y[0] == -float("inf")).all() and torch.isnan(y[T // 2]).all()
+        assert (y[[t for t in range(T) if t not in (0, T // 2)]] == R).all()
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("T,N,R", [(3, 48, 1 << 20), (70, 80, 1 << 20), (2, 1 << 20, 16), (40, 1 << 20, 32), (300, 1 << 20, 272),
+                                   (4100, 4112, (1 << 20) - 16)])
+def test_longest_rows(T, N, R, trans):
+    """The largest reductions and outputs, exact: codes to 1, at most 2^20 of them."""
+    torch.cuda.empty_cache()
+    step("longest rows", T, N, R, trans)
+    g = torch.Generator(device="cuda").manual_seed(T)
+
+    def signs(rows, d):
+        return torch.randint(-1, 2, (rows, d), generator=g, device="cuda", dtype=torch.int8).to(BF16).to(E4M3)
+    a, w = signs(T, R), signs(R if trans else N, N if trans else R)
+    sa, sw = torch.ones(groups(R), T, device="cuda"), torch.ones(groups(w.shape[0]), groups(w.shape[1]), device="cuda")
+    y = torch.full((T + 1, N), 7.0, device="cuda")
+    (rtq.fp8_dgrad if trans else rtq.fp8_qgemm)(a, sa, w, sw, y[:T])
+    rows = [0, T // 2, T - 1]
+    ref = torch.zeros(3, N, dtype=torch.float64, device="cuda")
+    for k in range(0, R, 1 << 15):
+        part = w[k:k + (1 << 15)] if trans else w[:, k:k + (1 << 15)].t().contiguous()
+        ref += a[rows, k:k + (1 << 15)].double() @ part.double()
+    assert torch.equal(y[rows].double(), ref) and (y[T] == 7.0).all()
+    if R <= 272:
+        x = torch.empty(T, R, dtype=BF16, device="cuda").copy_(a.to(BF16))
+        z = torch.empty(T, N, device="cuda")
+        if trans:
+            rtq.fp8_linear_dgrad(x, w, sw, z, grad_dtype=E4M3)
+        else:
+            rtq.fp8_linear(x, w, sw, z)
+        assert torch.equal(z[rows].double(), ref)
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 1 << 20, 16), (70, 1 << 20, 144), (3, 8, 1 << 20), (130, 264, 1 << 20)])
+def test_wgrad_longest_rows(T, N, K):
+    torch.cuda.empty_cache()
+    step("wgrad longest rows", T, N, K)
+    dy = torch.randint(-4, 5, (T, N), generator=gen(T)).to(BF16).cuda()
+    x, sx = int_codes(1, T, K).cuda(), pow2_scales(9, groups(K), T, -2, 2).cuda()
+    dw = torch.full((N + 1, K), 7.0, device="cuda")
+    rtq.fp8_wgrad(dy, x, sx, dw[:N])
+    xv = _values(x, sx)
+    for part in (slice(0, 200), slice(N - 200 if N > 200 else 0, N)):
+        assert torch.equal(dw[:N][part].double(), dy[:, part].double().t().contiguous() @ xv)
+    assert (dw[N] == 7.0).all()
+
+
+def test_longest_quantised_rows():
+    step("longest quantised rows")
+    T, d = 3, 1 << 20
+    x = rows_like(1, T, d).cuda()
+    codes, scale = empty_rows(T, d)
+    rtq.fp8_quantize(x, codes, scale)
+    part = x[:, -4096:].contiguous()
+    c1, s1 = empty_rows(T, 4096)
+    rtq.fp8_quantize(part, c1, s1)
+    assert same(codes[:, -4096:], c1) and same(scale[-32:], s1)
+    dh = torch.empty_like(x)
+    rtq.act_fp8_backward(x, codes, scale, ACTS["gelu"], dh)
+    d1 = torch.empty_like(part)
+    rtq.act_fp8_backward(part, c1, s1, ACTS["gelu"], d1)
+    assert same(dh[:, -4096:], d1)
