@@ -305,7 +305,7 @@ size_t rtq_rotated_qlinear_asym_workspace(int64_t T, int32_t d);
  *     Stored row-major: scale[ceil(N / 128)][ceil(K / 128)].
  *   - scales are F32 (any value; non-finite ones spread as in fp32 arithmetic) or E8M0, one type for
  *     both operands of a product.  The product of the two scales of a block must itself be an fp32 number
- *     (below 2^128).  Scale arrays are 16-byte aligned like every device pointer here.
+ *     (below 2^128; below 2^-126 it has fewer bits).  Scale arrays are 16-byte aligned like every device pointer here.
  *   - The quantiser's rule for a block: with m its largest finite magnitude, the scale is the smallest
  *     power of two s >= 2^-120 with m <= 448 s (E4M3) or m <= 57344 s (E5M2), and 1 when m = 0; a code
  *     is x / s (exact) rounded to nearest, ties to even.  NaN stays NaN; an infinity becomes NaN in
@@ -328,7 +328,9 @@ rtq_status rtq_fp8_dequantize(const void* codes, rtq_dtype ct, const void* scale
 /* y[t][n] = sum_kb a_scale[kb][t] w_scale[n / 128][kb] sum_{k in block kb} a[t][k] w[n][k].
  *   a_codes [T][K] of at (E4M3 or E5M2), row groups; w_codes [N][K] E4M3, blocks; y [T][N] of yt.
  *   Accuracy: each 128-long inner sum is one matrix instruction, which aligns its products to about
- *   2^-14 of the largest; block sums are scaled and added in fp32.
+ *   2^-14 of the largest; block sums are scaled and added in fp32.  With E8M0 scales large outputs add the
+ *   block inside the instruction, which cuts off what lies below 2^-20 of the running sum.  So an fp32 y
+ *   is good to about 4e-5 of its 2-norm, not to fp32.
  *   workspace: may be NULL.  With at least rtq_fp8_qgemm_workspace(T, N, K) bytes (any contents,
  *   16-byte aligned), products with few output tiles are split along the reduction; the fp32
  *   partial sums are then added in a fixed order, so equal calls give equal bits.  Calls sharing a
@@ -386,12 +388,14 @@ typedef enum {
 /* An activation function with its input kept in 8 bits, in one pass over h [rows][d] (F32 or BF16):
  *   h_codes (E4M3), h_scale (row groups): rtq_fp8_quantize(h), the checkpoint;
  *   y = f(h): either y [rows][d] of h's type (y_codes and y_scale NULL), or y_codes, y_scale (E4M3, row
- *   groups) for the next product (y NULL). */
+ *   groups) for the next product (y NULL).
+ *   Accuracy before y's rounding, relative: an exponential's argument z is rounded to fp32, so f is good to
+ *   about (3 |z| + 4) 2^-23 (z = h for SILU, 2 sqrt(2/pi) (h + ..) for GELU_TANH, h^2 for GELU below 0). */
 rtq_status rtq_act_fp8_forward(const void* h, rtq_dtype ht, int64_t rows, int32_t d, rtq_act act, void* h_codes,
                                void* h_scale, void* y, void* y_codes, void* y_scale, rtq_dtype st, void* stream);
 
 /* Its backward pass from the checkpoint: dh = dy f'(h^), h^ = h_scale h_codes.  dy, dh [rows][d] of dyt
- * (F32 or BF16); dh may be dy itself. */
+ * (F32 or BF16); dh may be dy itself.  f' has the accuracy of f, of its terms' size. */
 rtq_status rtq_act_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_codes, const void* h_scale,
                                 rtq_dtype st, int64_t rows, int32_t d, rtq_act act, void* dh, void* stream);
 

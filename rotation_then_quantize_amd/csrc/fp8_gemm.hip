@@ -245,7 +245,7 @@ struct Plan {
 //   128 x 128  19.9        21.1     21.4     22.2     23.2     24.3     42.9     49.3
 //   256 x 256  32.5        33.1     33.1     33.4     33.5     33.4     34.8     38.9
 // A tile costs its chain of stages as long as each CU has one (128: one workgroup per CU, 64: two), so the
-// largest tile whose workgroups fit at once is taken.  Splitting the reduction shortens the chain of the 64
+// smallest tile whose workgroups fit at once is taken, and where none fits the largest.  Splitting the reduction shortens the chain of the 64
 // x 64 tiles: in as many parts as give each CU one workgroup (64 x 1024 outputs, 4096 long: 12.3 us whole, 10.1
 // in two parts, 8.0 in five; M = 128: 13.4 and 12.4 in two), or two where the parts stay long (M = 128,
 // reduction of 16384: 45.0, in two 28.2, in four 22.9; of 4096: 12.4, 12.7).  The second kernel loads four

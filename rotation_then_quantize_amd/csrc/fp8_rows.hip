@@ -168,7 +168,8 @@ fp8_rows_kernel(const void* __restrict__ x, int64_t rows, int d, int col_waves, 
 //   quantise 16384          45.1     40.9     41.9     45.2     47.2
 //   GELU (tanh) 16384       69.1     68.2     69.8     77.5     84.5
 // at 40.9 and 68.2 us 5.5 TB/s: more rows fill a cache line of scales, but even out worse over the CUs).  One
-// where there are fewer waves than the CUs have SIMDs for twice over.
+// where there are fewer waves than the card has SIMDs for twice over (2048), so that no SIMD idles: there a pass takes
+// a launch's time either way (64 to 256 rows x 4096: 5.1-5.5 us with one and with two).
 template <bool kBF16, bool kE5M2, int kAct, int kY>
 hipError_t launch_rows(const void* x, int64_t rows, int d, const RowsOut& o, hipStream_t stream) {
     const int col_waves = (d + kWaveCols - 1) / kWaveCols;

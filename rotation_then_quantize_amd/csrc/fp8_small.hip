@@ -13,10 +13,10 @@
 // workgroup of a row of tiles does so again, which saves a launch; the first of them stores the codes and
 // scales where they are kept.
 //
-// A few tokens (kTT = 1) are bound by the weights' bytes.  More columns per workgroup and few units in flight
-// stream best (16384 x 4096 weights: 15.0 us, 4.5 TB/s, with 64 columns and one unit of 8 KB a wave beside
-// the one in use; when all XCDs began at the same place of their rows 16.3 so, 17.9 with two units, 25 with 32
-// columns, 29.6 with 16).  Small outputs are bound by latency: one
+// A few tokens (kTT = 1) are bound by the weights' bytes.  More columns per workgroup and few units a wave
+// stream best (16384 x 4096 weights: 15.0 us, 4.5 TB/s, with 64 columns and one unit of 8 KB a wave, loaded again
+// as soon as it has been multiplied, the other waves' loads being in flight meanwhile; when all XCDs began at the
+// same place of their rows 16.3 so, 17.9 with two units, 25 with 32 columns, 29.6 with 16).  Small outputs are bound by latency: one
 // launch, one chain of loads, products and sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(64 * kWaves)
 fp8_small_kernel(SmallParams sp) {
     const Fp8GemmParams& p = sp.g;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    constexpr int kAhead = kTrans ? 2 : (kTT == 1 && kRT == 4 ? 1 : 2);   // units in flight beside the one in use
+    constexpr int kUnits = kTrans ? 2 : (kTT == 1 && kRT == 4 ? 1 : 2);   // units a wave holds, the one in use among them
     constexpr int kScaleSize = kE8M0 ? 1 : 4;
     constexpr int kElem = kX == kCodes ? 1 : (kX == kBF16 ? 2 : 4);
     const int tid = threadIdx.x, lane = tid & 63;
@@ -241,14 +241,14 @@ fp8_small_kernel(SmallParams sp) {
         const int j = t + start;
         return t < turns ? wave + kWaves * (j < turns ? j : j - turns) : blocks;
     };
-    Unit<kTT, kRT, kX, kTrans> u[kAhead];
+    Unit<kTT, kRT, kX, kTrans> u[kUnits];
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) load(u[q], block(q), q);
-    for (int t = 0; t < turns; t += kAhead) {
+    for (int q = 0; q < kUnits; ++q) load(u[q], block(q), q);
+    for (int t = 0; t < turns; t += kUnits) {
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
+        for (int q = 0; q < kUnits; ++q) {
             multiply(u[q], block(t + q), q);
-            load(u[q], block(t + q + kAhead), q);
+            load(u[q], block(t + q + kUnits), q);
         }
     }
     if constexpr (kTrans) {
@@ -292,7 +292,9 @@ hipError_t launch_form(const SmallParams& p, hipStream_t stream) {
     const int64_t tiles = (p.g.N + 15) / 16;
     const int cus = device_cu_count();
     if (p.g.M > 16) {
-        // 32 tokens by 64 columns, or by 32 where that leaves CUs idle
+        // 32 tokens by 64 columns, or by 32 where that leaves CUs idle (layers, us with 64 and with 32: 32 x 1024, 1024
+        // columns, 16 tiles of 64: 10.0, 8.5; 200 x 2048, 1024, 112 tiles: 12.8, 10.5; 200 x 1024, 2048, 224 tiles: 10.2,
+        // 15.7; 256 x 2048, 2048, 256 tiles: 13.0, 19.7)
         if ((p.g.M + 31) / 32 * ((p.g.N + 63) / 64) >= cus / 2) return launch_tile<2, 4, kX, kE5M2, kE8M0, kTrans>(p, stream);
         return launch_tile<2, 2, kX, kE5M2, kE8M0, kTrans>(p, stream);
     }
@@ -324,6 +326,9 @@ bool fits(int64_t M, int64_t N, int R) {
 
 }  // namespace
 
+// At most 16 rows: always, but transposed weights, whose rows of 16 to 64 bytes a workgroup stream badly, only up to 16
+// M of them (16 tokens, reduction x columns, us here and with 64 x 64 tiles: 2048 x 4096 6.5, 9.4; 4096 x 4096 9.0, 9.9;
+// 8192 x 4096 16.0, 12.0; 16384 x 4096 34.0, 18.0; but 4096 x 8192 10.8, 12.0; 4096 x 16384 15.5, 15.8).
 bool fp8_small_takes(int64_t M, int64_t N, int R, bool trans) {
     if (M <= 16) return !trans || N * R <= int64_t{16} << 20;
     return fits(M, N, R);

@@ -210,7 +210,6 @@ wgrad_reduce_kernel(const float* __restrict__ part, int split, int64_t n, void* 
 
 int64_t tiles_of(int N, int K) { return static_cast<int64_t>((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile); }
 
-// Ranges of the tokens per tile: a workgroup for each CU, each at least eight stages long.
 // Parts of the tokens: as many as fill the CUs, of at least 8 stages (the second kernel costs what shorter chains
 // save: 512 tokens, 2048 x 1024 outputs 11.8 us whole, 16.0 in two parts; 4608 tokens, 512 x 512 outputs 16.6 us
 // in nine parts, 21.4 in four; 1024 tokens, 512 x 512: 13.4 in two, 15.0 whole).
