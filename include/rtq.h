@@ -390,7 +390,8 @@ typedef enum {
  *   y = f(h): either y [rows][d] of h's type (y_codes and y_scale NULL), or y_codes, y_scale (E4M3, row
  *   groups) for the next product (y NULL).
  *   Accuracy before y's rounding, relative: an exponential's argument z is rounded to fp32, so f is good to
- *   about (3 |z| + 4) 2^-23 (z = h for SILU, 2 sqrt(2/pi) (h + ..) for GELU_TANH, h^2 for GELU below 0). */
+ *   about (3 |z| + 4) 2^-23 (z = h for SILU, 2 sqrt(2/pi) (h + ..) for GELU_TANH, h^2 for GELU below 0); what is
+ *   smaller than 2^-119 may come out as 0. */
 rtq_status rtq_act_fp8_forward(const void* h, rtq_dtype ht, int64_t rows, int32_t d, rtq_act act, void* h_codes,
                                void* h_scale, void* y, void* y_codes, void* y_scale, rtq_dtype st, void* stream);
 
