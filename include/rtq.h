@@ -400,6 +400,77 @@ rtq_status rtq_act_fp8_forward(const void* h, rtq_dtype ht, int64_t rows, int32_
 rtq_status rtq_act_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_codes, const void* h_scale,
                                 rtq_dtype st, int64_t rows, int32_t d, rtq_act act, void* dh, void* stream);
 
+/* ---- Around the 8-bit linear layers of an MLP block: the norm before them, the gated feed-forward, and the
+ * gradients' norm behind them.  Formats, sizes and errors as in the calls above. */
+
+/* Root-mean-square norm of rows, with the residual's addition before it and codes for the next product behind it:
+ *   h = x + residual, rounded to rt (h = x without a residual), the residual stream;
+ *   n = h / sqrt(mean_j h_j^2 + eps) * gamma, from h as it is stored;
+ *   y = n rounded to xt, and/or codes (E4M3), scale (row groups, st): n quantised.
+ *   x, y [rows][d] of xt; residual, h [rows][d] of rt (all F32 or BF16); residual and h are given together or not at
+ *   all (rt is not used then); h may be residual, or x where rt is xt.  gamma [d] of gt.  y may be NULL, or codes and
+ *   scale.  eps > 0.  The sum of squares is held in 64 bits; n is good to 4 units of 2^-24 before it is rounded.
+ *   rows == 0 is a no-op. */
+rtq_status rtq_rmsnorm_forward(const void* x, rtq_dtype xt, const void* residual, rtq_dtype rt, int64_t rows, int32_t d,
+                               const void* gamma, rtq_dtype gt, float eps, void* h, void* y, void* codes, void* scale,
+                               rtq_dtype st, void* stream);
+
+/* Its backward pass, with rho = 1 / sqrt(mean_j h_j^2 + eps) and a = gamma dn of each row:
+ *   dh = dresidual + rho a - h rho^3 mean_j(a_j h_j): the gradient of h, thus of x and of residual;
+ *   dgamma_j (+)= sum over rows of dn_j h_j rho, summed in fp32 in an order that equal calls share.
+ *   dn [rows][d] of dnt; h, dresidual (or NULL: nothing is added), dh [rows][d] of ht; dh may be dresidual, or dn where
+ *   dnt is ht, not h.  dgamma [d] of dgt, or NULL; accumulate 0 (overwrite) or 1 (add; a BF16 dgamma is read, added in
+ *   fp32 and rounded again).  workspace: rtq_rmsnorm_backward_workspace(rows, d) bytes (any contents), required with
+ *   dgamma.  rows == 0 writes zeros to dgamma, or with accumulate leaves it as it is. */
+rtq_status rtq_rmsnorm_backward(const void* dn, rtq_dtype dnt, const void* h, rtq_dtype ht, const void* dresidual,
+                                int64_t rows, int32_t d, const void* gamma, rtq_dtype gt, float eps, void* dh,
+                                void* dgamma, rtq_dtype dgt, int32_t accumulate, void* workspace, size_t ws_bytes,
+                                void* stream);
+size_t rtq_rmsnorm_backward_workspace(int64_t rows, int32_t d);
+
+/* The gated feed-forward's first half: both projections, the activation and the product.
+ *   g[t][n] = (x W^T)[t][n], u[t][n] = (x W^T)[t][N + n], y = f(g) u: rtq_fp8_qgemm's product with fp32 sums.
+ *   x_codes [T][K] E4M3, row groups; w_codes [2 N][K] E4M3, blocks, the gate's N rows first (one weight matrix for
+ *   rtq_fp8_dgrad and rtq_fp8_wgrad); N a multiple of 128, so that no block or group holds both.
+ *   y: either y [T][N] of yt (F32 or BF16; y_codes and y_scale NULL), or y_codes (E4M3), y_scale (row groups) for the
+ *   next product (y NULL).  h_codes (E4M3) [T][2 N], h_scale (row groups): [g u] quantised, the checkpoint that
+ *   rtq_glu_fp8_backward takes; both NULL: not kept.  All scales of type st.
+ *   workspace: rtq_fp8_glu_workspace(T, N, K) bytes (any contents), required where that is not 0.  Calls sharing a
+ *   workspace must not overlap.  Accuracy of g and u as for rtq_fp8_qgemm, of f as for rtq_act_fp8_forward.  T == 0
+ *   is a no-op. */
+rtq_status rtq_fp8_glu(const void* x_codes, const void* x_scale, int64_t T, const void* w_codes, const void* w_scale,
+                       rtq_dtype st, int32_t N, int32_t K, rtq_act act, void* h_codes, void* h_scale, void* y, rtq_dtype yt,
+                       void* y_codes, void* y_scale, void* workspace, size_t ws_bytes, void* stream);
+size_t rtq_fp8_glu_workspace(int64_t T, int32_t N, int32_t K);
+
+/* Its backward pass from the checkpoint: dg = dy u^ f'(g^), du = dy f(g^), [g^ u^] = h_scale h_codes.
+ *   dy [T][N] of dyt (F32 or BF16).  dh [T][2 N] of dyt: [dg du] (rtq_fp8_wgrad takes it in BF16), and/or dh_codes of gt
+ *   (E4M3 or E5M2) [T][2 N], dh_scale (row groups, st): the same quantised, for rtq_fp8_dgrad.  What is not wanted is
+ *   NULL.  T == 0 is a no-op. */
+rtq_status rtq_glu_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_codes, const void* h_scale, rtq_dtype st,
+                                int64_t T, int32_t N, rtq_act act, void* dh, void* dh_codes, rtq_dtype gt, void* dh_scale,
+                                void* stream);
+
+/* A tensor of n elements, F32 or BF16, contiguous in device memory. */
+typedef struct {
+    void* data;
+    int64_t n;
+    rtq_dtype type;
+} rtq_tensor;
+
+/* norm[0] = sqrt(sum over all tensors and elements of g^2), the sum held in 64 bits and added in an order that the
+ * tensors' sizes alone decide.  tensors: `count` of them, an array in HOST memory, not used after the call returns; n up to 2^37
+ * each, 0 too.  norm: one float in device memory.  workspace: rtq_grad_norm_workspace(tensors, count) bytes (any
+ * contents).  No tensors: norm[0] = 0. */
+rtq_status rtq_grad_norm(const rtq_tensor* tensors, int32_t count, float* norm, void* workspace, size_t ws_bytes, void* stream);
+size_t rtq_grad_norm_workspace(const rtq_tensor* tensors, int32_t count);
+
+/* out = g * min(1, most / (norm[0] + 1e-6)) for every tensor, rounded to its type; most >= 0.  outs: `count` device
+ * pointers in HOST memory, tensors of the same sizes and types; NULL, or an entry that is the tensor's own data: in
+ * place (nothing is written then where the factor is 1).  An out may not overlap any other tensor or out.  norm: as
+ * rtq_grad_norm wrote it, or any other (the norm over several GPUs); a NaN spreads to every element. */
+rtq_status rtq_grad_clip(const rtq_tensor* tensors, void* const* outs, int32_t count, const float* norm, float most, void* stream);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* rtq_last_error(void);
 

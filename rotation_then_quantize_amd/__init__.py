@@ -51,7 +51,9 @@ EXPORTS = ("rtq_rpbh_make", "rtq_lloyd_max", "rtq_rpbh_rotate", "rtq_quantize_ro
            "rtq_fp8_dequantize", "rtq_fp8_qgemm", "rtq_fp8_qgemm_workspace", "rtq_fp8_dgrad",
            "rtq_fp8_dgrad_workspace", "rtq_fp8_linear", "rtq_fp8_linear_workspace", "rtq_fp8_linear_dgrad",
            "rtq_fp8_linear_dgrad_workspace", "rtq_fp8_wgrad", "rtq_fp8_wgrad_workspace", "rtq_act_fp8_forward",
-           "rtq_act_fp8_backward", "rtq_last_error")
+           "rtq_act_fp8_backward", "rtq_rmsnorm_forward", "rtq_rmsnorm_backward", "rtq_rmsnorm_backward_workspace",
+           "rtq_fp8_glu", "rtq_fp8_glu_workspace", "rtq_glu_fp8_backward", "rtq_grad_norm", "rtq_grad_norm_workspace",
+           "rtq_grad_clip", "rtq_last_error")
 
 NOALLOC_SCRATCH_BYTES = 96 << 20   # RTQ_NOALLOC_SCRATCH_BYTES
 
@@ -64,6 +66,10 @@ class RtqError(RuntimeError):
 
 class _Rpbh(ctypes.Structure):
     _fields_ = [("d", ctypes.c_int32), ("h", ctypes.c_int32), ("perm", ctypes.c_void_p), ("signs", ctypes.c_void_p)]
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int)]
 
 
 class _Codebook(ctypes.Structure):
@@ -117,13 +123,26 @@ def load_library():
                     ("rtq_fp8_wgrad_workspace", i32)):
         getattr(lib, name).argtypes = [i64, n, i32]
         getattr(lib, name).restype = sz
+    lib.rtq_rmsnorm_forward.argtypes = [vp, i32, vp, i32, i64, i32, vp, i32, f32, vp, vp, vp, vp, i32, vp]
+    lib.rtq_rmsnorm_backward.argtypes = [vp, i32, vp, i32, vp, i64, i32, vp, i32, f32, vp, vp, i32, i32, vp, sz, vp]
+    lib.rtq_rmsnorm_backward_workspace.argtypes = [i64, i32]
+    lib.rtq_rmsnorm_backward_workspace.restype = sz
+    lib.rtq_fp8_glu.argtypes = [vp, vp, i64, vp, vp, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    lib.rtq_fp8_glu_workspace.argtypes = [i64, i32, i32]
+    lib.rtq_fp8_glu_workspace.restype = sz
+    lib.rtq_glu_fp8_backward.argtypes = [vp, i32, vp, vp, i32, i64, i32, i32, vp, vp, i32, vp, vp]
+    lib.rtq_grad_norm.argtypes = [vp, i32, vp, vp, sz, vp]
+    lib.rtq_grad_norm_workspace.argtypes = [vp, i32]
+    lib.rtq_grad_norm_workspace.restype = sz
+    lib.rtq_grad_clip.argtypes = [vp, vp, i32, vp, f32, vp]
     lib.rtq_last_error.argtypes = []
     lib.rtq_last_error.restype = ctypes.c_char_p
     for name in ("rtq_rpbh_make", "rtq_lloyd_max", "rtq_rpbh_rotate", "rtq_quantize_rows", "rtq_qgemm",
                  "rtq_qgemm_ws", "rtq_rotated_qlinear", "rtq_quantize_rows_asym", "rtq_qgemm_asym",
                  "rtq_rotated_qlinear_asym", "rtq_rotated_qlinear_noalloc", "rtq_fp8_quantize", "rtq_fp8_dequantize",
                  "rtq_fp8_qgemm", "rtq_fp8_dgrad", "rtq_fp8_linear", "rtq_fp8_linear_dgrad", "rtq_fp8_wgrad",
-                 "rtq_act_fp8_forward", "rtq_act_fp8_backward"):
+                 "rtq_act_fp8_forward", "rtq_act_fp8_backward", "rtq_rmsnorm_forward", "rtq_rmsnorm_backward",
+                 "rtq_fp8_glu", "rtq_glu_fp8_backward", "rtq_grad_norm", "rtq_grad_clip"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -616,3 +635,159 @@ def act_fp8_backward(dy, h_codes, h_scale, act: int, dh, stream=None):
     _call(dy, stream, load_library().rtq_act_fp8_backward, _ptr(dy), dyt, _ptr(h_codes), _ptr(h_scale), st, rows, d,
           act, _ptr(dh))
     return dh
+
+
+# ------------------------------------------------------------------ around the 8-bit layers of an MLP block
+
+def rmsnorm_forward(x, gamma, eps: float, residual=None, h=None, codes=None, scale=None, y=None, stream=None):
+    """n = h / sqrt(mean h^2 + eps) gamma for rows of h = x, or of h = x + residual, which is written to h [rows][d]
+    (residual's type; h may be residual).  n comes back quantised, as codes [rows][d] (e4m3) and scale [groups][rows],
+    as y [rows][d] (x's type), or as both."""
+    floats = _types()[0]
+    xt = _operand(x, "x", floats)
+    rows, d = x.shape
+    gt = _operand(gamma, "gamma", floats, (d,), x)
+    if (residual is None) != (h is None):
+        raise ValueError("residual and h are given together or not at all")
+    if (codes is None) != (scale is None) or (y is None and codes is None):
+        raise ValueError("give y, or codes and scale, or all of them")
+    rt, st = xt, RTQ_F32
+    if residual is not None:
+        rt = _operand(residual, "residual", floats, x.shape, x)
+        _operand(h, "h", {residual.dtype: rt}, x.shape, x)
+    if codes is not None:
+        _operand(codes, "codes", _types()[2], x.shape, x)
+        st = _operand(scale, "scale", _types()[3], (fp8_groups(d), rows), x)
+    if y is not None:
+        _operand(y, "y", {x.dtype: xt}, x.shape, x)
+    _call(x, stream, load_library().rtq_rmsnorm_forward, _ptr(x), xt, _ptr(residual), rt, rows, d, _ptr(gamma), gt, eps,
+          _ptr(h), _ptr(y), _ptr(codes), _ptr(scale), st)
+    return x if h is None else h
+
+
+def rmsnorm_backward_workspace(rows: int, d: int) -> int:
+    return int(load_library().rtq_rmsnorm_backward_workspace(rows, d))
+
+
+def rmsnorm_backward(dn, h, gamma, eps: float, dh, dgamma=None, dresidual=None, accumulate: bool = False, workspace=None,
+                     stream=None):
+    """dh [rows][d] (h's type), the gradient of h and thus of x and residual, from the gradient dn [rows][d] of
+    rmsnorm_forward's n and the residual stream's own, dresidual (h's type, or None); dh may be dresidual, or dn if their
+    types agree.  dgamma [d] (float32 or bfloat16) is written, or added to with accumulate."""
+    floats = _types()[0]
+    dnt = _operand(dn, "dn", floats)
+    rows, d = dn.shape
+    ht = _operand(h, "h", floats, dn.shape, dn)
+    gt = _operand(gamma, "gamma", floats, (d,), dn)
+    _operand(dh, "dh", {h.dtype: ht}, dn.shape, dn)
+    if dresidual is not None:
+        _operand(dresidual, "dresidual", {h.dtype: ht}, dn.shape, dn)
+    dgt, ws = RTQ_F32, None
+    if dgamma is not None:
+        dgt = _operand(dgamma, "dgamma", floats, (d,), dn)
+        ws = _workspace(workspace, dn, stream, rmsnorm_backward_workspace, rows, d)
+    _call(dn, stream, load_library().rtq_rmsnorm_backward, _ptr(dn), dnt, _ptr(h), ht, _ptr(dresidual), rows, d, _ptr(gamma),
+          gt, eps, _ptr(dh), _ptr(dgamma), dgt, 1 if accumulate else 0, _ptr(ws),
+          0 if ws is None else ws.numel() * ws.element_size())
+    return dh
+
+
+def fp8_glu_workspace(T: int, N: int, K: int) -> int:
+    return int(load_library().rtq_fp8_glu_workspace(T, N, K))
+
+
+def fp8_glu(x_codes, x_scale, w_codes, w_scale, act: int, y=None, y_codes=None, y_scale=None, h_codes=None, h_scale=None,
+            workspace=None, stream=None):
+    """y = f(g) u with [g u] = x W^T of row-group codes x [T][K] and block codes W [2 N][K], the gate's N rows first (N a
+    multiple of 128); f is RTQ_ACT_GELU_TANH, RTQ_ACT_GELU or RTQ_ACT_SILU.  y [T][N] comes back as y (float32 or
+    bfloat16), or quantised as y_codes, y_scale.  With h_codes [T][2 N] and h_scale, [g u] is kept in 8 bits, for
+    glu_fp8_backward."""
+    e4m3 = _types()[2]
+    rows, K, st = _fp8_weight(w_codes, w_scale, x_codes)
+    if rows % 256 != 0:
+        raise ValueError(f"w_codes: {rows} rows, expected two projections of a multiple of {FP8_BLOCK} each")
+    T, N = x_codes.shape[0], rows // 2
+    _operand(x_codes, "x_codes", e4m3, (T, K))
+    scales = {w_scale.dtype: st}
+    _operand(x_scale, "x_scale", scales, (fp8_groups(K), T), x_codes)
+    if (y_codes is None) != (y_scale is None) or (y is None) == (y_codes is None):
+        raise ValueError("give either y, or y_codes and y_scale")
+    if (h_codes is None) != (h_scale is None):
+        raise ValueError("h_codes and h_scale are given together or not at all")
+    yt = RTQ_F32
+    if y is not None:
+        yt = _operand(y, "y", _types()[0], (T, N), x_codes)
+    else:
+        _operand(y_codes, "y_codes", e4m3, (T, N), x_codes)
+        _operand(y_scale, "y_scale", scales, (fp8_groups(N), T), x_codes)
+    if h_codes is not None:
+        _operand(h_codes, "h_codes", e4m3, (T, 2 * N), x_codes)
+        _operand(h_scale, "h_scale", scales, (fp8_groups(2 * N), T), x_codes)
+    ws = _workspace(workspace, x_codes, stream, fp8_glu_workspace, T, N, K)
+    _call(x_codes, stream, load_library().rtq_fp8_glu, _ptr(x_codes), _ptr(x_scale), T, _ptr(w_codes), _ptr(w_scale), st, N, K,
+          act, _ptr(h_codes), _ptr(h_scale), _ptr(y), yt, _ptr(y_codes), _ptr(y_scale), _ptr(ws),
+          ws.numel() * ws.element_size())
+    return y if y is not None else (y_codes, y_scale)
+
+
+def glu_fp8_backward(dy, h_codes, h_scale, act: int, dh=None, dh_codes=None, dh_scale=None, stream=None):
+    """[dg du] = [dy u^ f'(g^), dy f(g^)] from dy [T][N] and fp8_glu's checkpoint, as dh [T][2 N] (dy's type; fp8_wgrad
+    takes it in bfloat16) and/or quantised, as dh_codes [T][2 N] (e4m3 or e5m2) and dh_scale, for fp8_dgrad."""
+    dyt = _operand(dy, "dy", _types()[0])
+    T, N = dy.shape
+    _operand(h_codes, "h_codes", _types()[2], (T, 2 * N), dy)
+    st = _operand(h_scale, "h_scale", _types()[3], (fp8_groups(2 * N), T), dy)
+    if (dh_codes is None) != (dh_scale is None) or (dh is None and dh_codes is None):
+        raise ValueError("give dh, or dh_codes and dh_scale, or all of them")
+    gt = RTQ_E4M3
+    if dh is not None:
+        _operand(dh, "dh", {dy.dtype: dyt}, (T, 2 * N), dy)
+    if dh_codes is not None:
+        gt = _operand(dh_codes, "dh_codes", _types()[1], (T, 2 * N), dy)
+        _operand(dh_scale, "dh_scale", {h_scale.dtype: st}, (fp8_groups(2 * N), T), dy)
+    _call(dy, stream, load_library().rtq_glu_fp8_backward, _ptr(dy), dyt, _ptr(h_codes), _ptr(h_scale), st, T, N, act, _ptr(dh),
+          _ptr(dh_codes), gt, _ptr(dh_scale))
+    return dh if dh is not None else (dh_codes, dh_scale)
+
+
+class TensorList:
+    """Tensors (float32 or bfloat16, contiguous, on one GPU) as grad_norm and grad_clip take them, and where grad_clip puts
+    its results: outs, of the same shapes and types, or the tensors themselves.  It holds them; tensors that a program
+    replaces need a new list."""
+
+    def __init__(self, tensors, outs=None):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("no tensors")
+        self.outs = self.tensors if outs is None else list(outs)
+        if len(self.outs) != len(self.tensors):
+            raise ValueError(f"{len(self.outs)} outs for {len(self.tensors)} tensors")
+        floats, like, n = _types()[0], self.tensors[0], len(self.tensors)
+        self._c, self._outs, self.count = (_Tensor * n)(), (ctypes.c_void_p * n)(), n
+        for i, (t, o) in enumerate(zip(self.tensors, self.outs)):
+            code = _operand(t, f"tensors[{i}]", floats, t.shape, like)
+            _operand(o, f"outs[{i}]", {t.dtype: code}, t.shape, like)
+            self._c[i] = _Tensor(t.data_ptr(), t.numel(), code)
+            self._outs[i] = o.data_ptr()
+
+
+def grad_norm_workspace(tensors: TensorList) -> int:
+    return int(load_library().rtq_grad_norm_workspace(tensors._c, tensors.count))
+
+
+def grad_norm(tensors: TensorList, norm, workspace=None, stream=None):
+    """norm (one float32 on the GPU) = the 2-norm of all tensors together."""
+    like = tensors.tensors[0]
+    _operand(norm, "norm", {_torch().float32: RTQ_F32}, (1,) if norm.dim() else (), like)
+    ws = _workspace(workspace, like, stream, grad_norm_workspace, tensors)
+    _call(like, stream, load_library().rtq_grad_norm, tensors._c, tensors.count, _ptr(norm), _ptr(ws),
+          ws.numel() * ws.element_size())
+    return norm
+
+
+def grad_clip(tensors: TensorList, norm, most: float, stream=None):
+    """Each tensor times min(1, most / (norm + 1e-6)), to the list's outs."""
+    like = tensors.tensors[0]
+    _operand(norm, "norm", {_torch().float32: RTQ_F32}, (1,) if norm.dim() else (), like)
+    _call(like, stream, load_library().rtq_grad_clip, tensors._c, tensors._outs, tensors.count, _ptr(norm), most)
+    return tensors.outs

@@ -163,5 +163,16 @@ __device__ __forceinline__ void store8(void* y, int64_t i, const float* v) {
     }
 }
 
+
+// One row's 8 elements of a lane -> 8 codes; returns the group's exponent (the same in its 16 lanes).
+template <bool kE5M2>
+__device__ __forceinline__ int quantise8(const float* v, uint2* codes) {
+    const int e = scale_exponent<kE5M2>(max16(amax8(v)));
+    const float inv = pow2(-e);
+    codes->x = encode4<kE5M2>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    codes->y = encode4<kE5M2>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    return e;
+}
+
 }  // namespace fp8
 }  // namespace rtq

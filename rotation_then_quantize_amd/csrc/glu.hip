@@ -1,0 +1,208 @@
+// glu.hip -- the gated feed-forward's first half on gfx950, y = f(g) u with [g u] = x W^T from 8-bit codes, and its
+// backward pass from the 8-bit checkpoint of [g u]:
+//
+//   dg = dy u^ f'(g^),  du = dy f(g^)
+//
+// The backward pass is one pass over HBM: 4 bytes read and 6 written for each channel and token.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "block_internal.h"
+#include "fp8_act.h"
+#include "fp8_device.h"
+#include "fp8_internal.h"
+#include "rtq_internal.h"
+
+namespace rtq {
+namespace {
+
+using namespace fp8;
+
+constexpr int kThreads = 256;
+constexpr int kWaveCols = 512;   // a wave's channels: four groups of 16 lanes, 8 channels a lane
+
+// y = f(g) u from the sums [T][2 N], codes and scales on the way.  A wave takes 512 channels of a token.
+struct FinishParams {
+    const float* h;
+    int64_t T;
+    int N;
+    int col_waves;
+    void* h_codes;
+    void* h_scale;
+    void* y;
+    bool y_bf16;
+    void* y_codes;
+    void* y_scale;
+    bool e8m0;
+};
+
+template <int kAct>
+__global__ void __launch_bounds__(kThreads)
+glu_finish_kernel(FinishParams p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = block_index() * (kThreads / 64) + (threadIdx.x >> 6);
+    const int64_t t = wave / p.col_waves;
+    const int c = static_cast<int>(wave % p.col_waves) * kWaveCols + lane * 8;
+    if (t >= p.T) return;
+    const bool in = c < p.N;   // N is a multiple of 128: a group's lanes are all in or all out
+    Row8<false> rg, ru;
+    rg.zero();
+    ru.zero();
+    const int64_t at = t * 2 * p.N + c;
+    if (in) {
+        rg.load(p.h, at);
+        ru.load(p.h, at + p.N);
+    }
+    float g[8], u[8];
+    rg.get(g);
+    ru.get(u);
+    uint2 q;
+    auto put_scale = [&](void* s, int64_t group, int e) {
+        if (in && (lane & 15) == 0) store_scale(s, p.e8m0, group * p.T + t, e);
+    };
+    if (p.h_codes != nullptr) {
+        uint8_t* codes = static_cast<uint8_t*>(p.h_codes) + at;
+        int e = quantise8<false>(g, &q);
+        if (in) *reinterpret_cast<uint2*>(codes) = q;
+        put_scale(p.h_scale, c / kFp8Block, e);
+        e = quantise8<false>(u, &q);
+        if (in) *reinterpret_cast<uint2*>(codes + p.N) = q;
+        put_scale(p.h_scale, (p.N + c) / kFp8Block, e);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = act_value<kAct>(g[i]) * u[i];
+    const int64_t out = t * p.N + c;
+    if (p.y != nullptr) {
+        if (in && p.y_bf16) store8<true>(p.y, out, g);
+        if (in && !p.y_bf16) store8<false>(p.y, out, g);
+    } else {
+        const int e = quantise8<false>(g, &q);
+        if (in) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y_codes) + out) = q;
+        put_scale(p.y_scale, c / kFp8Block, e);
+    }
+}
+
+template <typename F>
+hipError_t with_act(int act, F f) {
+    switch (act) {
+        case RTQ_ACT_GELU_TANH: return f(std::integral_constant<int, RTQ_ACT_GELU_TANH>{});
+        case RTQ_ACT_GELU: return f(std::integral_constant<int, RTQ_ACT_GELU>{});
+        case RTQ_ACT_SILU: return f(std::integral_constant<int, RTQ_ACT_SILU>{});
+        default: return hipErrorInvalidValue;
+    }
+}
+
+size_t sums_bytes(int64_t T, int N) { return (static_cast<size_t>(T) * 2 * N * sizeof(float) + 255) / 256 * 256; }
+
+// A wave takes 512 channels of a token: their gradients' two parts, 512 channels of the gate and of the other.
+template <bool kBF16, bool kE8M0, bool kE5M2, int kAct>
+__global__ void __launch_bounds__(kThreads)
+glu_backward_kernel(const void* dy, const uint8_t* __restrict__ h_codes, const void* __restrict__ h_scale, int64_t T, int N,
+                    int col_waves, void* dh, void* dh_codes, void* dh_scale) {
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = block_index() * (kThreads / 64) + (threadIdx.x >> 6);
+    const int64_t t = wave / col_waves;
+    const int c = static_cast<int>(wave % col_waves) * kWaveCols + lane * 8;
+    if (t >= T) return;
+    const bool in = c < N;
+    const int64_t at = t * 2 * N + c;
+    uint2 qg = {0u, 0u}, qu = {0u, 0u};
+    Row8<kBF16> d;
+    d.zero();
+    float sg = 1.f, su = 1.f;
+    if (in) {
+        qg = *reinterpret_cast<const uint2*>(h_codes + at);
+        qu = *reinterpret_cast<const uint2*>(h_codes + at + N);
+        d.load(dy, t * N + c);
+        sg = load_scale<kE8M0>(h_scale, static_cast<int64_t>(c / kFp8Block) * T + t);
+        su = load_scale<kE8M0>(h_scale, static_cast<int64_t>((N + c) / kFp8Block) * T + t);
+    }
+    float g[8], u[8], v[8];
+    decode4<false>(qg.x, g);
+    decode4<false>(qg.y, g + 4);
+    decode4<false>(qu.x, u);
+    decode4<false>(qu.y, u + 4);
+    d.get(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = g[i] * sg;
+        g[i] = v[i] * (u[i] * su) * act_slope<kAct>(x);
+        u[i] = v[i] * act_value<kAct>(x);
+    }
+    if (dh != nullptr && in) {
+        store8<kBF16>(dh, at, g);
+        store8<kBF16>(dh, at + N, u);
+    }
+    if (dh_codes != nullptr) {
+        uint2 q;
+        uint8_t* codes = static_cast<uint8_t*>(dh_codes) + at;
+        const int eg = quantise8<kE5M2>(g, &q);
+        if (in) *reinterpret_cast<uint2*>(codes) = q;
+        const int eu = quantise8<kE5M2>(u, &q);
+        if (in) *reinterpret_cast<uint2*>(codes + N) = q;
+        if (in && (lane & 15) == 0) {
+            store_scale(dh_scale, kE8M0, static_cast<int64_t>(c / kFp8Block) * T + t, eg);
+            store_scale(dh_scale, kE8M0, static_cast<int64_t>((N + c) / kFp8Block) * T + t, eu);
+        }
+    }
+}
+
+template <bool kBF16, bool kE8M0, bool kE5M2>
+hipError_t backward(const GluBackwardArgs& a, hipStream_t stream) {
+    const int col_waves = (a.N + kWaveCols - 1) / kWaveCols;
+    const int64_t waves = a.T * col_waves;
+    return with_act(a.act, [&](auto act) {
+        glu_backward_kernel<kBF16, kE8M0, kE5M2, decltype(act)::value>
+            <<<grid_of((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(
+                a.dy, static_cast<const uint8_t*>(a.h_codes), a.h_scale, a.T, a.N, col_waves, a.dh, a.dh_codes, a.dh_scale);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+size_t fp8_glu_workspace_bytes(int64_t T, int N, int K) {
+    return sums_bytes(T, N) + fp8_gemm_workspace_bytes(T, 2 * N, K, false);
+}
+
+hipError_t launch_fp8_glu(const GluArgs& a, hipStream_t stream) {
+    const size_t sums = sums_bytes(a.T, a.N);
+    Fp8GemmArgs g{};
+    g.a = a.x;
+    g.a_scale = a.x_scale;
+    g.w = a.w;
+    g.w_scale = a.w_scale;
+    g.e8m0 = a.e8m0;
+    g.M = a.T;
+    g.N = 2 * a.N;
+    g.R = a.K;
+    g.y = a.workspace;
+    g.workspace = static_cast<uint8_t*>(a.workspace) + sums;
+    g.ws_bytes = a.ws_bytes - sums;
+    const hipError_t e = launch_fp8_gemm(g, stream);
+    if (e != hipSuccess) return e;
+    const int col_waves = (a.N + kWaveCols - 1) / kWaveCols;
+    const int64_t waves = a.T * col_waves;
+    const FinishParams p{static_cast<const float*>(a.workspace), a.T, a.N, col_waves, a.h_codes, a.h_scale, a.y, a.y_bf16,
+                         a.y_codes, a.y_scale, a.e8m0};
+    return with_act(a.act, [&](auto act) {
+        glu_finish_kernel<decltype(act)::value><<<grid_of((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_glu_backward(const GluBackwardArgs& a, hipStream_t stream) {
+    auto pick = [&](auto bf16, auto e8m0) {
+        constexpr bool kB = decltype(bf16)::value, k8 = decltype(e8m0)::value;
+        return a.e5m2 ? backward<kB, k8, true>(a, stream) : backward<kB, k8, false>(a, stream);
+    };
+    constexpr auto yes = std::true_type{};
+    constexpr auto no = std::false_type{};
+    if (a.bf16) return a.e8m0 ? pick(yes, yes) : pick(yes, no);
+    return a.e8m0 ? pick(no, yes) : pick(no, no);
+}
+
+}  // namespace rtq
