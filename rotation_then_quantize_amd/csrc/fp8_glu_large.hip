@@ -1,0 +1,455 @@
+// fp8_glu_large.hip -- the gated feed-forward's product for many tokens and channels: y = f(g) u, [g u] = x W^T, with 256
+// tokens by 128 channels per workgroup, their codes and scales made from the sums in registers.
+//
+// The product is the large one's (fp8_gemm_large.hip): 8 waves, each 128 x 64 sums in 8 x 4 tiles of
+// v_mfma_f32_16x16x128_f8f6f4, one block of 128 of the reduction a stage, two stages in LDS, loaded straight into it two
+// stages ahead over the ends of tiles, persistent workgroups.  What differs:
+//
+//   - The 256 weight rows of a stage are 128 of the gate and the same 128 channels' of the other projection, laid so that
+//     a wave's column tiles 0 and 1 are 32 channels' gates and 2 and 3 their partners: g and u of a channel and token meet
+//     in one lane.
+//   - A wave needs two weight scales a stage.  fp32: the row's scale and the two factors are read apart and multiplied
+//     when used (two multiplies a row tile; tables of both products would take eight more registers, and there are none).
+//     E8M0: four rows' bytes a register, the two weights' bytes in one, chosen by the instruction.
+//   - The epilogue: f(g) u, the largest magnitudes of 32 channels each, whose exponents the four waves of a group of 128
+//     exchange through LDS as bytes (the scale's exponent is monotone in the magnitude), and codes.  Four row tiles at a
+//     time, so that f(g) u is computed once and fits beside the sums; one barrier each.  Codes go through a wave's 2 KB of
+//     LDS, so that stores write runs of 32 bytes a token (of 128 with the other waves').
+//
+// Without the fusion [g u] would be written and read again in fp32: 4608 x 4096 -> 2 x 16384, 1.2 GB.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "fp8_glu.h"
+#include "fp8_internal.h"
+#include "rtq_internal.h"
+
+namespace rtq {
+namespace {
+
+using namespace fp8;
+
+constexpr int kXcds = 8;
+constexpr int kTileM = 256, kChannels = 128, BN = 2 * kChannels;
+constexpr int kWavesM = 2, kWavesN = 4, kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
+constexpr int kRing = 2 * (kTileM + BN) * BK;
+constexpr int kScaleBytes = 2 * 2 * kThreads * static_cast<int>(sizeof(float));   // [slot][tokens', weights'][thread]
+constexpr int kStageOut = kWaves * 2048;
+constexpr int kBytes = 3 * kTileM * kWavesN;                                      // exponents [y, g, u][token][wave]
+constexpr int kLds = kRing + kScaleBytes + kStageOut + kBytes;
+
+// Tile index within the XCD-ordered sequence -> (tile_m, tile_n), in bands of 8 N-tiles.
+__device__ __forceinline__ void tile_of(int lin, int tiles_m, int tiles_n, int* tm, int* tn) {
+    constexpr int kBand = 8;
+    const int band = lin / (kBand * tiles_m);
+    const int in_band = lin % (kBand * tiles_m);
+    const int band_w = min(kBand, tiles_n - band * kBand);
+    *tm = in_band / band_w;
+    *tn = band * kBand + in_band % band_w;
+}
+
+template <bool kE8M0>
+__device__ __forceinline__ uint32_t load_raw(const void* s, int64_t i) {
+    return kE8M0 ? static_cast<const uint8_t*>(s)[i] : static_cast<const uint32_t*>(s)[i];
+}
+// The same value, computed again where it is used, so that the K loop keeps no register for it.
+__device__ __forceinline__ int again(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+struct LargeParams {
+    GluParams g;
+    int full;      // tiles [0, full) are taken whole; the rest as two halves of their tokens
+};
+
+// Tiles of BM tokens: kTileM, or half of that.
+template <int BM, bool kE8M0>
+__device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds, int first, int end, int stride) {
+    constexpr int WM = BM / kWavesM, TM = WM / 16, TN = 4;
+    constexpr int kABytes = BM * BK, kStage = kABytes + BN * BK;
+    constexpr int kALoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves;   // 1 KB loads per wave
+    constexpr int kHalves = kTileM / BM;                                  // tiles of BM tokens per whole tile
+    static_assert(TM == 4 || TM == 8, "row tiles");
+    const GluParams& p = lp.g;
+    const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+    using Scale = std::conditional_t<kE8M0, uint8_t, float>;
+    Scale* s_scale = reinterpret_cast<Scale*>(lds + kRing);               // [slot][tokens' kThreads, weights' kThreads]
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / kWavesN, wn = wave % kWavesN;
+    const int g = lane >> 4, l15 = lane & 15;
+    const int nk = (p.K + BK - 1) / BK;
+
+    if (first >= end) return;
+    auto place = [&](int lin, int64_t* m0, int* n0) {
+        int tm, tn;
+        tile_of(lin / kHalves, p.tiles_t, p.tiles_n, &tm, &tn);
+        *m0 = static_cast<int64_t>(tm) * kTileM + (lin % kHalves) * BM;
+        *n0 = tn * kChannels;
+    };
+    // The loads run two stages ahead of the products, over the ends of tiles: their own tile and block.  Past the last
+    // tile the descriptors are empty, and loads give zeros that nothing uses.
+    int c_kb = 0, c_n0 = 0;
+    int64_t c_m0 = 0;
+    v4i rsa, rsw;
+    const int second = wave >= kWaves / 2 ? 1 : 0;   // this wave loads the other projection's rows
+    auto set_cursor = [&](int lin) {
+        const bool any = lin < end;
+        if (any) place(lin, &c_m0, &c_n0);
+        c_kb = 0;
+        const int rows_a = any ? static_cast<int>(max<int64_t>(0, min<int64_t>(BM, p.T - c_m0))) : 0;
+        const int rows_w = any ? kChannels : 0;
+        rsa = make_rsrc(p.x + c_m0 * p.K, static_cast<uint32_t>(rows_a) * static_cast<uint32_t>(p.K));
+        rsw = make_rsrc(p.w + (static_cast<int64_t>(second) * p.N + c_n0) * p.K, static_cast<uint32_t>(rows_w) * static_cast<uint32_t>(p.K));
+    };
+
+    // Load geometry as in the large product: instruction q of wave w fills LDS rows 8 (8 q + w) .. +8 of an operand, lane L
+    // the 16 bytes at 16 L; chunk c of row r sits at c ^ ((r >> 1) & 7).  LDS weight row 64 q + 16 j + l is channel
+    // 32 q + 16 (j % 2) + l of the gate (j < 2) or of its partner.
+    const int kcol = ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) << 4;
+    const uint32_t a_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * p.K + kcol);
+    const uint32_t w_off = static_cast<uint32_t>((8 * (wave % (kWaves / 2)) + (lane >> 3)) * p.K + kcol);
+    const uint32_t a_step = static_cast<uint32_t>(8 * kWaves * p.K), w_step = a_step / 2;   // rows q -> q + 1
+    const uint32_t wave_lds = static_cast<uint32_t>(wave * 1024);
+
+    // The stage's scales, written to LDS a stage ahead: thread t's are those of token t % BM, where a lane reads its row
+    // tiles' in one run, and of the gate's block (t < 256) or its partner's, next to each other.
+    const int s_row = tid % WM;
+    const int s_at = tid / BM * BM + (tid % BM / WM * 16 + (s_row & 15)) * TM + (s_row >> 4);
+    const int s_wat = kThreads + tid % 256 * 2 + tid / 256;
+    constexpr int kScaleSize = kE8M0 ? 1 : 4;
+    uint32_t r_a = 0u, r_w = 0u;   // as loaded: converting them here would wait for the loads just issued
+    auto load_scales = [&]() {
+        const int m = static_cast<int>(min<int64_t>(c_m0 + tid % BM, p.T - 1));
+        const uint8_t* sa = static_cast<const uint8_t*>(p.x_scale) + static_cast<int64_t>(c_kb) * p.T * kScaleSize;
+        const uint8_t* sw = static_cast<const uint8_t*>(p.w_scale) +
+                            (static_cast<int64_t>((second * p.N + c_n0) / kFp8Block) * nk + c_kb) * kScaleSize;
+        r_a = load_raw<kE8M0>(sa, m);
+        r_w = load_raw<kE8M0>(sw, 0);
+    };
+    auto write_scales = [&](int slot) {
+        if constexpr (kE8M0) {
+            s_scale[slot * 2 * kThreads + s_at] = static_cast<uint8_t>(r_a);
+            s_scale[slot * 2 * kThreads + s_wat] = static_cast<uint8_t>(r_w);
+        } else {
+            s_scale[slot * 2 * kThreads + s_at] = __uint_as_float(r_a);
+            s_scale[slot * 2 * kThreads + s_wat] = __uint_as_float(r_w);
+        }
+    };
+    auto issue = [&](int slot) {   // the cursor's stage, and the cursor moves on
+        const int kb = c_kb;
+        const uint32_t base = lds_base + static_cast<uint32_t>(slot * kStage) + wave_lds;
+        // past the row's end: an offset that every descriptor refuses (loads then give zeros)
+        const uint32_t k0 = kb * BK + kcol < p.K ? static_cast<uint32_t>(kb * BK) : kOob;
+#pragma unroll
+        for (int q = 0; q < kALoads; ++q) load_to_lds(rsa, a_off + q * a_step + k0, base + q * kWaves * 1024);
+#pragma unroll
+        for (int q = 0; q < kWLoads; ++q) load_to_lds(rsw, w_off + q * w_step + k0, base + kABytes + q * kWaves * 1024);
+        load_scales();
+        ++c_kb;
+    };
+
+    const uint32_t f0 = static_cast<uint32_t>(l15 * BK + ((g ^ (l15 >> 1)) << 4));
+    const uint32_t f1 = static_cast<uint32_t>(l15 * BK + (((g + 4) ^ (l15 >> 1)) << 4));
+    auto read_rows = [&](const uint8_t* base) {
+        const v4i x = *reinterpret_cast<const v4i*>(base + f0), y = *reinterpret_cast<const v4i*>(base + f1);
+        return v8i{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    };
+    auto read_a = [&](int slot, int i) { return read_rows(lds + slot * kStage + (wm * WM + i * 16) * BK); };
+    auto read_w = [&](int slot, int j) { return read_rows(lds + slot * kStage + kABytes + (wn * 64 + j * 16) * BK); };
+
+    v4f acc[TM][TN];
+    v8i fw[TN], fa[2];
+    // fp32 scales: the sums of the row tile multiplied last, the tokens' scales, the two weights', and the products
+    // carried over the stage's end.  E8M0: four row tiles' bytes a word, this stage's and the next's.
+    v4f d[TN];
+    float sc[TM], sw[2], last[2] = {0.f, 0.f};
+    uint32_t eb[TM / 4], eb_next[TM / 4], ew = 0u, ew_next = 0u;
+    auto read_scales = [&](int slot) {
+        const Scale* q = s_scale + slot * 2 * kThreads;
+        if constexpr (kE8M0) {
+#pragma unroll
+            for (int i = 0; i < TM / 4; ++i) eb_next[i] = reinterpret_cast<const uint32_t*>(q + (wm * 16 + l15) * TM)[i];
+            ew_next = *reinterpret_cast<const uint16_t*>(q + kThreads);
+        } else {
+#pragma unroll
+            for (int i = 0; i < TM / 4; ++i) {
+                const v4f x = reinterpret_cast<const v4f*>(q + (wm * 16 + l15) * TM)[i];
+                sc[4 * i] = x[0];
+                sc[4 * i + 1] = x[1];
+                sc[4 * i + 2] = x[2];
+                sc[4 * i + 3] = x[3];
+            }
+            sw[0] = q[kThreads];
+            sw[1] = q[kThreads + 1];
+        }
+    };
+    auto add = [&](v4f& a, const v4f& x, float s) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = __builtin_fmaf(x[r], s, a[r]);
+    };
+    // E8M0: the scaled product of row tile i and column tile j
+    auto scaled = [&](auto ic, auto jc) {
+        constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[j], fa[i & 1], acc[i][j], 0, 0, j / 2, static_cast<int>(ew),
+                                                                     i % 4, static_cast<int>(eb[i / 4]));
+    };
+
+    // One stage, from `slot`.  What it reads ahead is the next stage of this tile or of the next one; behind the last
+    // stage of all that is whatever the other slot holds, and is not used.
+    auto stage = [&](int slot) {
+        if constexpr (kE8M0) {
+#pragma unroll
+            for (int i = 0; i < TM / 4; ++i) eb[i] = eb_next[i];
+            ew = ew_next;
+        }
+        auto row = [&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            float s[2] = {0.f, 0.f};
+            if constexpr (!kE8M0) {
+                s[0] = i == 0 ? last[0] : sc[i == 0 ? 0 : i - 1] * sw[0];
+                s[1] = i == 0 ? last[1] : sc[i == 0 ? 0 : i - 1] * sw[1];
+            }
+            auto column = [&](auto jc) {
+                constexpr int j = decltype(jc)::value;
+                if constexpr (kE8M0) {
+                    scaled(ic, jc);
+                } else {
+                    // the sums of the row tile before this one, four instructions old
+                    add(acc[i == 0 ? TM - 1 : i - 1][j], d[j], s[j / 2]);
+                    d[j] = mfma<false>(fw[j], fa[i & 1], v4f{0.f, 0.f, 0.f, 0.f});
+                }
+                if constexpr (i == TM - 1) fw[j] = read_w(1 - slot, j);
+            };
+            column(std::integral_constant<int, 0>{});
+            column(std::integral_constant<int, 1>{});
+            column(std::integral_constant<int, 2>{});
+            column(std::integral_constant<int, 3>{});
+            if constexpr (i == 0 && !kE8M0) read_scales(slot);
+            if constexpr (i + 2 < TM) fa[i & 1] = read_a(slot, i + 2);
+            if constexpr (i == TM - 2) {
+                lds_done();          // this wave's last fragments of the stage are in registers
+                wait_vmcnt<0>();     // its part of the next stage, and that stage's scales, have landed
+                write_scales(1 - slot);
+                lds_done();
+                barrier();
+                issue(slot);
+                fa[0] = read_a(1 - slot, 0);
+                if constexpr (kE8M0) read_scales(1 - slot);
+            }
+            if constexpr (i == TM - 1) fa[1] = read_a(1 - slot, 1);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        row(std::integral_constant<int, 0>{});
+        row(std::integral_constant<int, 1>{});
+        row(std::integral_constant<int, 2>{});
+        row(std::integral_constant<int, 3>{});
+        if constexpr (TM == 8) {
+            row(std::integral_constant<int, TM - 4>{});
+            row(std::integral_constant<int, TM - 3>{});
+            row(std::integral_constant<int, TM - 2>{});
+            row(std::integral_constant<int, TM - 1>{});
+        }
+        if constexpr (!kE8M0) {
+            last[0] = sc[TM - 1] * sw[0];
+            last[1] = sc[TM - 1] * sw[1];
+        }
+    };
+
+    // The outputs of row tiles i0 .. i0 + 3: 64 tokens a wave, in which a lane holds 2 x 4 channels of four tokens.
+    auto outputs = [&](auto i0c, int64_t m0, int n0) {
+        constexpr int i0 = decltype(i0c)::value;
+        const int tid_e = again(tid), lane_e = tid_e & 63, g = lane_e >> 4, l15 = lane_e & 15;
+        uint8_t* stg = lds + kRing + kScaleBytes + wave * 2048;
+        uint8_t* bytes = lds + kRing + kScaleBytes + kStageOut;
+        const GluOut& o = p.out;
+        const int64_t cm0 = m0 + wm * WM + i0 * 16;
+        const int cn0 = n0 + wn * 32;
+        float y[4][8];
+        for_act(o.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[i][e] = act_value<decltype(act)::value>(acc[i0 + i][e / 4][e % 4]) * acc[i0 + i][2 + e / 4][e % 4];
+        });
+        if (o.y != nullptr) {
+            if (o.y_bf16) {   // two row tiles at a time, 64 bytes a token; chunk c of row r at c ^ (r & 3)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float* v = y[2 * h + i] + 4 * j;
+                            *reinterpret_cast<uint2*>(stg + (16 * i + l15) * 64 + (((2 * j + (g >> 1)) ^ (l15 & 3)) << 4) + (g & 1) * 8) =
+                                uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                        }
+                    lds_done();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int row = 16 * q + (lane_e >> 2), c = lane_e & 3;
+                        const v4i x = *reinterpret_cast<const v4i*>(stg + row * 64 + ((c ^ (row & 3)) << 4));
+                        const int64_t m = cm0 + 32 * h + row;
+                        if (m < p.T) __builtin_nontemporal_store(x, reinterpret_cast<v4i*>(static_cast<uint16_t*>(o.y) + m * p.N + cn0 + 8 * c));
+                    }
+                    lds_done();
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<v4f*>(stg + l15 * 128 + (((4 * j + g) ^ (l15 & 7)) << 4)) = v4f{y[i][4 * j], y[i][4 * j + 1], y[i][4 * j + 2], y[i][4 * j + 3]};
+                    lds_done();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int row = 8 * q + (lane_e >> 3), c = lane_e & 7;
+                        const v4f x = *reinterpret_cast<const v4f*>(stg + row * 128 + ((c ^ (row & 7)) << 4));
+                        const int64_t m = cm0 + 16 * i + row;
+                        if (m < p.T) __builtin_nontemporal_store(x, reinterpret_cast<v4f*>(static_cast<float*>(o.y) + m * p.N + cn0 + 4 * c));
+                    }
+                    lds_done();
+                }
+            }
+        }
+        const bool codes = o.y_codes != nullptr, keep = o.h_codes != nullptr;
+        if (!codes && !keep) return;
+        // exponents: of this wave's 32 channels, then of the group's 128
+        const int row0 = wm * WM + i0 * 16 + l15;
+        auto value = [&](int kind, int i, int e) { return kind == 0 ? y[i][e] : acc[i0 + i][(kind - 1) * 2 + e / 4][e % 4]; };
+        auto put_byte = [&](auto kindc) {
+            constexpr int kind = decltype(kindc)::value;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = value(kind, i, e);
+                uint32_t m = amax8(v);
+                m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
+                m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+                if (g == i) bytes[(kind * kTileM + row0 + 16 * i) * kWavesN + wn] = static_cast<uint8_t>(exponent_byte(m));
+            }
+        };
+        auto put_codes = [&](auto kindc, void* out, int64_t stride, int column, void* scale, int group) {
+            constexpr int kind = decltype(kindc)::value;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = byte_exponent(max_byte(reinterpret_cast<const uint32_t*>(bytes)[kind * kTileM + row0 + 16 * i]));
+                const float inv = pow2(-e);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<uint32_t*>(stg + (16 * i + l15) * 32 + 16 * j + 4 * g) =
+                        encode4<false>(value(kind, i, 4 * j) * inv, value(kind, i, 4 * j + 1) * inv, value(kind, i, 4 * j + 2) * inv, value(kind, i, 4 * j + 3) * inv);
+                const int64_t m = cm0 + 16 * i + l15;
+                if (wn == kind && g == i && m < p.T) store_scale(scale, kE8M0, group * p.T + m, e);
+            }
+            lds_done();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int row = 32 * q + (lane_e >> 1);
+                const v4i x = *reinterpret_cast<const v4i*>(stg + row * 32 + (lane_e & 1) * 16);
+                const int64_t m = cm0 + row;
+                if (m < p.T) __builtin_nontemporal_store(x, reinterpret_cast<v4i*>(static_cast<uint8_t*>(out) + m * stride + column + (lane_e & 1) * 16));
+            }
+            lds_done();
+        };
+        constexpr auto kY = std::integral_constant<int, 0>{};
+        constexpr auto kG = std::integral_constant<int, 1>{};
+        constexpr auto kU = std::integral_constant<int, 2>{};
+        if (codes) put_byte(kY);
+        if (keep) {
+            put_byte(kG);
+            put_byte(kU);
+        }
+        lds_done();
+        barrier();
+        if (codes) put_codes(kY, o.y_codes, p.N, cn0, o.y_scale, n0 / kFp8Block);
+        if (keep) {
+            put_codes(kG, o.h_codes, 2 * static_cast<int64_t>(p.N), cn0, o.h_scale, n0 / kFp8Block);
+            put_codes(kU, o.h_codes, 2 * static_cast<int64_t>(p.N), p.N + cn0, o.h_scale, (p.N + n0) / kFp8Block);
+        }
+    };
+
+    set_cursor(first);
+    issue(0);
+    wait_vmcnt<0>();
+    write_scales(0);
+    issue(1);
+    lds_done();
+    barrier();
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fw[j] = read_w(0, j);
+    fa[0] = read_a(0, 0);
+    fa[1] = read_a(0, 1);
+    if constexpr (kE8M0) read_scales(0);
+    int slot = 0;
+    for (int lin = first; lin < end; lin += stride) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            d[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < TM; ++i) acc[i][j] = d[j];
+        }
+        last[0] = last[1] = 0.f;
+        // nk - 2 stages that load this tile's, then two that load the next tile's (the stage stays one basic block)
+        for (int half = 0; half < 2; ++half) {
+            for (int s = half == 0 ? nk - 2 : 2; s > 0; --s) {
+                stage(slot);
+                slot = 1 - slot;
+            }
+            if (half == 0) set_cursor(lin + stride);
+        }
+        if constexpr (!kE8M0) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) add(acc[TM - 1][j], d[j], last[j / 2]);
+        }
+        int64_t m0;
+        int n0;
+        place(lin, &m0, &n0);
+        outputs(std::integral_constant<int, 0>{}, m0, n0);
+        if constexpr (TM == 8) outputs(std::integral_constant<int, TM - 4>{}, m0, n0);
+    }
+    wait_vmcnt<0>();   // nothing is still writing LDS when the workgroup's next tiles, or another workgroup, use it
+}
+
+template <bool kE8M0>
+__global__ void __launch_bounds__(kThreads, 1)
+glu_large_kernel(LargeParams p) {
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    // Tiles are split into 8 contiguous ranges, one per XCD (block b runs on XCD b % 8); the blocks of an XCD walk their
+    // range together, in bands of 8 N-tiles, and share operand panels in that L2.
+    const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds, stride = gridDim.x / kXcds;
+    const int per = (p.full + kXcds - 1) / kXcds;
+    large_tiles<kTileM, kE8M0>(p, lds, xcd * per + local, min((xcd + 1) * per, p.full), stride);
+    const int rest = 2 * (p.g.tiles_t * p.g.tiles_n - p.full), rper = (rest + kXcds - 1) / kXcds;
+    if (rest > 0) {
+        __syncthreads();
+        const int r0 = 2 * p.full;
+        large_tiles<kTileM / 2, kE8M0>(p, lds, r0 + xcd * rper + local, r0 + min((xcd + 1) * rper, rest), stride);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_glu_large(const GluParams& g, bool e8m0, hipStream_t stream) {
+    auto kernel = e8m0 ? glu_large_kernel<true> : glu_large_kernel<false>;
+    int per_cu = 0;
+    hipError_t e = kernel_blocks_per_cu(reinterpret_cast<const void*>(kernel), kThreads, kLds, &per_cu);
+    if (e != hipSuccess) return e;
+    LargeParams p{};
+    p.g = g;
+    p.g.tiles_t = static_cast<int>((g.T + kTileM - 1) / kTileM);
+    p.g.tiles_n = g.N / kChannels;
+    const int cus = std::max(kXcds, device_cu_count() / kXcds * kXcds);
+    // whole rounds of whole tiles; a remainder that fills at most half a round goes as halves of 128 tokens
+    const int total = p.g.tiles_t * p.g.tiles_n, rest = total % cus;
+    p.full = rest > 0 && rest <= cus / 2 ? total - rest : total;
+    kernel<<<cus, kThreads, kLds, stream>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace rtq

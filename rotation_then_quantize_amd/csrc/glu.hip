@@ -13,6 +13,7 @@
 #include "block_internal.h"
 #include "fp8_act.h"
 #include "fp8_device.h"
+#include "fp8_glu.h"
 #include "fp8_internal.h"
 #include "rtq_internal.h"
 
@@ -97,6 +98,40 @@ hipError_t with_act(int act, F f) {
 
 size_t sums_bytes(int64_t T, int N) { return (static_cast<size_t>(T) * 2 * N * sizeof(float) + 255) / 256 * 256; }
 
+// The products' sums to the workspace, and the outputs from there.
+hipError_t launch_sums(const GluArgs& a, hipStream_t stream) {
+    const size_t sums = sums_bytes(a.T, a.N);
+    Fp8GemmArgs g{};
+    g.a = a.x;
+    g.a_scale = a.x_scale;
+    g.w = a.w;
+    g.w_scale = a.w_scale;
+    g.e8m0 = a.e8m0;
+    g.M = a.T;
+    g.N = 2 * a.N;
+    g.R = a.K;
+    g.y = a.workspace;
+    g.workspace = static_cast<uint8_t*>(a.workspace) + sums;
+    g.ws_bytes = a.ws_bytes - sums;
+    const hipError_t e = launch_fp8_gemm(g, stream);
+    if (e != hipSuccess) return e;
+    const int col_waves = (a.N + kWaveCols - 1) / kWaveCols;
+    const int64_t waves = a.T * col_waves;
+    const FinishParams p{static_cast<const float*>(a.workspace), a.T, a.N, col_waves, a.h_codes, a.h_scale, a.y, a.y_bf16,
+                         a.y_codes, a.y_scale, a.e8m0};
+    return with_act(a.act, [&](auto act) {
+        glu_finish_kernel<decltype(act)::value><<<grid_of((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
+        return hipGetLastError();
+    });
+}
+
+// How a product runs.
+enum Form : int { kSums, kLarge };
+Form plan(int64_t T, int N, int K) {
+    if (K > kFp8Block && (T + 255) / 256 * (N / 128) >= device_cu_count() / 2) return kLarge;
+    return kSums;
+}
+
 // A wave takes 512 channels of a token: their gradients' two parts, 512 channels of the gate and of the other.
 template <bool kBF16, bool kE8M0, bool kE5M2, int kAct>
 __global__ void __launch_bounds__(kThreads)
@@ -164,34 +199,29 @@ hipError_t backward(const GluBackwardArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+fp8::GluParams glu_params(const GluArgs& a) {
+    fp8::GluParams p{};
+    p.x = static_cast<const uint8_t*>(a.x);
+    p.x_scale = a.x_scale;
+    p.w = static_cast<const uint8_t*>(a.w);
+    p.w_scale = a.w_scale;
+    p.T = a.T;
+    p.N = a.N;
+    p.K = a.K;
+    p.out = fp8::GluOut{a.act, a.h_codes, a.h_scale, a.y, a.y_bf16, a.y_codes, a.y_scale};
+    return p;
+}
+
 size_t fp8_glu_workspace_bytes(int64_t T, int N, int K) {
+    if (T == 0 || plan(T, N, K) != kSums) return 0;
     return sums_bytes(T, N) + fp8_gemm_workspace_bytes(T, 2 * N, K, false);
 }
 
 hipError_t launch_fp8_glu(const GluArgs& a, hipStream_t stream) {
-    const size_t sums = sums_bytes(a.T, a.N);
-    Fp8GemmArgs g{};
-    g.a = a.x;
-    g.a_scale = a.x_scale;
-    g.w = a.w;
-    g.w_scale = a.w_scale;
-    g.e8m0 = a.e8m0;
-    g.M = a.T;
-    g.N = 2 * a.N;
-    g.R = a.K;
-    g.y = a.workspace;
-    g.workspace = static_cast<uint8_t*>(a.workspace) + sums;
-    g.ws_bytes = a.ws_bytes - sums;
-    const hipError_t e = launch_fp8_gemm(g, stream);
-    if (e != hipSuccess) return e;
-    const int col_waves = (a.N + kWaveCols - 1) / kWaveCols;
-    const int64_t waves = a.T * col_waves;
-    const FinishParams p{static_cast<const float*>(a.workspace), a.T, a.N, col_waves, a.h_codes, a.h_scale, a.y, a.y_bf16,
-                         a.y_codes, a.y_scale, a.e8m0};
-    return with_act(a.act, [&](auto act) {
-        glu_finish_kernel<decltype(act)::value><<<grid_of((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
-        return hipGetLastError();
-    });
+    switch (plan(a.T, a.N, a.K)) {
+        case kLarge: return launch_glu_large(glu_params(a), a.e8m0, stream);
+        default: return launch_sums(a, stream);
+    }
 }
 
 hipError_t launch_glu_backward(const GluBackwardArgs& a, hipStream_t stream) {
