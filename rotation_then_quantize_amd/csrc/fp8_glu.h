@@ -51,9 +51,25 @@ __device__ __forceinline__ void for_act(int act, F f) {
 // is the whole group's.
 __device__ __forceinline__ uint32_t exponent_byte(uint32_t amax) { return amax == 0u ? 0u : static_cast<uint32_t>(scale_exponent<false>(amax) + 121); }
 __device__ __forceinline__ int byte_exponent(uint32_t b) { return b == 0u ? 0 : static_cast<int>(b) - 121; }
+// 2^-e of a byte's exponent; for zeros, whose codes do not depend on it, 2^121.
+__device__ __forceinline__ float byte_inverse(uint32_t b) { return __uint_as_float((248u - b) << 23); }
 // The largest of the four bytes of a word.
 __device__ __forceinline__ uint32_t max_byte(uint32_t w) {
     return max(max(w & 0xffu, w >> 8 & 0xffu), max(w >> 16 & 0xffu, w >> 24));
+}
+
+// Bits of the largest magnitude of m and v: one instruction, whose median with infinity is the larger of two numbers, and
+// where one of them is no number the other one.
+__device__ __forceinline__ float magnitude(float m, float v) {
+    return __builtin_amdgcn_fmed3f(m, __builtin_fabsf(v), __builtin_inff());
+}
+
+// m[i]'s maximum over the four 16-lane rows of a wave, in row i: two swaps of halves for four numbers, then one of rows.
+__device__ __forceinline__ uint32_t max_rows(const uint32_t (&m)[4]) {
+    const auto a = __builtin_amdgcn_permlane32_swap(m[0], m[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(m[1], m[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(max(a[0], a[1]), max(b[0], b[1]), false, false);
+    return max(c[0], c[1]);
 }
 
 }  // namespace fp8

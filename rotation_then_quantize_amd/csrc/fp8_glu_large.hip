@@ -323,29 +323,39 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         auto value = [&](int kind, int i, int e) { return kind == 0 ? y[i][e] : acc[i0 + i][(kind - 1) * 2 + e / 4][e % 4]; };
         auto put_byte = [&](auto kindc) {
             constexpr int kind = decltype(kindc)::value;
+            float m[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float v[8];
+                m[i] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = value(kind, i, e);
-                uint32_t m = amax8(v);
-                m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
-                m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
-                if (g == i) bytes[(kind * kTileM + row0 + 16 * i) * kWavesN + wn] = static_cast<uint8_t>(exponent_byte(m));
+                for (int e = 0; e < 8; ++e) m[i] = magnitude(m[i], value(kind, i, e));
             }
+            if (max(max(m[0], m[1]), max(m[2], m[3])) == __builtin_inff()) {   // one branch for the four: with one each their latencies add up
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    m[i] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = __builtin_fabsf(value(kind, i, e));
+                        m[i] = v < __builtin_inff() ? max(m[i], v) : m[i];
+                    }
+                }
+            }
+            const uint32_t mine = max_rows({__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3])});
+            bytes[(kind * kTileM + row0 + 16 * g) * kWavesN + wn] = static_cast<uint8_t>(exponent_byte(mine));
         };
         auto put_codes = [&](auto kindc, void* out, int64_t stride, int column, void* scale, int group) {
             constexpr int kind = decltype(kindc)::value;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int e = byte_exponent(max_byte(reinterpret_cast<const uint32_t*>(bytes)[kind * kTileM + row0 + 16 * i]));
-                const float inv = pow2(-e);
+                const uint32_t b = max_byte(reinterpret_cast<const uint32_t*>(bytes)[kind * kTileM + row0 + 16 * i]);
+                const float inv = byte_inverse(b);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     *reinterpret_cast<uint32_t*>(stg + (16 * i + l15) * 32 + 16 * j + 4 * g) =
                         encode4<false>(value(kind, i, 4 * j) * inv, value(kind, i, 4 * j + 1) * inv, value(kind, i, 4 * j + 2) * inv, value(kind, i, 4 * j + 3) * inv);
                 const int64_t m = cm0 + 16 * i + l15;
-                if (wn == kind && g == i && m < p.T) store_scale(scale, kE8M0, group * p.T + m, e);
+                if (wn == kind && g == i && m < p.T) store_scale(scale, kE8M0, group * p.T + m, byte_exponent(b));
             }
             lds_done();
 #pragma unroll
@@ -353,7 +363,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
                 const int row = 32 * q + (lane_e >> 1);
                 const v4i x = *reinterpret_cast<const v4i*>(stg + row * 32 + (lane_e & 1) * 16);
                 const int64_t m = cm0 + row;
-                if (m < p.T) __builtin_nontemporal_store(x, reinterpret_cast<v4i*>(static_cast<uint8_t*>(out) + m * stride + column + (lane_e & 1) * 16));
+                if (m < p.T) *reinterpret_cast<v4i*>(static_cast<uint8_t*>(out) + m * stride + column + (lane_e & 1) * 16) = x;
             }
             lds_done();
         };
