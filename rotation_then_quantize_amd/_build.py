@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librtq.so")
 SOURCES = ["rpbh_rows.hip", "rpbh_quant.hip", "gemm_i8.hip", "gemm_lut.hip", "fp8_rows.hip", "fp8_gemm.hip", "fp8_gemm_large.hip", "fp8_small.hip",
-           "fp8_wgrad.hip", "fp8_wgrad_large.hip", "rmsnorm.hip", "glu.hip", "fp8_glu_large.hip", "grads.hip", "rtq_api.cpp", "fp8_api.cpp",
+           "fp8_wgrad.hip", "fp8_wgrad_large.hip", "rmsnorm.hip", "glu.hip", "fp8_glu_large.hip", "fp8_glu_tile.hip", "fp8_glu_small.hip", "grads.hip", "rtq_api.cpp", "fp8_api.cpp",
            "block_api.cpp", "rtq_host.cpp", "launch_cache.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

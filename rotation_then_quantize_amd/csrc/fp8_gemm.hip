@@ -277,11 +277,12 @@ hipError_t launch_tiles(Fp8GemmParams p, const Fp8GemmArgs& g, int split, hipStr
     p.tiles_n = static_cast<int>((g.N + BT - 1) / BT);
     p.split = split;
     if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(split) * g.M * g.N * sizeof(float)) p.split = 1;
-    if (p.split > 1) p.y = g.workspace;
+    if (p.split > 1) p.y = g.workspace;   // (a caller that adds the parts itself gives the same place for both)
     const int64_t total = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.split;
     kernel<<<grid_of((total + 7) / 8 * 8), threads, lds, stream>>>(p);
     e = hipGetLastError();
-    if (e != hipSuccess || p.split == 1) return e;
+    if (g.parts != nullptr) *g.parts = p.split;
+    if (e != hipSuccess || p.split == 1 || g.parts != nullptr) return e;
     const int64_t n = g.M * g.N;
     fp8_reduce_kernel<<<static_cast<unsigned>((n + 1023) / 1024), 256, 0, stream>>>(static_cast<const float*>(g.workspace),
                                                                                     p.split, n, g.y, g.y_bf16);
@@ -292,6 +293,7 @@ template <bool kTrans, bool kE5M2>
 hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
     const Fp8GemmParams p = fp8_gemm_params(g);
     const Plan how = plan(g.M, g.N, g.R, kTrans);
+    if (g.parts != nullptr) *g.parts = 1;
     switch (how.form) {
         case kSmall: return launch_fp8_small(p, kTrans, kE5M2, stream);
         case kLarge: return launch_fp8_gemm_large(p, kTrans, kE5M2, stream);

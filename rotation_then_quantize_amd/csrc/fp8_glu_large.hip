@@ -11,10 +11,7 @@
 //   - A wave needs two weight scales a stage.  fp32: the row's scale and the two factors are read apart and multiplied
 //     when used (two multiplies a row tile; tables of both products would take eight more registers, and there are none).
 //     E8M0: four rows' bytes a register, the two weights' bytes in one, chosen by the instruction.
-//   - The epilogue: f(g) u, the largest magnitudes of 32 channels each, whose exponents the four waves of a group of 128
-//     exchange through LDS as bytes (the scale's exponent is monotone in the magnitude), and codes.  Four row tiles at a
-//     time, so that f(g) u is computed once and fits beside the sums; one barrier each.  Codes go through a wave's 2 KB of
-//     LDS, so that stores write runs of 32 bytes a token (of 128 with the other waves').
+//   - The epilogue (glu_outputs), four row tiles at a time, with one barrier each where codes are written.
 //
 // Without the fusion [g u] would be written and read again in fp32: 4608 x 4096 -> 2 x 16384, 1.2 GB.
 #include <hip/hip_runtime.h>
@@ -36,8 +33,8 @@ constexpr int kTileM = 256, kChannels = 128, BN = 2 * kChannels;
 constexpr int kWavesM = 2, kWavesN = 4, kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
 constexpr int kRing = 2 * (kTileM + BN) * BK;
 constexpr int kScaleBytes = 2 * 2 * kThreads * static_cast<int>(sizeof(float));   // [slot][tokens', weights'][thread]
-constexpr int kStageOut = kWaves * 2048;
-constexpr int kBytes = 3 * kTileM * kWavesN;                                      // exponents [y, g, u][token][wave]
+constexpr int kStageOut = kWaves * kGluStage;
+constexpr int kBytes = glu_bytes(kTileM);
 constexpr int kLds = kRing + kScaleBytes + kStageOut + kBytes;
 
 // Tile index within the XCD-ordered sequence -> (tile_m, tile_n), in bands of 8 N-tiles.
@@ -260,130 +257,6 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         }
     };
 
-    // The outputs of row tiles i0 .. i0 + 3: 64 tokens a wave, in which a lane holds 2 x 4 channels of four tokens.
-    auto outputs = [&](auto i0c, int64_t m0, int n0) {
-        constexpr int i0 = decltype(i0c)::value;
-        const int tid_e = again(tid), lane_e = tid_e & 63, g = lane_e >> 4, l15 = lane_e & 15;
-        uint8_t* stg = lds + kRing + kScaleBytes + wave * 2048;
-        uint8_t* bytes = lds + kRing + kScaleBytes + kStageOut;
-        const GluOut& o = p.out;
-        const int64_t cm0 = m0 + wm * WM + i0 * 16;
-        const int cn0 = n0 + wn * 32;
-        float y[4][8];
-        for_act(o.act, [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[i][e] = act_value<decltype(act)::value>(acc[i0 + i][e / 4][e % 4]) * acc[i0 + i][2 + e / 4][e % 4];
-        });
-        if (o.y != nullptr) {
-            if (o.y_bf16) {   // two row tiles at a time, 64 bytes a token; chunk c of row r at c ^ (r & 3)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float* v = y[2 * h + i] + 4 * j;
-                            *reinterpret_cast<uint2*>(stg + (16 * i + l15) * 64 + (((2 * j + (g >> 1)) ^ (l15 & 3)) << 4) + (g & 1) * 8) =
-                                uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                        }
-                    lds_done();
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int row = 16 * q + (lane_e >> 2), c = lane_e & 3;
-                        const v4i x = *reinterpret_cast<const v4i*>(stg + row * 64 + ((c ^ (row & 3)) << 4));
-                        const int64_t m = cm0 + 32 * h + row;
-                        if (m < p.T) __builtin_nontemporal_store(x, reinterpret_cast<v4i*>(static_cast<uint16_t*>(o.y) + m * p.N + cn0 + 8 * c));
-                    }
-                    lds_done();
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<v4f*>(stg + l15 * 128 + (((4 * j + g) ^ (l15 & 7)) << 4)) = v4f{y[i][4 * j], y[i][4 * j + 1], y[i][4 * j + 2], y[i][4 * j + 3]};
-                    lds_done();
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int row = 8 * q + (lane_e >> 3), c = lane_e & 7;
-                        const v4f x = *reinterpret_cast<const v4f*>(stg + row * 128 + ((c ^ (row & 7)) << 4));
-                        const int64_t m = cm0 + 16 * i + row;
-                        if (m < p.T) __builtin_nontemporal_store(x, reinterpret_cast<v4f*>(static_cast<float*>(o.y) + m * p.N + cn0 + 4 * c));
-                    }
-                    lds_done();
-                }
-            }
-        }
-        const bool codes = o.y_codes != nullptr, keep = o.h_codes != nullptr;
-        if (!codes && !keep) return;
-        // exponents: of this wave's 32 channels, then of the group's 128
-        const int row0 = wm * WM + i0 * 16 + l15;
-        auto value = [&](int kind, int i, int e) { return kind == 0 ? y[i][e] : acc[i0 + i][(kind - 1) * 2 + e / 4][e % 4]; };
-        auto put_byte = [&](auto kindc) {
-            constexpr int kind = decltype(kindc)::value;
-            float m[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                m[i] = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m[i] = magnitude(m[i], value(kind, i, e));
-            }
-            if (max(max(m[0], m[1]), max(m[2], m[3])) == __builtin_inff()) {   // one branch for the four: with one each their latencies add up
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    m[i] = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float v = __builtin_fabsf(value(kind, i, e));
-                        m[i] = v < __builtin_inff() ? max(m[i], v) : m[i];
-                    }
-                }
-            }
-            const uint32_t mine = max_rows({__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3])});
-            bytes[(kind * kTileM + row0 + 16 * g) * kWavesN + wn] = static_cast<uint8_t>(exponent_byte(mine));
-        };
-        auto put_codes = [&](auto kindc, void* out, int64_t stride, int column, void* scale, int group) {
-            constexpr int kind = decltype(kindc)::value;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t b = max_byte(reinterpret_cast<const uint32_t*>(bytes)[kind * kTileM + row0 + 16 * i]);
-                const float inv = byte_inverse(b);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    *reinterpret_cast<uint32_t*>(stg + (16 * i + l15) * 32 + 16 * j + 4 * g) =
-                        encode4<false>(value(kind, i, 4 * j) * inv, value(kind, i, 4 * j + 1) * inv, value(kind, i, 4 * j + 2) * inv, value(kind, i, 4 * j + 3) * inv);
-                const int64_t m = cm0 + 16 * i + l15;
-                if (wn == kind && g == i && m < p.T) store_scale(scale, kE8M0, group * p.T + m, byte_exponent(b));
-            }
-            lds_done();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int row = 32 * q + (lane_e >> 1);
-                const v4i x = *reinterpret_cast<const v4i*>(stg + row * 32 + (lane_e & 1) * 16);
-                const int64_t m = cm0 + row;
-                if (m < p.T) *reinterpret_cast<v4i*>(static_cast<uint8_t*>(out) + m * stride + column + (lane_e & 1) * 16) = x;
-            }
-            lds_done();
-        };
-        constexpr auto kY = std::integral_constant<int, 0>{};
-        constexpr auto kG = std::integral_constant<int, 1>{};
-        constexpr auto kU = std::integral_constant<int, 2>{};
-        if (codes) put_byte(kY);
-        if (keep) {
-            put_byte(kG);
-            put_byte(kU);
-        }
-        lds_done();
-        barrier();
-        if (codes) put_codes(kY, o.y_codes, p.N, cn0, o.y_scale, n0 / kFp8Block);
-        if (keep) {
-            put_codes(kG, o.h_codes, 2 * static_cast<int64_t>(p.N), cn0, o.h_scale, n0 / kFp8Block);
-            put_codes(kU, o.h_codes, 2 * static_cast<int64_t>(p.N), p.N + cn0, o.h_scale, (p.N + n0) / kFp8Block);
-        }
-    };
-
     set_cursor(first);
     issue(0);
     wait_vmcnt<0>();
@@ -420,8 +293,11 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         int64_t m0;
         int n0;
         place(lin, &m0, &n0);
-        outputs(std::integral_constant<int, 0>{}, m0, n0);
-        if constexpr (TM == 8) outputs(std::integral_constant<int, TM - 4>{}, m0, n0);
+        // four row tiles at a time, so that f(g) u is computed once and fits beside the sums
+        uint8_t* stg = lds + kRing + kScaleBytes;
+        glu_outputs<4, 0, kE8M0>(p, acc, m0, wm * WM, n0, wn, again(tid), stg + wave * kGluStage, stg + kStageOut, kTileM);
+        if constexpr (TM == 8)
+            glu_outputs<4, TM - 4, kE8M0>(p, acc, m0, wm * WM, n0, wn, again(tid), stg + wave * kGluStage, stg + kStageOut, kTileM);
     }
     wait_vmcnt<0>();   // nothing is still writing LDS when the workgroup's next tiles, or another workgroup, use it
 }

@@ -1,0 +1,152 @@
+// fp8_glu_small.hip -- the gated feed-forward's product for at most 16 tokens: bound by the weights' bytes.
+//
+// A workgroup takes 16 kC channels, as many rows of the gate and their partners, and the whole reduction, its 8 waves the blocks of 128 in turn.  Each wave loads its operands straight into the matrix instruction's registers, 16
+// rows of its next block as soon as it has multiplied those before.  The waves' sums meet in LDS, in a fixed order, and y = f(g) u
+// is written from there; where codes are wanted, whose scales go over the channels of several workgroups, the sums are
+// (glu_finish_kernel makes the codes).  A workgroup for the 128 channels of a scale, which needs no second launch, reads at
+// most 32 GB/s on its CU: 1 x 4096, 16384 channels in 39 us, 4096 channels in 33 (25 and 9 so).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "fp8_glu.h"
+#include "fp8_internal.h"
+#include "rtq_internal.h"
+
+namespace rtq {
+namespace {
+
+using namespace fp8;
+
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+
+// sums: [T][2 N] fp32, or nullptr: y is written
+template <int kC, bool kE8M0>
+__global__ void __launch_bounds__(kThreads)
+glu_small_kernel(GluParams p, float* sums) {
+    constexpr int kTiles = 2 * kC, kSums = kTiles * 64;
+    __shared__ __attribute__((aligned(16))) v4f s_sums[kWaves * kSums];   // [wave][tile][lane]
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, l15 = lane & 15;
+    const int K = p.K, blocks = (K + BK - 1) / BK, T = static_cast<int>(p.T);
+
+    // 8 contiguous ranges of channels, one per XCD (workgroup b runs on XCD b % 8); an XCD's workgroups begin at the same
+    // place of their rows, see below (1 x 4096, 16384 channels: 25.3 us, neighbours on different XCDs 32.1)
+    const int total = p.tiles_n, per = (total + 7) / 8;
+    const int b = static_cast<int>(blockIdx.x), local = b / 8, lin = b % 8 * per + local;
+    if (local >= per || lin >= total) return;
+    const int n0 = lin * 16 * kC, channels = min(16 * kC, p.N - n0);
+
+    auto resource = [](const void* base, int64_t bytes) {   // loads past its end give zeros
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, static_cast<int>(bytes), kBufferWord3);
+    };
+    const __amdgpu_buffer_rsrc_t rw[2] = {resource(p.w + static_cast<int64_t>(n0) * K, static_cast<int64_t>(channels) * K),
+                                          resource(p.w + static_cast<int64_t>(p.N + n0) * K, static_cast<int64_t>(channels) * K)};
+    const __amdgpu_buffer_rsrc_t rx = resource(p.x, static_cast<int64_t>(T) * K);
+    const uint32_t off = static_cast<uint32_t>(l15 * K + 16 * g), tile = static_cast<uint32_t>(16 * K);
+
+    v4i lo[kTiles], hi[kTiles];   // chunks g and g + 4 of 16 rows each: the gate's kC tiles, then their partners
+    v4i x0, x1;
+    float sx, sw;                 // sw: lane i holds tile i's
+    const int w_tile = lane % kTiles;
+    const int64_t w_row = static_cast<int64_t>((w_tile / kC * p.N + min(n0 + w_tile % kC * 16, p.N - 16)) / kFp8Block) * blocks;
+    uint32_t o0, o1;
+    auto begin = [&](int kb) {    // the block's offsets; past the last block all reads as zeros
+        const int k = kb * BK + 16 * g;
+        o0 = k < K ? off + static_cast<uint32_t>(kb * BK) : kOob;
+        o1 = k + 64 < K ? off + static_cast<uint32_t>(kb * BK + 64) : kOob;
+    };
+    auto load_tile = [&](int i) {
+        const uint32_t row = static_cast<uint32_t>(i % kC) * tile;
+        lo[i] = __builtin_amdgcn_raw_buffer_load_b128(rw[i / kC], o0 + row, 0, 0);
+        hi[i] = __builtin_amdgcn_raw_buffer_load_b128(rw[i / kC], o1 + row, 0, 0);
+    };
+    auto load_tokens = [&](int kb) {
+        const int kc = min(kb, blocks - 1);
+        x0 = __builtin_amdgcn_raw_buffer_load_b128(rx, o0, 0, 0);
+        x1 = __builtin_amdgcn_raw_buffer_load_b128(rx, o1, 0, 0);
+        const float a = load_scale<kE8M0>(p.x_scale, kc * p.T + min(l15, T - 1)), w = load_scale<kE8M0>(p.w_scale, w_row + kc);
+        sx = kb < blocks ? a : 0.f;   // past the last block no infinity meets the zeros
+        sw = kb < blocks ? w : 0.f;
+    };
+    v4f acc[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    // The wave's blocks: wave + 8 j, j over turns from a place of the XCD's own: rows a power of two apart share memory
+    // channels, and workgroups at the same place of their rows would crowd them (33.6 us).
+    const int turns = (blocks + kWaves - 1) / kWaves, start = b % turns;
+    auto block = [&](int t) {
+        const int j = t + start;
+        return t < turns ? wave + kWaves * (j < turns ? j : j - turns) : blocks;
+    };
+    begin(block(0));
+    load_tokens(block(0));
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) load_tile(i);
+    for (int turn = 0; turn < turns; ++turn) {
+        const v8i a = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        float s[kTiles];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) s[i] = sx * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw), i));
+        const int next = block(turn + 1);
+        begin(next);
+        load_tokens(next);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+            const v8i w = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+            const v4f d = mfma<false>(w, a, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(d[r], s[i], acc[i][r]);
+            load_tile(i);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) s_sums[wave * kSums + i * 64 + lane] = acc[i];
+    __syncthreads();
+    auto sum = [&](int e) {
+        v4f s = s_sums[e];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) s += s_sums[w * kSums + e];
+        return s;
+    };
+    // a wave takes 16 rows: lane l token l % 16, channels 4 (l / 16) .. +4
+    if (sums != nullptr) {
+        const int c = n0 + wave % kC * 16 + 4 * g;
+        if (wave >= kTiles) return;
+        const v4f s = sum(tid);
+        if (l15 < T && c < p.N) *reinterpret_cast<v4f*>(sums + (static_cast<int64_t>(l15) * 2 + wave / kC) * p.N + c) = s;
+        return;
+    }
+    if (wave >= kC) return;
+    const v4f gate = sum(tid), up = sum(tid + 64 * kC);
+    v4f y;
+    for_act(p.out.act, [&](auto act) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = act_value<decltype(act)::value>(gate[r]) * up[r];
+    });
+    store4(p.out.y, p.out.y_bf16, T, p.N, l15, n0 + wave * 16 + 4 * g, y);
+}
+
+}  // namespace
+
+// Channels per workgroup: as many as balance the CUs' rows (13 x 4096, 10880 channels, 680 tiles of 16: three a workgroup, one
+// workgroup on each of 227 CUs, 16.4 us; with two, 84 CUs have two workgroups, 23.3), and of equals the most.
+hipError_t launch_glu_small(GluParams p, bool e8m0, float* sums, hipStream_t stream) {
+    const int tiles = p.N / 16, cus = device_cu_count();
+    auto cost = [&](int c) { return ((tiles + c - 1) / c + cus - 1) / cus * c; };
+    auto go = [&](auto channels) {
+        constexpr int kC = decltype(channels)::value;
+        auto kernel = e8m0 ? glu_small_kernel<kC, true> : glu_small_kernel<kC, false>;
+        p.tiles_n = (tiles + kC - 1) / kC;
+        kernel<<<static_cast<unsigned>((p.tiles_n + 7) / 8 * 8), kThreads, 0, stream>>>(p, sums);
+        return hipGetLastError();
+    };
+    if (cost(3) <= std::min(cost(1), cost(2))) return go(std::integral_constant<int, 3>{});
+    if (cost(2) <= cost(1)) return go(std::integral_constant<int, 2>{});
+    return go(std::integral_constant<int, 1>{});
+}
+
+}  // namespace rtq

@@ -15,6 +15,7 @@
 #include "fp8_device.h"
 #include "fp8_glu.h"
 #include "fp8_internal.h"
+#include "fp8_tile.h"
 #include "rtq_internal.h"
 
 namespace rtq {
@@ -25,9 +26,10 @@ using namespace fp8;
 constexpr int kThreads = 256;
 constexpr int kWaveCols = 512;   // a wave's channels: four groups of 16 lanes, 8 channels a lane
 
-// y = f(g) u from the sums [T][2 N], codes and scales on the way.  A wave takes 512 channels of a token.
+// y = f(g) u from the sums [parts][T][2 N], codes and scales on the way.  A wave takes 512 channels of a token.
 struct FinishParams {
     const float* h;
+    int parts;
     int64_t T;
     int N;
     int col_waves;
@@ -49,17 +51,19 @@ glu_finish_kernel(FinishParams p) {
     const int c = static_cast<int>(wave % p.col_waves) * kWaveCols + lane * 8;
     if (t >= p.T) return;
     const bool in = c < p.N;   // N is a multiple of 128: a group's lanes are all in or all out
-    Row8<false> rg, ru;
-    rg.zero();
-    ru.zero();
     const int64_t at = t * 2 * p.N + c;
-    if (in) {
-        rg.load(p.h, at);
-        ru.load(p.h, at + p.N);
-    }
     float g[8], u[8];
-    rg.get(g);
-    ru.get(u);
+    auto load = [&](float* v, int64_t i) {
+        v4f s[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+        if (in) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) s[q] = sum_parts<v4f>(p.h + i + 4 * q, p.parts, p.T * 2 * p.N);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = s[e / 4][e % 4];
+    };
+    load(g, at);
+    load(u, at + p.N);
     uint2 q;
     auto put_scale = [&](void* s, int64_t group, int e) {
         if (in && (lane & 15) == 0) store_scale(s, p.e8m0, group * p.T + t, e);
@@ -98,9 +102,21 @@ hipError_t with_act(int act, F f) {
 
 size_t sums_bytes(int64_t T, int N) { return (static_cast<size_t>(T) * 2 * N * sizeof(float) + 255) / 256 * 256; }
 
+// The outputs from the sums in the workspace.
+hipError_t launch_finish(const GluArgs& a, int parts, hipStream_t stream) {
+    const int col_waves = (a.N + kWaveCols - 1) / kWaveCols;
+    const int64_t waves = a.T * col_waves;
+    const FinishParams p{static_cast<const float*>(a.workspace), parts, a.T, a.N, col_waves, a.h_codes, a.h_scale, a.y, a.y_bf16,
+                         a.y_codes, a.y_scale, a.e8m0};
+    return with_act(a.act, [&](auto act) {
+        glu_finish_kernel<decltype(act)::value><<<grid_of((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
+        return hipGetLastError();
+    });
+}
+
 // The products' sums to the workspace, and the outputs from there.
 hipError_t launch_sums(const GluArgs& a, hipStream_t stream) {
-    const size_t sums = sums_bytes(a.T, a.N);
+    int parts = 1;
     Fp8GemmArgs g{};
     g.a = a.x;
     g.a_scale = a.x_scale;
@@ -111,25 +127,58 @@ hipError_t launch_sums(const GluArgs& a, hipStream_t stream) {
     g.N = 2 * a.N;
     g.R = a.K;
     g.y = a.workspace;
-    g.workspace = static_cast<uint8_t*>(a.workspace) + sums;
-    g.ws_bytes = a.ws_bytes - sums;
+    g.workspace = a.workspace;
+    g.ws_bytes = a.ws_bytes;
+    g.parts = &parts;
     const hipError_t e = launch_fp8_gemm(g, stream);
-    if (e != hipSuccess) return e;
-    const int col_waves = (a.N + kWaveCols - 1) / kWaveCols;
-    const int64_t waves = a.T * col_waves;
-    const FinishParams p{static_cast<const float*>(a.workspace), a.T, a.N, col_waves, a.h_codes, a.h_scale, a.y, a.y_bf16,
-                         a.y_codes, a.y_scale, a.e8m0};
-    return with_act(a.act, [&](auto act) {
-        glu_finish_kernel<decltype(act)::value><<<grid_of((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
-        return hipGetLastError();
-    });
+    return e != hipSuccess ? e : launch_finish(a, parts, stream);
 }
 
-// How a product runs.
-enum Form : int { kSums, kLarge };
-Form plan(int64_t T, int N, int K) {
-    if (K > kFp8Block && (T + 255) / 256 * (N / 128) >= device_cu_count() / 2) return kLarge;
-    return kSums;
+hipError_t launch_small(const GluArgs& a, bool codes, hipStream_t stream) {
+    if (!codes) return launch_glu_small(glu_params(a), a.e8m0, nullptr, stream);
+    const hipError_t e = launch_glu_small(glu_params(a), a.e8m0, static_cast<float*>(a.workspace), stream);
+    return e != hipSuccess ? e : launch_finish(a, 1, stream);
+}
+
+// How a product runs; `codes`: codes come out, of y or of [g u].
+enum Form : int { kSmall, kSums, kTile64, kTile128, kLarge };
+// Measured with codes (us; T x K, N channels):
+//                        sums    64     128    256 tokens a tile
+//   64 x 512, 1152       10.3    7.3    8.7
+//   64 x 1024, 4096      10.8    8.1   12.0
+//   391 x 1936, 1152     13.9   15.9   20.4   24.7
+//   100 x 4096, 1152     12.4   21.1   32.4   36.8
+//   64 x 4096, 4096      14.2   21.6   32.5   36.4
+//   256 x 4096, 4096     22.2   21.6   33.2   37.3
+//   512 x 4096, 4096     29.8   22.6   33.5   37.5
+//   1024 x 4096, 4096    47.7   44.6   35.9   38.5
+//   2048 x 4096, 4096    82     90     72     64.6
+//   128 x 8192, 8192     52     57     71
+//   256 x 16384, 4096    83     98    129
+// A tile costs its chain of blocks (0.6, 1 and 1.15 us each) as long as each CU has one, so the smallest whose workgroups fit
+// at once is taken, and where none fits the largest.  The product that leaves its sums in the workspace splits the reduction
+// over idle CUs and costs a launch: it is better where tiles of 64 are few or the reduction is long.  Few tokens: as the
+// weights stream (fp8_glu_small.hip), but where the output is too narrow for that (1 x 16384, 1024 channels: 21.6, sums 14.4),
+// and for codes of a short reduction in one launch (4 x 1024, 4096: 8.1, small 10.4; its y alone 6.9).
+Form plan(int64_t T, int N, int K, bool codes) {
+    const int64_t cus = device_cu_count();
+    const int blocks = static_cast<int>(fp8_groups(K));
+    auto tiles = [&](int tokens) { return (T + tokens - 1) / tokens * (N / 128); };
+    if (T <= 16) {
+        if (codes && blocks <= 8 && tiles(64) <= cus) return kTile64;
+        return blocks > 64 && N / 16 < cus / 2 ? kSums : kSmall;
+    }
+    if (tiles(64) <= cus) return blocks <= 12 || 2 * tiles(64) > cus || (2 * tiles(64) == cus && blocks <= 48) ? kTile64 : kSums;
+    if (tiles(128) <= cus || blocks == 1) return kTile128;   // (the large form's loads run two blocks ahead)
+    return kLarge;
+}
+
+size_t workspace_bytes(int64_t T, int N, int K, bool codes) {
+    switch (plan(T, N, K, codes)) {
+        case kSums: return std::max(sums_bytes(T, N), fp8_gemm_workspace_bytes(T, 2 * N, K, false));
+        case kSmall: return codes ? sums_bytes(T, N) : 0;
+        default: return 0;
+    }
 }
 
 // A wave takes 512 channels of a token: their gradients' two parts, 512 channels of the gate and of the other.
@@ -213,12 +262,15 @@ fp8::GluParams glu_params(const GluArgs& a) {
 }
 
 size_t fp8_glu_workspace_bytes(int64_t T, int N, int K) {
-    if (T == 0 || plan(T, N, K) != kSums) return 0;
-    return sums_bytes(T, N) + fp8_gemm_workspace_bytes(T, 2 * N, K, false);
+    return T == 0 ? 0 : std::max(workspace_bytes(T, N, K, false), workspace_bytes(T, N, K, true));
 }
 
 hipError_t launch_fp8_glu(const GluArgs& a, hipStream_t stream) {
-    switch (plan(a.T, a.N, a.K)) {
+    const bool codes = a.y_codes != nullptr || a.h_codes != nullptr;
+    switch (plan(a.T, a.N, a.K, codes)) {
+        case kSmall: return launch_small(a, codes, stream);
+        case kTile64: return launch_glu_tile(glu_params(a), a.e8m0, 64, stream);
+        case kTile128: return launch_glu_tile(glu_params(a), a.e8m0, 128, stream);
         case kLarge: return launch_glu_large(glu_params(a), a.e8m0, stream);
         default: return launch_sums(a, stream);
     }

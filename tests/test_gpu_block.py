@@ -240,7 +240,8 @@ def test_glu_activations(T, N, K, st, name):
 
 
 @pytest.mark.parametrize("st", [F32, E8M0])
-@pytest.mark.parametrize("T,N,K", [(4608, 2176, 640), (4099, 4096, 144), (2500, 2816, 2064), (8300, 1152, 272), (1500, 16384, 384)])
+@pytest.mark.parametrize("T,N,K", [(4608, 2176, 640), (4099, 4096, 144), (2500, 2816, 2064), (8300, 1152, 272), (1500, 16384, 384),
+                                   (4608, 1024, 112)])
 def test_glu_large(T, N, K, st):
     """Whole rounds of tiles and parts of one, few blocks of the reduction and many, ragged last rows."""
     check_glu(T, N, K, st, "silu")
@@ -318,6 +319,23 @@ def test_glu_non_finite(T, N, K):
     rtq.fp8_glu(x, sx, w, sw, ACTS["silu"], y_codes=c, y_scale=s)
     cf = c.float()
     assert torch.isnan(cf[3]).all() and torch.isnan(cf[:, 150]).all() and torch.isfinite(cf[rows][:, cols]).all()
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 256, 144), (16, 128, 1040), (40, 256, 2064), (100, 128, 144), (300, 256, 4112), (2100, 4096, 272)])
+def test_glu_infinite_scale_of_the_last_block(T, N, K):
+    """Nothing that fills a block, a stage or a turn meets the infinite scales: the last token's sums stay infinite, the first
+    gate block's too."""
+    step("glu infinite scale", T, N, K)
+    x, w = torch.ones(T, K, device="cuda").to(E4M3), torch.ones(2 * N, K, device="cuda").to(E4M3)
+    sx, sw = torch.ones(groups(K), T, device="cuda"), torch.ones(groups(2 * N), groups(K), device="cuda") / K
+    sx[-1, T - 1] = float("inf")
+    y = torch.empty(T, N, device="cuda")
+    rtq.fp8_glu(x, sx, w, sw, ACTS["silu"], y=y)
+    assert (y[T - 1] == float("inf")).all() and torch.isfinite(y[:T - 1]).all()
+    sx[-1, T - 1] = 1.0
+    sw[0, -1] = float("inf")
+    rtq.fp8_glu(x, sx, w, sw, ACTS["silu"], y=y)
+    assert (y[:, :128] == float("inf")).all() and torch.isfinite(y[:, 128:]).all()
 
 
 @pytest.mark.parametrize("st", [F32, E8M0])
