@@ -15,7 +15,7 @@ namespace {
 
 using namespace rtq;
 
-constexpr int64_t kMostElements = int64_t{1} << 37;   // of a tensor (2^23 pieces, 2^31 work-items)
+constexpr int64_t kMostElements = int64_t{1} << 37;   // of a tensor
 constexpr int32_t kMostTensors = 1 << 20;
 
 rtq_status check_eps(float eps) {

@@ -164,6 +164,20 @@ __device__ __forceinline__ void store8(void* y, int64_t i, const float* v) {
 }
 
 
+// The same past the caches, for what is not read again soon.
+template <bool kBF16>
+__device__ __forceinline__ void stream8(void* y, int64_t i, const float* v) {
+    if constexpr (kBF16) {
+        const v4i p = {static_cast<int>(pack_bf16x2(v[0], v[1])), static_cast<int>(pack_bf16x2(v[2], v[3])),
+                       static_cast<int>(pack_bf16x2(v[4], v[5])), static_cast<int>(pack_bf16x2(v[6], v[7]))};
+        __builtin_nontemporal_store(p, reinterpret_cast<v4i*>(static_cast<uint16_t*>(y) + i));
+    } else {
+        v4f* p = reinterpret_cast<v4f*>(static_cast<float*>(y) + i);
+        __builtin_nontemporal_store(v4f{v[0], v[1], v[2], v[3]}, p);
+        __builtin_nontemporal_store(v4f{v[4], v[5], v[6], v[7]}, p + 1);
+    }
+}
+
 // One row's 8 elements of a lane -> 8 codes; returns the group's exponent (the same in its 16 lanes).
 template <bool kE5M2>
 __device__ __forceinline__ int quantise8(const float* v, uint2* codes) {

@@ -20,7 +20,8 @@ using namespace fp8;
 
 constexpr int kThreads = 256;
 constexpr int kMost = 96;                        // tensors of a launch: their table fits the 4 KB of arguments
-constexpr int kPiece = 16 * 1024;                // elements a workgroup takes
+constexpr int kPass = kThreads * 8;              // elements a workgroup takes at a time
+constexpr int64_t kScalePiece = 2 * kPass;       // elements of a piece that is scaled
 
 struct Table {
     const void* data[kMost];
@@ -28,6 +29,7 @@ struct Table {
     int64_t n[kMost];
     uint32_t first[kMost + 1];                   // piece that each tensor begins with, and their number
     uint32_t bf16[kMost / 32];
+    int64_t piece;                               // elements a workgroup takes
     int count;
 };
 static_assert(sizeof(Table) + 64 <= 4096, "kernel arguments");
@@ -48,8 +50,8 @@ __device__ __forceinline__ Place place(const Table& t, uint32_t piece) {
         else
             hi = mid;
     }
-    const int64_t begin = static_cast<int64_t>(piece - t.first[lo]) * kPiece;
-    return {lo, begin, min(begin + kPiece, t.n[lo]), (t.bf16[lo / 32] >> (lo % 32) & 1u) != 0u};
+    const int64_t begin = static_cast<int64_t>(piece - t.first[lo]) * t.piece;
+    return {lo, begin, min(begin + t.piece, t.n[lo]), (t.bf16[lo / 32] >> (lo % 32) & 1u) != 0u};
 }
 
 __device__ __forceinline__ double block_sum(double v, double* slots) {
@@ -96,8 +98,13 @@ __global__ void __launch_bounds__(1024)
 grad_root_kernel(const double* __restrict__ part, int64_t n, float* norm) {
     __shared__ double slots[1024 / 64];
     double s = 0.0;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+    for (int64_t i = threadIdx.x; i < n; i += 4 * 1024) {   // four loads at once
+        double v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = part[min<int64_t>(i + 1024 * q, n - 1)];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s += i + 1024 * q < n ? v[q] : 0.0;
+    }
     s = block_sum(s, slots);
     if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(s));
 }
@@ -113,7 +120,7 @@ __device__ __forceinline__ void scale(const void* data, void* out, int64_t begin
         r.get(v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= c;
-        store8<kBF16>(out, i, v);
+        stream8<kBF16>(out, i, v);
     }
     for (; i < end; ++i) {
         if constexpr (kBF16)
@@ -127,7 +134,7 @@ __global__ void __launch_bounds__(kThreads)
 grad_scale_kernel(Table t, const float* __restrict__ norm, float most) {
     const float c0 = most / (*norm + 1e-6f);
     const float c = c0 > 1.f ? 1.f : c0;         // a NaN stays
-    const Place w = place(t, blockIdx.x);
+    const Place w = place(t, gridDim.x - 1 - blockIdx.x);   // the other way round: the norm's pass has left the last pieces in the cache
     const void* data = t.data[w.tensor];
     void* out = t.out[w.tensor];
     if (c == 1.f && data == out) return;         // nothing to change
@@ -137,24 +144,33 @@ grad_scale_kernel(Table t, const float* __restrict__ norm, float most) {
         scale<false>(data, out, w.begin, w.end, c);
 }
 
-int64_t pieces(int64_t n) { return (n + kPiece - 1) / kPiece; }
+// Elements of a piece whose squares are summed: about 2048 pieces in all, 8 a CU (805 MB of bf16: 139 us, with pieces of 16384
+// 158; their sums are two loads a thread).  What is scaled goes in pieces of 4096 (norm and scaling of 805 MB 400 us, with
+// 2048 elements 404, 8192 409, 16384 415, 32768 425; with stores through the cache, which push out what the norm's pass has
+// left there, 454).
+int64_t piece_of(const TensorSpan* t, int count) {
+    int64_t total = 0;
+    for (int i = 0; i < count; ++i) total += t[i].n;
+    return std::max<int64_t>(4, (total + 2048 * kPass - 1) / (2048 * kPass)) * kPass;
+}
 
 // f(table, its pieces) for as many tables as the tensors need.
 template <typename F>
-hipError_t each_table(const TensorSpan* t, int count, F f) {
+hipError_t each_table(const TensorSpan* t, int count, int64_t piece, F f) {
     Table table{};
+    table.piece = piece;
     int64_t at = 0;
     auto flush = [&]() {
         table.first[table.count] = static_cast<uint32_t>(at);
         const hipError_t e = table.count > 0 ? f(table, at) : hipSuccess;
         table = Table{};
+        table.piece = piece;
         at = 0;
         return e;
     };
     for (int i = 0; i < count; ++i) {
         if (t[i].n == 0) continue;
-        const int64_t more = pieces(t[i].n);
-        if (table.count == kMost || at + more > UINT32_MAX / kThreads) {   // a grid holds 2^32 work-items
+        if (table.count == kMost) {
             const hipError_t e = flush();
             if (e != hipSuccess) return e;
         }
@@ -164,25 +180,24 @@ hipError_t each_table(const TensorSpan* t, int count, F f) {
         table.n[k] = t[i].n;
         table.first[k] = static_cast<uint32_t>(at);
         if (t[i].bf16) table.bf16[k / 32] |= 1u << (k % 32);
-        at += more;
+        at += (t[i].n + piece - 1) / piece;
     }
     return flush();
 }
 
-int64_t total_pieces(const TensorSpan* t, int count) {
-    int64_t n = 0;
-    for (int i = 0; i < count; ++i) n += pieces(t[i].n);
-    return n;
-}
-
 }  // namespace
 
-size_t grad_norm_workspace_bytes(const TensorSpan* t, int count) { return static_cast<size_t>(total_pieces(t, count)) * sizeof(double); }
+size_t grad_norm_workspace_bytes(const TensorSpan* t, int count) {
+    const int64_t piece = piece_of(t, count);
+    int64_t pieces = 0;
+    for (int i = 0; i < count; ++i) pieces += (t[i].n + piece - 1) / piece;
+    return static_cast<size_t>(pieces) * sizeof(double);
+}
 
 hipError_t launch_grad_norm(const TensorSpan* t, int count, float* norm, void* workspace, hipStream_t stream) {
     double* part = static_cast<double*>(workspace);
     int64_t done = 0;
-    const hipError_t e = each_table(t, count, [&](const Table& table, int64_t n) {
+    const hipError_t e = each_table(t, count, piece_of(t, count), [&](const Table& table, int64_t n) {
         grad_squares_kernel<<<static_cast<unsigned>(n), kThreads, 0, stream>>>(table, part + done);
         done += n;
         return hipGetLastError();
@@ -193,7 +208,7 @@ hipError_t launch_grad_norm(const TensorSpan* t, int count, float* norm, void* w
 }
 
 hipError_t launch_grad_clip(const TensorSpan* t, int count, const float* norm, float most, hipStream_t stream) {
-    return each_table(t, count, [&](const Table& table, int64_t n) {
+    return each_table(t, count, kScalePiece, [&](const Table& table, int64_t n) {
         grad_scale_kernel<<<static_cast<unsigned>(n), kThreads, 0, stream>>>(table, norm, most);
         return hipGetLastError();
     });

@@ -7,6 +7,10 @@
 // Both are one pass over HBM: a row stays in registers between its sum and what is computed from it.  Sums of
 // squares are held in fp64 (products of fp32 values neither overflow nor round there, and fp64 adds run at the
 // fp32 rate), so rho is good to its rounding to fp32.
+//
+// h and dh are stored past the caches: the residual stream is read again a sublayer later, the codes at once (4608 x 4096: 23.9
+// us, 26.9 with plain stores, backward 31.3 and 33.3; 132 and 151 MB, 5.5 and 4.8 TB/s.  Non-temporal loads of x and r bring as
+// much where they come from HBM and cost 20% where a kernel before has left them in the cache).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -116,25 +120,17 @@ __device__ __forceinline__ void put_chunk(const RmsForwardParams& p, const float
     }
 }
 
-// Row of a team, in 8 contiguous ranges, one per XCD (workgroup b runs on XCD b % 8): neighbouring rows' scales
-// share cache lines.
-__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t blocks) {
-    const int64_t per = (blocks + 7) / 8, local = b / 8;
-    return local < per ? b % 8 * per + local : blocks;
-}
-
 constexpr int forward_waves(int team) { return team < 4 ? 4 : team; }
 
 // A team of kTeam waves takes a row of at most kTeam * kChunks * 512 elements.
 template <bool kX16, bool kRes, bool kR16, bool kG16, int kTeam>
 __global__ void __launch_bounds__(64 * forward_waves(kTeam))
-rmsnorm_forward_kernel(RmsForwardParams p, int64_t blocks) {
+rmsnorm_forward_kernel(RmsForwardParams p) {
     constexpr int kTeams = forward_waves(kTeam) / kTeam;
     __shared__ double slots[kTeams * kTeam];
-    const int64_t b = xcd_order(block_index(), blocks);
-    if (b >= blocks) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, team = wave / kTeam, mine = wave % kTeam;
-    const int64_t row = b * kTeams + team;
+    const int64_t row = block_index() * kTeams + team;
+    if (row - team >= p.rows) return;
     const bool any = row < p.rows;
     Row8<kX16> x[kChunks];
     Row8<kR16> r[kChunks];
@@ -160,7 +156,7 @@ rmsnorm_forward_kernel(RmsForwardParams p, int64_t blocks) {
     for (int i = 0; i < kChunks; ++i) {
         add_residual<kX16, kRes, kR16>(x[i], r[i], h[i]);
         if constexpr (kRes) {
-            if (put[i]) store8<kR16>(p.h, row * p.d + c[i], h[i]);
+            if (put[i]) stream8<kR16>(p.h, row * p.d + c[i], h[i]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[0] = __builtin_fma(static_cast<double>(h[i][e]), static_cast<double>(h[i][e]), sum[0]);
@@ -175,10 +171,10 @@ rmsnorm_forward_kernel(RmsForwardParams p, int64_t blocks) {
 // and wrote it before).
 template <bool kX16, bool kRes, bool kR16, bool kG16>
 __global__ void __launch_bounds__(64 * kMostTeam)
-rmsnorm_forward_long_kernel(RmsForwardParams p, int64_t blocks) {
+rmsnorm_forward_long_kernel(RmsForwardParams p) {
     __shared__ double slots[kMostTeam];
-    const int64_t row = xcd_order(block_index(), blocks);
-    if (row >= blocks) return;
+    const int64_t row = block_index();
+    if (row >= p.rows) return;
     constexpr int kStep = kMostTeam * kWaveCols;
     const int c0 = static_cast<int>(threadIdx.x) * kLaneCols;
     double sum[1] = {0.0};
@@ -233,13 +229,13 @@ hipError_t forward(const RmsForwardArgs& a, hipStream_t stream) {
     const RmsForwardParams p{a.x, a.residual, a.rows, a.d, 1.0 / a.d, a.eps, a.gamma, a.h, a.y, a.codes, a.scale, a.e8m0};
     const int team = team_of(a.d);
     if (team == 0) {
-        rmsnorm_forward_long_kernel<kX16, kRes, kR16, kG16><<<grid_of((a.rows + 7) / 8 * 8), 64 * kMostTeam, 0, stream>>>(p, a.rows);
+        rmsnorm_forward_long_kernel<kX16, kRes, kR16, kG16><<<grid_of(a.rows), 64 * kMostTeam, 0, stream>>>(p);
         return hipGetLastError();
     }
     return with_team(team, [&](auto t) {
         constexpr int kTeam = decltype(t)::value, kWaves = forward_waves(kTeam), kTeams = kWaves / kTeam;
         const int64_t blocks = (a.rows + kTeams - 1) / kTeams;
-        rmsnorm_forward_kernel<kX16, kRes, kR16, kG16, kTeam><<<grid_of((blocks + 7) / 8 * 8), 64 * kWaves, 0, stream>>>(p, blocks);
+        rmsnorm_forward_kernel<kX16, kRes, kR16, kG16, kTeam><<<grid_of(blocks), 64 * kWaves, 0, stream>>>(p);
         return hipGetLastError();
     });
 }
@@ -354,7 +350,7 @@ rmsnorm_backward_kernel(RmsBackwardParams p) {
                 a[e] *= w[e];
             }
             row_gradient(v, a, h, rho, k);
-            if (row < p.rows && c[i] < p.d) store8<kH16>(p.dh, row * p.d + c[i], v);
+            if (row < p.rows && c[i] < p.d) stream8<kH16>(p.dh, row * p.d + c[i], v);
         }
     }
     if (p.part == nullptr) return;
@@ -448,22 +444,23 @@ rmsnorm_backward_long_kernel(RmsBackwardParams p) {
 }
 
 // dgamma = (dgamma +) the parts' sum, in an order that their number alone decides: 32 columns a workgroup, thread t
-// parts t / 32, + 8, ..
+// parts t / 32, + 32, ..
 template <bool kG16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 dgamma_kernel(const float* __restrict__ part, int parts, int d, void* dgamma, bool accumulate) {
-    __shared__ float sums[8][32];
-    const int c = static_cast<int>(blockIdx.x) * 32 + static_cast<int>(threadIdx.x & 31), slice = static_cast<int>(threadIdx.x >> 5);
+    __shared__ float sums[32][33];
+    const int lane = static_cast<int>(threadIdx.x & 31), slice = static_cast<int>(threadIdx.x >> 5);
+    const int c = static_cast<int>(blockIdx.x) * 32 + lane;
     float s = 0.f;
     if (c < d) {
 #pragma unroll 8
-        for (int q = slice; q < parts; q += 8) s += part[static_cast<int64_t>(q) * d + c];
+        for (int q = slice; q < parts; q += 32) s += part[static_cast<int64_t>(q) * d + c];
     }
-    sums[slice][threadIdx.x & 31] = s;
+    sums[slice][lane] = s;
     __syncthreads();
     if (slice != 0 || c >= d) return;
 #pragma unroll
-    for (int q = 1; q < 8; ++q) s += sums[q][threadIdx.x];
+    for (int q = 1; q < 32; ++q) s += sums[q][lane];
     if constexpr (kG16) {
         uint16_t* out = static_cast<uint16_t*>(dgamma) + c;
         if (accumulate) s += bf16_lo(*out);
@@ -502,7 +499,7 @@ hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
     }
     if (a.dgamma == nullptr || (parts == 0 && a.accumulate)) return hipSuccess;
     auto kernel = a.dg_bf16 ? dgamma_kernel<true> : dgamma_kernel<false>;
-    kernel<<<(a.d + 31) / 32, 256, 0, stream>>>(static_cast<const float*>(a.workspace), parts, a.d, a.dgamma, a.accumulate);
+    kernel<<<(a.d + 31) / 32, 1024, 0, stream>>>(static_cast<const float*>(a.workspace), parts, a.d, a.dgamma, a.accumulate);
     return hipGetLastError();
 }
 
