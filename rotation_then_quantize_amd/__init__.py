@@ -639,29 +639,28 @@ def act_fp8_backward(dy, h_codes, h_scale, act: int, dh, stream=None):
 
 # ------------------------------------------------------------------ around the 8-bit layers of an MLP block
 
+@functools.lru_cache(maxsize=None)
+def _bound():
+    """The compiled binding (csrc/bind.cpp): it checks the tensors and calls the library.  Raises if it has not been built."""
+    load_library()
+    _torch()
+    try:
+        import importlib
+        native = importlib.import_module("._native", __package__)
+    except ImportError as e:
+        raise RuntimeError(f"{os.path.join(_PKG, '_native.so')} cannot be loaded ({e}): build it with __graft_entry__.build(); "
+                           f"there is no fallback path") from e
+    native.load(LIB_PATH)
+    return native
+
+
 def rmsnorm_forward(x, gamma, eps: float, residual=None, h=None, codes=None, scale=None, y=None, stream=None):
     """n = h / sqrt(mean h^2 + eps) gamma for rows of h = x, or of h = x + residual, which is written to h [rows][d]
     (residual's type; h may be residual).  n comes back quantised, as codes [rows][d] (e4m3) and scale [groups][rows],
     as y [rows][d] (x's type), or as both."""
-    floats = _types()[0]
-    xt = _operand(x, "x", floats)
-    rows, d = x.shape
-    gt = _operand(gamma, "gamma", floats, (d,), x)
-    if (residual is None) != (h is None):
-        raise ValueError("residual and h are given together or not at all")
-    if (codes is None) != (scale is None) or (y is None and codes is None):
-        raise ValueError("give y, or codes and scale, or all of them")
-    rt, st = xt, RTQ_F32
-    if residual is not None:
-        rt = _operand(residual, "residual", floats, x.shape, x)
-        _operand(h, "h", {residual.dtype: rt}, x.shape, x)
-    if codes is not None:
-        _operand(codes, "codes", _types()[2], x.shape, x)
-        st = _operand(scale, "scale", _types()[3], (fp8_groups(d), rows), x)
-    if y is not None:
-        _operand(y, "y", {x.dtype: xt}, x.shape, x)
-    _call(x, stream, load_library().rtq_rmsnorm_forward, _ptr(x), xt, _ptr(residual), rt, rows, d, _ptr(gamma), gt, eps,
-          _ptr(h), _ptr(y), _ptr(codes), _ptr(scale), st)
+    status = _bound().rmsnorm_forward(x, gamma, eps, residual, h, codes, scale, y, stream)
+    if status:
+        _check(status)
     return x if h is None else h
 
 
@@ -674,21 +673,12 @@ def rmsnorm_backward(dn, h, gamma, eps: float, dh, dgamma=None, dresidual=None, 
     """dh [rows][d] (h's type), the gradient of h and thus of x and residual, from the gradient dn [rows][d] of
     rmsnorm_forward's n and the residual stream's own, dresidual (h's type, or None); dh may be dresidual, or dn if their
     types agree.  dgamma [d] (float32 or bfloat16) is written, or added to with accumulate."""
-    floats = _types()[0]
-    dnt = _operand(dn, "dn", floats)
-    rows, d = dn.shape
-    ht = _operand(h, "h", floats, dn.shape, dn)
-    gt = _operand(gamma, "gamma", floats, (d,), dn)
-    _operand(dh, "dh", {h.dtype: ht}, dn.shape, dn)
-    if dresidual is not None:
-        _operand(dresidual, "dresidual", {h.dtype: ht}, dn.shape, dn)
-    dgt, ws = RTQ_F32, None
-    if dgamma is not None:
-        dgt = _operand(dgamma, "dgamma", floats, (d,), dn)
-        ws = _workspace(workspace, dn, stream, rmsnorm_backward_workspace, rows, d)
-    _call(dn, stream, load_library().rtq_rmsnorm_backward, _ptr(dn), dnt, _ptr(h), ht, _ptr(dresidual), rows, d, _ptr(gamma),
-          gt, eps, _ptr(dh), _ptr(dgamma), dgt, 1 if accumulate else 0, _ptr(ws),
-          0 if ws is None else ws.numel() * ws.element_size())
+    if workspace is None and dgamma is not None:
+        _operand(dn, "dn", _types()[0])
+        workspace = _workspace(None, dn, stream, rmsnorm_backward_workspace, *dn.shape)
+    status = _bound().rmsnorm_backward(dn, h, gamma, eps, dh, dgamma, dresidual, accumulate, workspace, stream)
+    if status:
+        _check(status)
     return dh
 
 
@@ -702,51 +692,22 @@ def fp8_glu(x_codes, x_scale, w_codes, w_scale, act: int, y=None, y_codes=None, 
     multiple of 128); f is RTQ_ACT_GELU_TANH, RTQ_ACT_GELU or RTQ_ACT_SILU.  y [T][N] comes back as y (float32 or
     bfloat16), or quantised as y_codes, y_scale.  With h_codes [T][2 N] and h_scale, [g u] is kept in 8 bits, for
     glu_fp8_backward."""
-    e4m3 = _types()[2]
-    rows, K, st = _fp8_weight(w_codes, w_scale, x_codes)
-    if rows % 256 != 0:
-        raise ValueError(f"w_codes: {rows} rows, expected two projections of a multiple of {FP8_BLOCK} each")
-    T, N = x_codes.shape[0], rows // 2
-    _operand(x_codes, "x_codes", e4m3, (T, K))
-    scales = {w_scale.dtype: st}
-    _operand(x_scale, "x_scale", scales, (fp8_groups(K), T), x_codes)
-    if (y_codes is None) != (y_scale is None) or (y is None) == (y_codes is None):
-        raise ValueError("give either y, or y_codes and y_scale")
-    if (h_codes is None) != (h_scale is None):
-        raise ValueError("h_codes and h_scale are given together or not at all")
-    yt = RTQ_F32
-    if y is not None:
-        yt = _operand(y, "y", _types()[0], (T, N), x_codes)
-    else:
-        _operand(y_codes, "y_codes", e4m3, (T, N), x_codes)
-        _operand(y_scale, "y_scale", scales, (fp8_groups(N), T), x_codes)
-    if h_codes is not None:
-        _operand(h_codes, "h_codes", e4m3, (T, 2 * N), x_codes)
-        _operand(h_scale, "h_scale", scales, (fp8_groups(2 * N), T), x_codes)
-    ws = _workspace(workspace, x_codes, stream, fp8_glu_workspace, T, N, K)
-    _call(x_codes, stream, load_library().rtq_fp8_glu, _ptr(x_codes), _ptr(x_scale), T, _ptr(w_codes), _ptr(w_scale), st, N, K,
-          act, _ptr(h_codes), _ptr(h_scale), _ptr(y), yt, _ptr(y_codes), _ptr(y_scale), _ptr(ws),
-          ws.numel() * ws.element_size())
+    if workspace is None:
+        _operand(x_codes, "x_codes", _types()[2])
+        _operand(w_codes, "w_codes", _types()[2], None, x_codes)
+        workspace = _workspace(None, x_codes, stream, fp8_glu_workspace, x_codes.shape[0], w_codes.shape[0] // 2, x_codes.shape[1])
+    status = _bound().fp8_glu(x_codes, x_scale, w_codes, w_scale, act, y, y_codes, y_scale, h_codes, h_scale, workspace, stream)
+    if status:
+        _check(status)
     return y if y is not None else (y_codes, y_scale)
 
 
 def glu_fp8_backward(dy, h_codes, h_scale, act: int, dh=None, dh_codes=None, dh_scale=None, stream=None):
     """[dg du] = [dy u^ f'(g^), dy f(g^)] from dy [T][N] and fp8_glu's checkpoint, as dh [T][2 N] (dy's type; fp8_wgrad
     takes it in bfloat16) and/or quantised, as dh_codes [T][2 N] (e4m3 or e5m2) and dh_scale, for fp8_dgrad."""
-    dyt = _operand(dy, "dy", _types()[0])
-    T, N = dy.shape
-    _operand(h_codes, "h_codes", _types()[2], (T, 2 * N), dy)
-    st = _operand(h_scale, "h_scale", _types()[3], (fp8_groups(2 * N), T), dy)
-    if (dh_codes is None) != (dh_scale is None) or (dh is None and dh_codes is None):
-        raise ValueError("give dh, or dh_codes and dh_scale, or all of them")
-    gt = RTQ_E4M3
-    if dh is not None:
-        _operand(dh, "dh", {dy.dtype: dyt}, (T, 2 * N), dy)
-    if dh_codes is not None:
-        gt = _operand(dh_codes, "dh_codes", _types()[1], (T, 2 * N), dy)
-        _operand(dh_scale, "dh_scale", {h_scale.dtype: st}, (fp8_groups(2 * N), T), dy)
-    _call(dy, stream, load_library().rtq_glu_fp8_backward, _ptr(dy), dyt, _ptr(h_codes), _ptr(h_scale), st, T, N, act, _ptr(dh),
-          _ptr(dh_codes), gt, _ptr(dh_scale))
+    status = _bound().glu_fp8_backward(dy, h_codes, h_scale, act, dh, dh_codes, dh_scale, stream)
+    if status:
+        _check(status)
     return dh if dh is not None else (dh_codes, dh_scale)
 
 
@@ -769,6 +730,7 @@ class TensorList:
             _operand(o, f"outs[{i}]", {t.dtype: code}, t.shape, like)
             self._c[i] = _Tensor(t.data_ptr(), t.numel(), code)
             self._outs[i] = o.data_ptr()
+        self._like, self._at, self._outs_at = like, ctypes.addressof(self._c), ctypes.addressof(self._outs)
 
 
 def grad_norm_workspace(tensors: TensorList) -> int:
@@ -777,17 +739,17 @@ def grad_norm_workspace(tensors: TensorList) -> int:
 
 def grad_norm(tensors: TensorList, norm, workspace=None, stream=None):
     """norm (one float32 on the GPU) = the 2-norm of all tensors together."""
-    like = tensors.tensors[0]
-    _operand(norm, "norm", {_torch().float32: RTQ_F32}, (1,) if norm.dim() else (), like)
-    ws = _workspace(workspace, like, stream, grad_norm_workspace, tensors)
-    _call(like, stream, load_library().rtq_grad_norm, tensors._c, tensors.count, _ptr(norm), _ptr(ws),
-          ws.numel() * ws.element_size())
+    if workspace is None:
+        workspace = _workspace(None, tensors._like, stream, grad_norm_workspace, tensors)
+    status = _bound().grad_norm(tensors._like, tensors._at, tensors.count, norm, workspace, stream)
+    if status:
+        _check(status)
     return norm
 
 
 def grad_clip(tensors: TensorList, norm, most: float, stream=None):
     """Each tensor times min(1, most / (norm + 1e-6)), to the list's outs."""
-    like = tensors.tensors[0]
-    _operand(norm, "norm", {_torch().float32: RTQ_F32}, (1,) if norm.dim() else (), like)
-    _call(like, stream, load_library().rtq_grad_clip, tensors._c, tensors._outs, tensors.count, _ptr(norm), most)
+    status = _bound().grad_clip(tensors._like, tensors._at, tensors._outs_at, tensors.count, norm, most, stream)
+    if status:
+        _check(status)
     return tensors.outs
