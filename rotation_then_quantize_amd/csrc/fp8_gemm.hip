@@ -277,7 +277,7 @@ hipError_t launch_tiles(Fp8GemmParams p, const Fp8GemmArgs& g, int split, hipStr
     p.tiles_n = static_cast<int>((g.N + BT - 1) / BT);
     p.split = split;
     if (g.workspace == nullptr || g.ws_bytes < static_cast<size_t>(split) * g.M * g.N * sizeof(float)) p.split = 1;
-    if (p.split > 1) p.y = g.workspace;   // (a caller that adds the parts itself gives the same place for both)
+    if (p.split > 1) p.y = g.workspace;
     const int64_t total = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.split;
     kernel<<<grid_of((total + 7) / 8 * 8), threads, lds, stream>>>(p);
     e = hipGetLastError();

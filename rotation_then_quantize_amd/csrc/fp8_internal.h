@@ -84,7 +84,7 @@ struct Fp8GemmArgs {
     bool y_bf16;
     void* workspace;      // optional: partial sums of a split reduction
     size_t ws_bytes;
-    int* parts = nullptr; // if given (y fp32, in the workspace): partial sums [*parts][M][N] are left there, and not added
+    int* parts = nullptr; // if given (y fp32 and workspace the same place): the partial sums [*parts][M][N] are left there, and not added
 };
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t stream);
 // The layer for a few rows or a small output in one launch: x [M][R] (fp32 or bf16) is quantised on the way

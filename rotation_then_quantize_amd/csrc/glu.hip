@@ -100,7 +100,7 @@ hipError_t with_act(int act, F f) {
     }
 }
 
-size_t sums_bytes(int64_t T, int N) { return (static_cast<size_t>(T) * 2 * N * sizeof(float) + 255) / 256 * 256; }
+size_t sums_bytes(int64_t T, int N) { return static_cast<size_t>(T) * 2 * N * sizeof(float); }
 
 // The outputs from the sums in the workspace.
 hipError_t launch_finish(const GluArgs& a, int parts, hipStream_t stream) {
@@ -134,51 +134,43 @@ hipError_t launch_sums(const GluArgs& a, hipStream_t stream) {
     return e != hipSuccess ? e : launch_finish(a, parts, stream);
 }
 
-hipError_t launch_small(const GluArgs& a, bool codes, hipStream_t stream) {
-    if (!codes) return launch_glu_small(glu_params(a), a.e8m0, nullptr, stream);
+hipError_t launch_small(const GluArgs& a, hipStream_t stream) {
+    if (a.y_codes == nullptr && a.h_codes == nullptr) return launch_glu_small(glu_params(a), a.e8m0, nullptr, stream);
     const hipError_t e = launch_glu_small(glu_params(a), a.e8m0, static_cast<float*>(a.workspace), stream);
     return e != hipSuccess ? e : launch_finish(a, 1, stream);
 }
 
-// How a product runs; `codes`: codes come out, of y or of [g u].
+// How a product runs.
 enum Form : int { kSmall, kSums, kTile64, kTile128, kLarge };
 // Measured with codes (us; T x K, N channels):
 //                        sums    64     128    256 tokens a tile
-//   64 x 512, 1152       10.3    7.3    8.7
-//   64 x 1024, 4096      10.8    8.1   12.0
-//   391 x 1936, 1152     13.9   15.9   20.4   24.7
-//   100 x 4096, 1152     12.4   21.1   32.4   36.8
-//   64 x 4096, 4096      14.2   21.6   32.5   36.4
-//   256 x 4096, 4096     22.2   21.6   33.2   37.3
-//   512 x 4096, 4096     29.8   22.6   33.5   37.5
+//   64 x 512, 1152        7.7    6.2    8.6    9.5
+//   64 x 1024, 4096      10.8    8.2   11.8   13.1
+//   391 x 1936, 1152     13.8   15.9   21.5   24.8
+//   100 x 4096, 1152     12.4   21.0   32.5   36.9
+//   64 x 4096, 4096      14.1   21.5   32.6   36.3
+//   25 x 2048, 16384     16.5   14.2   19.4   21.4
+//   256 x 4096, 4096     22.7   21.4   33.2   37.3
+//   512 x 4096, 4096     30.3   25.2   33.5   37.3
 //   1024 x 4096, 4096    47.7   44.6   35.9   38.5
 //   2048 x 4096, 4096    82     90     72     64.6
-//   128 x 8192, 8192     52     57     71
-//   256 x 16384, 4096    83     98    129
+//   128 x 8192, 8192     52     57     73     81
+//   256 x 16384, 4096    83     98    133    159
 // A tile costs its chain of blocks (0.6, 1 and 1.15 us each) as long as each CU has one, so the smallest whose workgroups fit
 // at once is taken, and where none fits the largest.  The product that leaves its sums in the workspace splits the reduction
-// over idle CUs and costs a launch: it is better where tiles of 64 are few or the reduction is long.  Few tokens: as the
-// weights stream (fp8_glu_small.hip), but where the output is too narrow for that (1 x 16384, 1024 channels: 21.6, sums 14.4),
-// and for codes of a short reduction in one launch (4 x 1024, 4096: 8.1, small 10.4; its y alone 6.9).
-Form plan(int64_t T, int N, int K, bool codes) {
+// over idle CUs and costs a launch: it is better where tiles of 64 are few or the reduction is long.
+// Few tokens: as the weights stream (fp8_glu_small.hip), but where workgroups are fewer than CUs and the reduction long (y
+// alone, with codes, and either from sums: 1 x 16384, 1024 channels 19.6, 21.5, 14.2; 1 x 8192, 1152: 11.3, 13.2, 9.7; 4 x 4096,
+// 1152: 7.3, 9.4, 7.9; 4 x 2048, 1152: 5.2, 7.5, 7.6).  Which outputs are asked for does not choose: y is the same bits with the
+// checkpoint and without.
+Form plan(int64_t T, int N, int K) {
     const int64_t cus = device_cu_count();
     const int blocks = static_cast<int>(fp8_groups(K));
     auto tiles = [&](int tokens) { return (T + tokens - 1) / tokens * (N / 128); };
-    if (T <= 16) {
-        if (codes && blocks <= 8 && tiles(64) <= cus) return kTile64;
-        return blocks > 64 && N / 16 < cus / 2 ? kSums : kSmall;
-    }
+    if (T <= 16) return N / 16 < cus && blocks >= 32 ? kSums : kSmall;
     if (tiles(64) <= cus) return blocks <= 12 || 2 * tiles(64) > cus || (2 * tiles(64) == cus && blocks <= 48) ? kTile64 : kSums;
     if (tiles(128) <= cus || blocks == 1) return kTile128;   // (the large form's loads run two blocks ahead)
     return kLarge;
-}
-
-size_t workspace_bytes(int64_t T, int N, int K, bool codes) {
-    switch (plan(T, N, K, codes)) {
-        case kSums: return std::max(sums_bytes(T, N), fp8_gemm_workspace_bytes(T, 2 * N, K, false));
-        case kSmall: return codes ? sums_bytes(T, N) : 0;
-        default: return 0;
-    }
 }
 
 // A wave takes 512 channels of a token: their gradients' two parts, 512 channels of the gate and of the other.
@@ -262,13 +254,17 @@ fp8::GluParams glu_params(const GluArgs& a) {
 }
 
 size_t fp8_glu_workspace_bytes(int64_t T, int N, int K) {
-    return T == 0 ? 0 : std::max(workspace_bytes(T, N, K, false), workspace_bytes(T, N, K, true));
+    if (T == 0) return 0;
+    switch (plan(T, N, K)) {
+        case kSums: return std::max(sums_bytes(T, N), fp8_gemm_workspace_bytes(T, 2 * N, K, false));
+        case kSmall: return sums_bytes(T, N);
+        default: return 0;
+    }
 }
 
 hipError_t launch_fp8_glu(const GluArgs& a, hipStream_t stream) {
-    const bool codes = a.y_codes != nullptr || a.h_codes != nullptr;
-    switch (plan(a.T, a.N, a.K, codes)) {
-        case kSmall: return launch_small(a, codes, stream);
+    switch (plan(a.T, a.N, a.K)) {
+        case kSmall: return launch_small(a, stream);
         case kTile64: return launch_glu_tile(glu_params(a), a.e8m0, 64, stream);
         case kTile128: return launch_glu_tile(glu_params(a), a.e8m0, 128, stream);
         case kLarge: return launch_glu_large(glu_params(a), a.e8m0, stream);
