@@ -408,7 +408,7 @@ rtq_status rtq_act_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_cod
  *   n = h / sqrt(mean_j h_j^2 + eps) * gamma, from h as it is stored;
  *   y = n rounded to xt, and/or codes (E4M3), scale (row groups, st): n quantised.
  *   x, y [rows][d] of xt; residual, h [rows][d] of rt (all F32 or BF16); residual and h are given together or not at
- *   all (rt is not used then); h may be residual, or x where rt is xt.  gamma [d] of gt.  y may be NULL, or codes and
+ *   all (rt is not used then); h may be residual, or x where rt is xt; y may be x where h is not.  gamma [d] of gt.  y may be NULL, or codes and
  *   scale.  eps > 0.  The sum of squares is held in 64 bits; n is good to 4 units of 2^-24 before it is rounded.
  *   rows == 0 is a no-op. */
 rtq_status rtq_rmsnorm_forward(const void* x, rtq_dtype xt, const void* residual, rtq_dtype rt, int64_t rows, int32_t d,
@@ -421,7 +421,7 @@ rtq_status rtq_rmsnorm_forward(const void* x, rtq_dtype xt, const void* residual
  *   dn [rows][d] of dnt; h, dresidual (or NULL: nothing is added), dh [rows][d] of ht; dh may be dresidual, or dn where
  *   dnt is ht, not h.  dgamma [d] of dgt, or NULL; accumulate 0 (overwrite) or 1 (add; a BF16 dgamma is read, added in
  *   fp32 and rounded again).  workspace: rtq_rmsnorm_backward_workspace(rows, d) bytes (any contents), required with
- *   dgamma.  rows == 0 writes zeros to dgamma, or with accumulate leaves it as it is. */
+ *   dgamma; calls sharing a workspace must not overlap.  rows == 0 writes zeros to dgamma, or with accumulate leaves it as it is. */
 rtq_status rtq_rmsnorm_backward(const void* dn, rtq_dtype dnt, const void* h, rtq_dtype ht, const void* dresidual,
                                 int64_t rows, int32_t d, const void* gamma, rtq_dtype gt, float eps, void* dh,
                                 void* dgamma, rtq_dtype dgt, int32_t accumulate, void* workspace, size_t ws_bytes,
@@ -436,8 +436,8 @@ size_t rtq_rmsnorm_backward_workspace(int64_t rows, int32_t d);
  *   next product (y NULL).  h_codes (E4M3) [T][2 N], h_scale (row groups): [g u] quantised, the checkpoint that
  *   rtq_glu_fp8_backward takes; both NULL: not kept.  All scales of type st.
  *   workspace: rtq_fp8_glu_workspace(T, N, K) bytes (any contents), required where that is not 0.  Calls sharing a
- *   workspace must not overlap.  Accuracy of g and u as for rtq_fp8_qgemm, of f as for rtq_act_fp8_forward.  T == 0
- *   is a no-op. */
+ *   workspace must not overlap.  Accuracy of g and u as for rtq_fp8_qgemm, of f as for rtq_act_fp8_forward; y has the same
+ *   bits whichever outputs are asked for beside it.  T == 0 is a no-op. */
 rtq_status rtq_fp8_glu(const void* x_codes, const void* x_scale, int64_t T, const void* w_codes, const void* w_scale,
                        rtq_dtype st, int32_t N, int32_t K, rtq_act act, void* h_codes, void* h_scale, void* y, rtq_dtype yt,
                        void* y_codes, void* y_scale, void* workspace, size_t ws_bytes, void* stream);
@@ -461,7 +461,7 @@ typedef struct {
 /* norm[0] = sqrt(sum over all tensors and elements of g^2), the sum held in 64 bits and added in an order that the
  * tensors' sizes alone decide.  tensors: `count` of them, an array in HOST memory, not used after the call returns; n up to 2^37
  * each, 0 too.  norm: one float in device memory.  workspace: rtq_grad_norm_workspace(tensors, count) bytes (any
- * contents).  No tensors: norm[0] = 0. */
+ * contents); calls sharing a workspace must not overlap.  No tensors: norm[0] = 0. */
 rtq_status rtq_grad_norm(const rtq_tensor* tensors, int32_t count, float* norm, void* workspace, size_t ws_bytes, void* stream);
 size_t rtq_grad_norm_workspace(const rtq_tensor* tensors, int32_t count);
 

@@ -10,9 +10,9 @@ namespace fp8 {
 
 // A launch of more work-items than a grid's first dimension holds (2^32) goes over two; each kernel returns in
 // the workgroups past its last.  The first dimension is a multiple of 8, the number of XCDs.
-inline dim3 grid_of(int64_t blocks) {
-    constexpr int64_t kMost = 1 << 22;
-    return blocks <= kMost ? dim3(static_cast<unsigned>(blocks)) : dim3(kMost, static_cast<unsigned>((blocks + kMost - 1) / kMost));
+inline dim3 grid_of(int64_t blocks, int64_t most = 1 << 22) {   // most: times the workgroup's threads, below 2^32
+    return blocks <= most ? dim3(static_cast<unsigned>(blocks))
+                          : dim3(static_cast<unsigned>(most), static_cast<unsigned>((blocks + most - 1) / most));
 }
 __device__ __forceinline__ int64_t block_index() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
 

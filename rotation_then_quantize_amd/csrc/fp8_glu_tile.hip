@@ -48,7 +48,7 @@ glu_tile_kernel(GluParams p) {
 
     // 8 contiguous ranges of tiles, one per XCD (workgroup b runs on XCD b % 8), a column's tiles next to each other
     const int total = p.tiles_t * p.tiles_n, per = (total + 7) / 8;
-    const int b = static_cast<int>(blockIdx.x), local = b / 8, lin = b % 8 * per + local;
+    const int b = static_cast<int>(block_index()), local = b / 8, lin = b % 8 * per + local;
     if (local >= per || lin >= total) return;
     const int64_t m0 = static_cast<int64_t>(lin % p.tiles_t) * BM;
     const int n0 = lin / p.tiles_t * kChannels;
@@ -180,7 +180,7 @@ hipError_t launch(GluParams p, bool e8m0, hipStream_t stream) {
     p.tiles_t = static_cast<int>((p.T + BM - 1) / BM);
     p.tiles_n = p.N / kChannels;
     const int64_t total = static_cast<int64_t>(p.tiles_t) * p.tiles_n;
-    kernel<<<static_cast<unsigned>((total + 7) / 8 * 8), kThreads, tile_lds<BM>(), stream>>>(p);
+    kernel<<<grid_of((total + 7) / 8 * 8), kThreads, tile_lds<BM>(), stream>>>(p);
     return hipGetLastError();
 }
 

@@ -229,13 +229,13 @@ hipError_t forward(const RmsForwardArgs& a, hipStream_t stream) {
     const RmsForwardParams p{a.x, a.residual, a.rows, a.d, 1.0 / a.d, a.eps, a.gamma, a.h, a.y, a.codes, a.scale, a.e8m0};
     const int team = team_of(a.d);
     if (team == 0) {
-        rmsnorm_forward_long_kernel<kX16, kRes, kR16, kG16><<<grid_of(a.rows), 64 * kMostTeam, 0, stream>>>(p);
+        rmsnorm_forward_long_kernel<kX16, kRes, kR16, kG16><<<grid_of(a.rows, 1 << 21), 64 * kMostTeam, 0, stream>>>(p);
         return hipGetLastError();
     }
     return with_team(team, [&](auto t) {
         constexpr int kTeam = decltype(t)::value, kWaves = forward_waves(kTeam), kTeams = kWaves / kTeam;
         const int64_t blocks = (a.rows + kTeams - 1) / kTeams;
-        rmsnorm_forward_kernel<kX16, kRes, kR16, kG16, kTeam><<<grid_of(blocks), 64 * kWaves, 0, stream>>>(p);
+        rmsnorm_forward_kernel<kX16, kRes, kR16, kG16, kTeam><<<grid_of(blocks, 1 << 21), 64 * kWaves, 0, stream>>>(p);
         return hipGetLastError();
     });
 }

@@ -113,6 +113,9 @@ def test_norm(T, d, xt, rt):
         else:
             rtq.rmsnorm_forward(x, gamma, EPS, residual=r, h=None if r is None else h[:T], y=y2)
         assert same(y2, y[:T].contiguous())
+        own = x.clone()
+        rtq.rmsnorm_forward(own, gamma, EPS, residual=r, h=None if r is None else h[:T], y=own)
+        assert same(own, y2)
 
 
 @pytest.mark.parametrize("T,d", [(4608, 4096), (2050, 208), (8190, 16)])
@@ -319,6 +322,10 @@ def test_glu_non_finite(T, N, K):
     rtq.fp8_glu(x, sx, w, sw, ACTS["silu"], y_codes=c, y_scale=s)
     cf = c.float()
     assert torch.isnan(cf[3]).all() and torch.isnan(cf[:, 150]).all() and torch.isfinite(cf[rows][:, cols]).all()
+    # the other channels' codes go by the largest finite magnitude of their group
+    finite = torch.isfinite(y[rows])
+    want = torch.where(finite, y[rows], torch.zeros_like(y[rows])).double()
+    check_codes(torch.where(finite, cf[rows], torch.zeros_like(cf[rows])), s[:, rows], want, torch.zeros_like(want))
 
 
 @pytest.mark.parametrize("T,N,K", [(5, 256, 144), (16, 128, 1040), (40, 256, 2064), (100, 128, 144), (300, 256, 4112), (2100, 4096, 272)])
@@ -332,6 +339,10 @@ def test_glu_infinite_scale_of_the_last_block(T, N, K):
     y = torch.empty(T, N, device="cuda")
     rtq.fp8_glu(x, sx, w, sw, ACTS["silu"], y=y)
     assert (y[T - 1] == float("inf")).all() and torch.isfinite(y[:T - 1]).all()
+    (c, s), (hc, hs) = empty_rows(T, N), empty_rows(T, 2 * N)
+    rtq.fp8_glu(x, sx, w, sw, ACTS["silu"], y_codes=c, y_scale=s, h_codes=hc, h_scale=hs)
+    assert torch.isnan(c[T - 1].float()).all() and torch.isnan(hc[T - 1].float()).all()      # e4m3 has no infinity
+    assert (s[:, T - 1] == 1.0).all() and (hs[:, T - 1] == 1.0).all() and torch.isfinite(c[:T - 1].float()).all()
     sx[-1, T - 1] = 1.0
     sw[0, -1] = float("inf")
     rtq.fp8_glu(x, sx, w, sw, ACTS["silu"], y=y)
@@ -573,3 +584,65 @@ def test_past_32_bits():
     rtq.glu_fp8_backward(dy1.repeat(530, 1), hc.view(E4M3), hs, ACTS["silu"], dh=dh)
     rtq.glu_fp8_backward(dy1, c1, s1, ACTS["silu"], dh=d1)
     assert same(dh[-1000:], d1) and same(dh[:1000], d1)
+    del dh, hc, hs
+    step("past 2^31: glu")
+    T, N, K = 140000, 8192, 272
+    (x, sx, w, sw), _ = glu_operands(1000, N, K, E8M0)
+    (c1, s1), (hc1, hs1) = empty_rows(1000, N, st=E8M0), empty_rows(1000, 2 * N, st=E8M0)
+    rtq.fp8_glu(x, sx, w, sw, ACTS["silu"], y_codes=c1, y_scale=s1, h_codes=hc1, h_scale=hs1)
+    many = lambda t, n: t.view(torch.uint8).repeat(*n).view(t.dtype)
+    (c, s), (hc, hs) = empty_rows(T, N, st=E8M0), empty_rows(T, 2 * N, st=E8M0)
+    rtq.fp8_glu(many(x, (140, 1)), many(sx, (1, 140)), w, sw, ACTS["silu"], y_codes=c, y_scale=s, h_codes=hc, h_scale=hs)
+    for i in (0, 70, 139):
+        part = slice(1000 * i, 1000 * i + 1000)
+        assert same(c[part], c1) and same(hc[part], hc1)
+        assert same(s[:, part].contiguous(), s1) and same(hs[:, part].contiguous(), hs1)
+
+
+def test_binding_refusals():
+    step("refusals")
+    bf, e = BF16, lambda *s, dt=BF16: torch.empty(*s, dtype=dt, device="cuda")
+    x, gamma, (codes, scale) = e(4, 256), e(256), empty_rows(4, 256)
+    good = dict(codes=codes, scale=scale)
+    for change, error, match in (
+            (dict(codes=codes, scale=None), ValueError, "codes and scale"), (dict(), ValueError, "give y"),
+            (dict(good, residual=x), ValueError, "together"), (dict(good, residual=x, h=e(4, 256, dt=F32)), TypeError, "h: unsupported dtype"),
+            (dict(y=e(4, 256, dt=F32)), TypeError, "y: unsupported"), (dict(y=e(4, 128)), ValueError, "y: shape"),
+            (dict(y=e(256, 4).t()), ValueError, "contiguous"), (dict(codes=codes.view(torch.uint8), scale=scale), TypeError, "codes"),
+            (dict(codes=codes, scale=e(4, 2, dt=F32)), ValueError, "scale: shape"), (dict(good, stream=7), AttributeError, "device_index"),
+            (dict(y=torch.empty(4, 256, dtype=bf)), ValueError, "GPU tensor"), (dict(y="no"), TypeError, "tensor")):
+        with pytest.raises(error, match=match):
+            rtq.rmsnorm_forward(x, gamma, EPS, **change)
+    with pytest.raises(ValueError, match="gamma: shape"):
+        rtq.rmsnorm_forward(x, e(128), EPS, **good)
+    with pytest.raises(rtq.RtqError, match="eps"):
+        rtq.rmsnorm_forward(x, gamma, 0.0, **good)
+    with pytest.raises(rtq.RtqError, match="multiple of 16"):
+        rtq.rmsnorm_forward(e(4, 40), e(40), EPS, y=e(4, 40))
+    with pytest.raises(rtq.RtqError, match="dh must not be h"):
+        rtq.rmsnorm_backward(e(4, 256), x, gamma, EPS, x)
+    with pytest.raises(rtq.RtqError, match="workspace too small"):
+        rtq.rmsnorm_backward(x, e(4, 256), gamma, EPS, e(4, 256), dgamma=e(256), workspace=e(16, dt=torch.uint8))
+    xc, xs = empty_rows(4, 256)
+    w, ws = e(512, 256, dt=E4M3), e(4, 2, dt=F32)
+    for change, error, match in (
+            (dict(), ValueError, "give either y"), (dict(y=e(4, 256), y_codes=xc, y_scale=xs), ValueError, "give either y"),
+            (dict(y=e(4, 256), h_codes=e(4, 512, dt=E4M3)), ValueError, "together"), (dict(y=e(4, 512)), ValueError, "y: shape"),
+            (dict(y_codes=xc, y_scale=e(2, 4, dt=torch.uint8).view(E8M0)), TypeError, "y_scale")):
+        with pytest.raises(error, match=match):
+            rtq.fp8_glu(xc, xs, w, ws, ACTS["silu"], **change)
+    with pytest.raises(ValueError, match="two projections"):
+        rtq.fp8_glu(xc, xs, e(384, 256, dt=E4M3), e(3, 2, dt=F32), ACTS["silu"], y=e(4, 192))
+    with pytest.raises(rtq.RtqError, match="activation"):
+        rtq.fp8_glu(xc, xs, w, ws, 9, y=e(4, 256))
+    with pytest.raises(ValueError, match="give dh"):
+        rtq.glu_fp8_backward(x, e(4, 512, dt=E4M3), e(4, 4, dt=F32), ACTS["silu"])
+    flat = torch.zeros(1001, device="cuda")
+    with pytest.raises(rtq.RtqError, match="aligned"):                 # a view that begins inside a 16-byte line
+        rtq.grad_norm(rtq.TensorList([flat[1:]]), e(1, dt=F32))
+    with pytest.raises(TypeError, match="dtype"):
+        rtq.TensorList([flat.double()])
+    with pytest.raises(ValueError, match="norm: shape"):
+        rtq.grad_norm(rtq.TensorList([flat]), e(2, dt=F32))
+    with pytest.raises(rtq.RtqError, match="most"):
+        rtq.grad_clip(rtq.TensorList([flat]), e(1, dt=F32), -1.0)
