@@ -52,155 +52,211 @@ __device__ __forceinline__ void for_act(int act, F f) {
 // is the whole group's.
 __device__ __forceinline__ uint32_t exponent_byte(uint32_t amax) { return amax == 0u ? 0u : static_cast<uint32_t>(scale_exponent<false>(amax) + 121); }
 __device__ __forceinline__ int byte_exponent(uint32_t b) { return b == 0u ? 0 : static_cast<int>(b) - 121; }
-// 2^-e of a byte's exponent; for zeros, whose codes do not depend on it, 2^121.
-__device__ __forceinline__ float byte_inverse(uint32_t b) { return __uint_as_float((248u - b) << 23); }
+// 2^e of a byte's exponent; for zeros, whose codes do not depend on it, 2^-121.
+__device__ __forceinline__ float byte_scale(uint32_t b) { return __uint_as_float((b + 6u) << 23); }
 // The largest of the four bytes of a word.
 __device__ __forceinline__ uint32_t max_byte(uint32_t w) {
     return max(max(w & 0xffu, w >> 8 & 0xffu), max(w >> 16 & 0xffu, w >> 24));
 }
 
-// Bits of the largest magnitude of m and v: one instruction, whose median with infinity is the larger of two numbers, and
-// where one of them is no number the other one.
-__device__ __forceinline__ float magnitude(float m, float v) {
-    return __builtin_amdgcn_fmed3f(m, __builtin_fabsf(v), __builtin_inff());
+// The largest magnitude of m, a and b in one instruction; of numbers that are none, the others'.  (From fmaxf the compiler makes
+// it with an instruction more for each number.)  a and b must not come straight from a matrix instruction, for whose results
+// the compiler does not wait here.
+__device__ __forceinline__ float magnitude(float m, float a, float b) {
+    float r;
+    asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(m), "v"(a), "v"(b));
+    return r;
 }
 
 // m[i]'s maximum over the four 16-lane rows of a wave, in row i: two swaps of halves for four numbers, then one of rows.
-__device__ __forceinline__ uint32_t max_rows(const uint32_t (&m)[4]) {
-    const auto a = __builtin_amdgcn_permlane32_swap(m[0], m[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(m[1], m[3], false, false);
+__device__ __forceinline__ uint32_t max_rows(float m0, float m1, float m2, float m3) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(m0), __float_as_uint(m2), false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(m1), __float_as_uint(m3), false, false);
     const auto c = __builtin_amdgcn_permlane16_swap(max(a[0], a[1]), max(b[0], b[1]), false, false);
     return max(c[0], c[1]);
 }
 
-constexpr int kGluStage = 2048;                                    // LDS that a wave's outputs go through
+// Codes of four values by 2^e, as encode4 of the values times 2^-e.
+typedef short v2s __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t encode4_by(const float* v, float scale) {
+    v2s w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[0], v[1], scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[2], v[3], scale, true);
+    return __builtin_bit_cast(uint32_t, w);
+}
+
+constexpr int kGluStep = 8192, kGluStage = 3 * kGluStep;           // LDS that outputs go through, in three buffers
 constexpr int glu_bytes(int tokens) { return 3 * tokens * 4; }     // exponents [y, g, u][token][wave]
 
-// The outputs of kR row tiles from kI0 on, kR * 16 tokens of a wave: acc[i][j], j < 2, are the sums of 16 channels' gates
-// (lane: token l % 16, channels 4 (l / 16) .. +4), j + 2 those of their partners.  The tile's first token and channel are m0
-// and n0 (N and n0 multiples of 128); the wave's tokens begin at `row` of the tile, its 32 channels at 32 wn: four waves make
-// a group, and all waves of the workgroup come here.  Codes take the largest magnitudes of 32 channels each, whose exponents
-// the four waves exchange as bytes (the scale's exponent is monotone in the magnitude).  stage: the wave's kGluStage bytes of
-// LDS, so that stores write runs of 32 bytes of a token's codes (of 128 with the other waves'); bytes: glu_bytes of LDS.
-template <int kR, int kI0, bool kE8M0, int TM>
-__device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)[TM][4], int64_t m0, int row, int n0, int wn, int tid,
-                                            uint8_t* stage, uint8_t* bytes, int tokens) {
+// The outputs of kR row tiles from kI0 on, kR * 16 tokens of a wave: acc[i][j], j < 2, are the sums of 16 channels' gates (lane:
+// token l % 16, channels 4 (l / 16) .. +4), j + 2 those of their partners.  All 8 waves of the workgroup come here: wave (wm,
+// wn) has kWaveRows tokens from kWaveRows wm on of the tile and 32 channels from 32 wn on of its 128, a group; m0 and n0 are the
+// tile's first token and channel.  kKeep: with the checkpoint.
+//
+// Codes take the largest magnitudes of 32 channels each, whose exponents the four waves of a group exchange as bytes (the
+// scale's exponent is monotone in the magnitude), and go through LDS to whole lines of a token's 128.  Two barriers for all
+// kinds of codes; kR is as large as the LDS for them allows (4608 x 4096, 16384 channels with the checkpoint: 593 us; the
+// three kinds one after the other, of four row tiles, 611, half of the outputs' time then waits for LDS and barriers).
+//
+// stage: kGluStage bytes of LDS, bytes: glu_bytes, turn: the buffer of the next values, kept from call to call.
+template <int kR, bool kKeep, int kI0, int kWaveRows, bool kE8M0, int TM>
+__device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)[TM][4], int64_t m0, int n0, int wm, int wn, int tid,
+                                            uint8_t* stage, uint8_t* bytes, int& turn) {
+    constexpr int kTokens = 2 * kWaveRows, kKinds = kKeep ? 3 : 1, kBuffer = 32 * kR * kFp8Block;
     static_assert(kR == 2 || kR == 4, "row tiles");
+    static_assert(kKinds * kBuffer <= kGluStage, "a buffer for each kind of codes");
     const int lane = tid & 63, g = lane >> 4, l15 = lane & 15;
     const GluOut& o = p.out;
-    const int64_t cm0 = m0 + row + kI0 * 16;
-    const int cn0 = n0 + wn * 32;
-    float y[kR][8];
+    const int rows = static_cast<int>(min<int64_t>(kTokens, p.T - m0));   // of the tile: what a lane adds to its first is below 2^32
+    float v[kKinds][kR][8];   // y, and g, u
+#pragma unroll
+    for (int i = 0; i < kR; ++i)
+#pragma unroll
+        for (int e = 0; kKeep && e < 8; ++e) {
+            v[kKinds - 2][i][e] = acc[kI0 + i][e / 4][e % 4];
+            v[kKinds - 1][i][e] = acc[kI0 + i][2 + e / 4][e % 4];
+        }
     for_act(o.act, [&](auto act) {
 #pragma unroll
         for (int i = 0; i < kR; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[i][e] = act_value<decltype(act)::value>(acc[kI0 + i][e / 4][e % 4]) * acc[kI0 + i][2 + e / 4][e % 4];
+            for (int e = 0; e < 8; ++e) v[0][i][e] = act_value<decltype(act)::value>(acc[kI0 + i][e / 4][e % 4]) * acc[kI0 + i][2 + e / 4][e % 4];
     });
-    if (o.y != nullptr) {
-        if (o.y_bf16) {   // two row tiles at a time, 64 bytes a token; chunk c of row r at c ^ (r & 3)
-#pragma unroll
-            for (int h = 0; h < kR / 2; ++h) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float* v = y[2 * h + i] + 4 * j;
-                        *reinterpret_cast<uint2*>(stage + (16 * i + l15) * 64 + (((2 * j + (g >> 1)) ^ (l15 & 3)) << 4) + (g & 1) * 8) =
-                            uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                    }
-                lds_done();
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int at = 16 * q + (lane >> 2), c = lane & 3;
-                    const v4i x = *reinterpret_cast<const v4i*>(stage + at * 64 + ((c ^ (at & 3)) << 4));
-                    const int64_t m = cm0 + 32 * h + at;
-                    if (m < p.T) __builtin_nontemporal_store(x, reinterpret_cast<v4i*>(static_cast<uint16_t*>(o.y) + m * p.N + cn0 + 8 * c));
-                }
-                lds_done();
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kR; ++i) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    *reinterpret_cast<v4f*>(stage + l15 * 128 + (((4 * j + g) ^ (l15 & 7)) << 4)) = v4f{y[i][4 * j], y[i][4 * j + 1], y[i][4 * j + 2], y[i][4 * j + 3]};
-                lds_done();
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int at = 8 * q + (lane >> 3), c = lane & 7;
-                    const v4f x = *reinterpret_cast<const v4f*>(stage + at * 128 + ((c ^ (at & 7)) << 4));
-                    const int64_t m = cm0 + 16 * i + at;
-                    if (m < p.T) __builtin_nontemporal_store(x, reinterpret_cast<v4f*>(static_cast<float*>(o.y) + m * p.N + cn0 + 4 * c));
-                }
-                lds_done();
-            }
-        }
-    }
-    const bool codes = o.y_codes != nullptr, keep = o.h_codes != nullptr;
-    if (!codes && !keep) return;
-    // exponents: of this wave's 32 channels, then of the group's 128
-    const int row0 = row + kI0 * 16 + l15;
-    auto value = [&](int kind, int i, int e) { return kind == 0 ? y[i][e] : acc[kI0 + i][(kind - 1) * 2 + e / 4][e % 4]; };
-    auto put_byte = [&](auto kindc) {
-        constexpr int kind = decltype(kindc)::value;
-        float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m[i] = magnitude(m[i], value(kind, i, e));
-        }
-        if (max(max(m[0], m[1]), max(m[2], m[3])) == __builtin_inff()) {   // one branch for all: with one each their latencies add up
-#pragma unroll
-            for (int i = 0; i < kR; ++i) {
-                m[i] = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = __builtin_fabsf(value(kind, i, e));
-                    m[i] = v < __builtin_inff() ? max(m[i], v) : m[i];
-                }
-            }
-        }
-        const uint32_t mine = max_rows({__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]), __float_as_uint(m[3])});
-        if (g < kR) bytes[(kind * tokens + row0 + 16 * g) * 4 + wn] = static_cast<uint8_t>(exponent_byte(mine));
+    __builtin_amdgcn_sched_barrier(0);   // all sums have been read here, as magnitude() wants it
+    // Values.  A step's rows in LDS: those of wave-row 0, then of 1; chunk c (16 bytes) of row r is at c ^ (r & 7).
+    auto buffer = [&]() { return stage + turn * kGluStep; };
+    auto next = [&]() { turn = turn == 2 ? 0 : turn + 1; };
+    auto handed = [&]() {   // what the waves wrote is in LDS, for every wave
+        lds_done();
+        barrier();
     };
-    auto put_codes = [&](auto kindc, void* out, int64_t stride, int column, void* scale, int group) {
-        constexpr int kind = decltype(kindc)::value;
+    if (o.y != nullptr && o.y_bf16) {   // a row tile a step: 32 rows of 256 bytes
 #pragma unroll
         for (int i = 0; i < kR; ++i) {
-            const uint32_t b = max_byte(reinterpret_cast<const uint32_t*>(bytes)[kind * tokens + row0 + 16 * i]);
-            const float inv = byte_inverse(b);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float* y = v[0][i] + 4 * j;
+                *reinterpret_cast<uint2*>(buffer() + (16 * wm + l15) * 256 + (((4 * wn + 2 * j + (g >> 1)) ^ (l15 & 7)) << 4) + (g & 1) * 8) =
+                    uint2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+            }
+            handed();
+            const int r = tid >> 4, c = tid & 15, line = (r >> 4) * kWaveRows + (kI0 + i) * 16 + (r & 15);
+            const v4i x = *reinterpret_cast<const v4i*>(buffer() + r * 256 + ((c ^ (r & 7)) << 4));
+            const uint32_t far = static_cast<uint32_t>(line) * static_cast<uint32_t>(p.N) + static_cast<uint32_t>(8 * c);
+            if (line < rows) __builtin_nontemporal_store(x, reinterpret_cast<v4i*>(static_cast<uint16_t*>(o.y) + m0 * p.N + n0 + far));
+            next();
+        }
+    } else if (o.y != nullptr) {   // half a row tile's rows of each wave-row a step: 16 rows of 512 bytes
+#pragma unroll
+        for (int i = 0; i < kR; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (l15 >> 3 == q) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<v4f*>(buffer() + (8 * wm + (l15 & 7)) * 512 + (((8 * wn + 4 * j + g) ^ (l15 & 7)) << 4)) =
+                            v4f{v[0][i][4 * j], v[0][i][4 * j + 1], v[0][i][4 * j + 2], v[0][i][4 * j + 3]};
+                }
+                handed();
+                const int r = tid >> 5, c = tid & 31, line = (r >> 3) * kWaveRows + (kI0 + i) * 16 + 8 * q + (r & 7);
+                const v4f x = *reinterpret_cast<const v4f*>(buffer() + r * 512 + ((c ^ (r & 7)) << 4));
+                const uint32_t far = static_cast<uint32_t>(line) * static_cast<uint32_t>(p.N) + static_cast<uint32_t>(4 * c);
+                if (line < rows) __builtin_nontemporal_store(x, reinterpret_cast<v4f*>(static_cast<float*>(o.y) + m0 * p.N + n0 + far));
+                next();
+            }
+    }
+    const bool codes = o.y_codes != nullptr;
+    if (!codes && !kKeep) return;
+    // Exponents of this wave's 32 channels, of four parts (a kind's row tile) at a time: lane row k has part k's.
+    const int row0 = kWaveRows * wm + kI0 * 16 + l15;
+    auto largest = [&](const float* x) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) m = magnitude(m, x[e], x[e + 1]);
+        return m;
+    };
+    auto finite = [&](const float* x) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = __builtin_fabsf(x[e]) < __builtin_inff() ? max(m, __builtin_fabsf(x[e])) : m;
+        return m;
+    };
+    auto put_bytes = [&](const float* x0, const float* x1, const float* x2, const float* x3, int kind, bool some) {
+        float m0 = largest(x0), m1 = largest(x1), m2 = largest(x2), m3 = largest(x3);
+        if (max(max(m0, m1), max(m2, m3)) == __builtin_inff()) m0 = finite(x0), m1 = finite(x1), m2 = finite(x2), m3 = finite(x3);
+        const uint32_t mine = max_rows(m0, m1, m2, m3);
+        if (some) bytes[((kind + g / kR) * kTokens + row0 + 16 * (g % kR)) * 4 + wn] = static_cast<uint8_t>(exponent_byte(mine));
+    };
+    if (codes) put_bytes(v[0][0], v[0][1], v[0][kR - 2], v[0][kR - 1], 0, g < kR);
+    if constexpr (kKeep) put_bytes(v[1][0], v[1][1], v[2][0], v[2][1], 1, true);
+    handed();
+    // Codes: a buffer for each kind, 32 kR rows of 128 bytes.  All exponents are read first: behind a write to LDS the compiler
+    // would hold the next read back until it has been done.
+    uint32_t top[kKinds][kR];
+#pragma unroll
+    for (int kind = 0; kind < kKinds; ++kind)
+#pragma unroll
+        for (int i = 0; i < kR; ++i) top[kind][i] = reinterpret_cast<const uint32_t*>(bytes)[kind * kTokens + row0 + 16 * i];
+    uint8_t* mine = stage + (16 * kR * wm + l15) * 128 + 4 * g;
+    const int place[2] = {(2 * wn ^ (l15 & 7)) << 4, ((2 * wn + 1) ^ (l15 & 7)) << 4};
+    auto put_codes = [&](auto kindc, void* scale, int group) {
+        constexpr int kind = decltype(kindc)::value;
+        uint32_t of_mine = 0u;   // lane row i's
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            const uint32_t b = max_byte(top[kind][i]);
+            const float by = byte_scale(b);
+            of_mine = g == i ? b : of_mine;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<uint32_t*>(stage + (16 * i + l15) * 32 + 16 * j + 4 * g) =
-                    encode4<false>(value(kind, i, 4 * j) * inv, value(kind, i, 4 * j + 1) * inv, value(kind, i, 4 * j + 2) * inv, value(kind, i, 4 * j + 3) * inv);
-            const int64_t m = cm0 + 16 * i + l15;
-            if (wn == kind && g == i && m < p.T) store_scale(scale, kE8M0, group * p.T + m, byte_exponent(b));
+                *reinterpret_cast<uint32_t*>(mine + kind * kBuffer + 16 * i * 128 + place[j]) = encode4_by(v[kind][i] + 4 * j, by);
         }
-        lds_done();
-#pragma unroll
-        for (int q = 0; q < kR / 2; ++q) {
-            const int at = 32 * q + (lane >> 1);
-            const v4i x = *reinterpret_cast<const v4i*>(stage + at * 32 + (lane & 1) * 16);
-            const int64_t m = cm0 + at;
-            if (m < p.T) *reinterpret_cast<v4i*>(static_cast<uint8_t*>(out) + m * stride + column + (lane & 1) * 16) = x;
-        }
-        lds_done();
+        if (wn == kind && g < kR && row0 + 16 * g < rows)
+            store_scale(scale, kE8M0, group * p.T + m0 + row0 + 16 * g, byte_exponent(of_mine));
     };
-    constexpr auto kY = std::integral_constant<int, 0>{};
-    constexpr auto kG = std::integral_constant<int, 1>{};
-    constexpr auto kU = std::integral_constant<int, 2>{};
-    if (codes) put_byte(kY);
-    if (keep) {
-        put_byte(kG);
-        put_byte(kU);
+    if (codes) put_codes(std::integral_constant<int, 0>{}, o.y_scale, n0 / kFp8Block);
+    if constexpr (kKeep) {
+        put_codes(std::integral_constant<int, kKinds - 2>{}, o.h_scale, n0 / kFp8Block);
+        put_codes(std::integral_constant<int, kKinds - 1>{}, o.h_scale, (p.N + n0) / kFp8Block);
     }
-    lds_done();
-    barrier();
-    if (codes) put_codes(kY, o.y_codes, p.N, cn0, o.y_scale, n0 / kFp8Block);
-    if (keep) {
-        put_codes(kG, o.h_codes, 2 * static_cast<int64_t>(p.N), cn0, o.h_scale, n0 / kFp8Block);
-        put_codes(kU, o.h_codes, 2 * static_cast<int64_t>(p.N), p.N + cn0, o.h_scale, (p.N + n0) / kFp8Block);
+    handed();
+#pragma unroll
+    for (int q = 0; q < kR / 2; ++q) {
+        const int r = 64 * q + (tid >> 3), c = tid & 7, line = r / (16 * kR) * kWaveRows + kI0 * 16 + r % (16 * kR);   // of the tile
+        const uint8_t* at = stage + r * 128 + ((c ^ (r & 7)) << 4);
+        v4i x[kKinds];
+#pragma unroll
+        for (int kind = 0; kind < kKinds; ++kind) x[kind] = *reinterpret_cast<const v4i*>(at + kind * kBuffer);
+        // a tile's lines are at most 2^28 bytes apart
+        const uint32_t far = static_cast<uint32_t>(line) * static_cast<uint32_t>(p.N) + static_cast<uint32_t>(16 * c);
+        if (line < rows) {
+            if (codes) *reinterpret_cast<v4i*>(static_cast<uint8_t*>(o.y_codes) + m0 * p.N + n0 + far) = x[0];
+            if constexpr (kKeep) {
+                uint8_t* out = static_cast<uint8_t*>(o.h_codes) + m0 * 2 * p.N + n0;
+                const uint32_t twice = 2 * far - static_cast<uint32_t>(16 * c);
+                *reinterpret_cast<v4i*>(out + twice) = x[kKinds - 2];
+                *reinterpret_cast<v4i*>(out + p.N + twice) = x[kKinds - 1];
+            }
+        }
+    }
+    lds_done();   // read before the next barrier, behind which codes are written again ...
+    if (o.y != nullptr) barrier();   // ... and values at once
+}
+
+// All outputs of a tile.
+template <int kWaveRows, bool kE8M0, int TM>
+__device__ __forceinline__ void glu_tile_outputs(const GluParams& p, const v4f (&acc)[TM][4], int64_t m0, int n0, int wm, int wn, int tid,
+                                                 uint8_t* stage, uint8_t* bytes, int& turn) {
+    if (p.out.h_codes != nullptr) {
+        glu_outputs<2, true, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
+        if constexpr (TM >= 4) glu_outputs<2, true, 2, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
+        if constexpr (TM == 8) {
+            glu_outputs<2, true, 4, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
+            glu_outputs<2, true, 6, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
+        }
+    } else {
+        glu_outputs<TM == 2 ? 2 : 4, false, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
+        if constexpr (TM == 8) glu_outputs<4, false, 4, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
     }
 }
 

@@ -11,7 +11,8 @@
 //   - A wave needs two weight scales a stage.  fp32: the row's scale and the two factors are read apart and multiplied
 //     when used (two multiplies a row tile; tables of both products would take eight more registers, and there are none).
 //     E8M0: four rows' bytes a register, the two weights' bytes in one, chosen by the instruction.
-//   - The epilogue (glu_outputs), four row tiles at a time, with one barrier each where codes are written.
+//   - The outputs (glu_outputs), two or four row tiles at a time: f(g) u fits beside the sums, and the LDS that is left holds
+//     their codes.
 //
 // Without the fusion [g u] would be written and read again in fp32: 4608 x 4096 -> 2 x 16384, 1.2 GB.
 #include <hip/hip_runtime.h>
@@ -32,10 +33,10 @@ constexpr int kXcds = 8;
 constexpr int kTileM = 256, kChannels = 128, BN = 2 * kChannels;
 constexpr int kWavesM = 2, kWavesN = 4, kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
 constexpr int kRing = 2 * (kTileM + BN) * BK;
-constexpr int kScaleBytes = 2 * 2 * kThreads * static_cast<int>(sizeof(float));   // [slot][tokens', weights'][thread]
-constexpr int kStageOut = kWaves * kGluStage;
+constexpr int kSlotScales = kTileM + 2 * 64;                                       // tokens', then 64 copies of the two weights'
+constexpr int kScaleBytes = 2 * kSlotScales * static_cast<int>(sizeof(float));
 constexpr int kBytes = glu_bytes(kTileM);
-constexpr int kLds = kRing + kScaleBytes + kStageOut + kBytes;
+constexpr int kLds = kRing + kScaleBytes + kGluStage + kBytes;
 
 // Tile index within the XCD-ordered sequence -> (tile_m, tile_n), in bands of 8 N-tiles.
 __device__ __forceinline__ void tile_of(int lin, int tiles_m, int tiles_n, int* tm, int* tn) {
@@ -73,7 +74,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     const GluParams& p = lp.g;
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
     using Scale = std::conditional_t<kE8M0, uint8_t, float>;
-    Scale* s_scale = reinterpret_cast<Scale*>(lds + kRing);               // [slot][tokens' kThreads, weights' kThreads]
+    Scale* s_scale = reinterpret_cast<Scale*>(lds + kRing);               // [slot][kSlotScales]
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -114,10 +115,11 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     const uint32_t wave_lds = static_cast<uint32_t>(wave * 1024);
 
     // The stage's scales, written to LDS a stage ahead: thread t's are those of token t % BM, where a lane reads its row
-    // tiles' in one run, and of the gate's block (t < 256) or its partner's, next to each other.
+    // tiles' in one run, and of the gate's block (t < 256) or its partner's, next to each other.  (Several threads write the
+    // same value to the same place: without a branch.)
     const int s_row = tid % WM;
-    const int s_at = tid / BM * BM + (tid % BM / WM * 16 + (s_row & 15)) * TM + (s_row >> 4);
-    const int s_wat = kThreads + tid % 256 * 2 + tid / 256;
+    const int s_at = (tid % BM / WM * 16 + (s_row & 15)) * TM + (s_row >> 4);
+    const int s_wat = kTileM + tid % 64 * 2 + tid / 256;
     constexpr int kScaleSize = kE8M0 ? 1 : 4;
     uint32_t r_a = 0u, r_w = 0u;   // as loaded: converting them here would wait for the loads just issued
     auto load_scales = [&]() {
@@ -130,11 +132,11 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     };
     auto write_scales = [&](int slot) {
         if constexpr (kE8M0) {
-            s_scale[slot * 2 * kThreads + s_at] = static_cast<uint8_t>(r_a);
-            s_scale[slot * 2 * kThreads + s_wat] = static_cast<uint8_t>(r_w);
+            s_scale[slot * kSlotScales + s_at] = static_cast<uint8_t>(r_a);
+            s_scale[slot * kSlotScales + s_wat] = static_cast<uint8_t>(r_w);
         } else {
-            s_scale[slot * 2 * kThreads + s_at] = __uint_as_float(r_a);
-            s_scale[slot * 2 * kThreads + s_wat] = __uint_as_float(r_w);
+            s_scale[slot * kSlotScales + s_at] = __uint_as_float(r_a);
+            s_scale[slot * kSlotScales + s_wat] = __uint_as_float(r_w);
         }
     };
     auto issue = [&](int slot) {   // the cursor's stage, and the cursor moves on
@@ -167,11 +169,11 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     float sc[TM], sw[2], last[2] = {0.f, 0.f};
     uint32_t eb[TM / 4], eb_next[TM / 4], ew = 0u, ew_next = 0u;
     auto read_scales = [&](int slot) {
-        const Scale* q = s_scale + slot * 2 * kThreads;
+        const Scale* q = s_scale + slot * kSlotScales;
         if constexpr (kE8M0) {
 #pragma unroll
             for (int i = 0; i < TM / 4; ++i) eb_next[i] = reinterpret_cast<const uint32_t*>(q + (wm * 16 + l15) * TM)[i];
-            ew_next = *reinterpret_cast<const uint16_t*>(q + kThreads);
+            ew_next = *reinterpret_cast<const uint16_t*>(q + kTileM);
         } else {
 #pragma unroll
             for (int i = 0; i < TM / 4; ++i) {
@@ -181,8 +183,8 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
                 sc[4 * i + 2] = x[2];
                 sc[4 * i + 3] = x[3];
             }
-            sw[0] = q[kThreads];
-            sw[1] = q[kThreads + 1];
+            sw[0] = q[kTileM];
+            sw[1] = q[kTileM + 1];
         }
     };
     auto add = [&](v4f& a, const v4f& x, float s) {
@@ -269,7 +271,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     fa[0] = read_a(0, 0);
     fa[1] = read_a(0, 1);
     if constexpr (kE8M0) read_scales(0);
-    int slot = 0;
+    int slot = 0, turn = 0;
     for (int lin = first; lin < end; lin += stride) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
@@ -293,11 +295,8 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         int64_t m0;
         int n0;
         place(lin, &m0, &n0);
-        // four row tiles at a time, so that f(g) u is computed once and fits beside the sums
         uint8_t* stg = lds + kRing + kScaleBytes;
-        glu_outputs<4, 0, kE8M0>(p, acc, m0, wm * WM, n0, wn, again(tid), stg + wave * kGluStage, stg + kStageOut, kTileM);
-        if constexpr (TM == 8)
-            glu_outputs<4, TM - 4, kE8M0>(p, acc, m0, wm * WM, n0, wn, again(tid), stg + wave * kGluStage, stg + kStageOut, kTileM);
+        glu_tile_outputs<WM, kE8M0>(p, acc, m0, n0, wm, wn, again(tid), stg, stg + kGluStage, turn);
     }
     wait_vmcnt<0>();   // nothing is still writing LDS when the workgroup's next tiles, or another workgroup, use it
 }

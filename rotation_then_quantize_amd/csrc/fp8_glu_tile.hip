@@ -35,7 +35,7 @@ glu_tile_kernel(GluParams p) {
     constexpr int WM = BM / kWavesM, TM = WM / 16, TN = 4;
     constexpr int kABytes = BM * BK, kStage = kABytes + BN * BK;
     constexpr int kALoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves, kLoads = kALoads + kWLoads;   // 1 KB loads per wave
-    static_assert(kWaves * kGluStage + glu_bytes(BM) <= kSlots * kStage, "the outputs' LDS");
+    static_assert(kGluStage + glu_bytes(BM) <= kSlots * kStage, "the outputs' LDS");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
     float* table = reinterpret_cast<float*>(lds + kSlots * kStage);   // [block][token], then [block][gate, partner]
@@ -168,7 +168,8 @@ glu_tile_kernel(GluParams p) {
     wait_vmcnt<0>();   // nothing is still writing the LDS that the outputs go through ...
     lds_done();
     barrier();         // ... nor reading it, in any wave
-    glu_outputs<TM, 0, kE8M0>(p, acc, m0, wm * WM, n0, wn, tid, lds + wave * kGluStage, lds + kWaves * kGluStage, BM);
+    int turn = 0;
+    glu_tile_outputs<WM, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds, lds + kGluStage, turn);
 }
 
 template <int BM>
