@@ -40,16 +40,15 @@ struct Place {
     bool bf16;
 };
 
-// The piece of this workgroup: the last tensor that begins at or before it.
+// The piece of this workgroup: of the last tensor that begins at or before it, which all lanes look for at once (arguments are
+// read from host memory: a search in steps takes as many of its round trips).
 __device__ __forceinline__ Place place(const Table& t, uint32_t piece) {
-    int lo = 0, hi = t.count;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (t.first[mid] <= piece)
-            lo = mid;
-        else
-            hi = mid;
-    }
+    static_assert(kMost <= 128, "two tensors a lane");
+    const int lane = static_cast<int>(threadIdx.x & 63);
+    const uint32_t* first = t.first;
+    const uint32_t a = first[min(lane, t.count)], b = first[min(lane + 64, t.count)];
+    const int before = __popcll(__ballot(lane < t.count && a <= piece)) + __popcll(__ballot(lane + 64 < t.count && b <= piece));
+    const int lo = __builtin_amdgcn_readfirstlane(before) - 1;
     const int64_t begin = static_cast<int64_t>(piece - t.first[lo]) * t.piece;
     return {lo, begin, min(begin + t.piece, t.n[lo]), (t.bf16[lo / 32] >> (lo % 32) & 1u) != 0u};
 }
