@@ -50,9 +50,14 @@ glu_small_kernel(GluParams p, float* sums) {
 
     v4i lo[kTiles], hi[kTiles];   // chunks g and g + 4 of 16 rows each: the gate's kC tiles, then their partners
     v4i x0, x1;
-    float sx, sw;                 // sw: lane i holds tile i's
-    const int w_tile = lane % kTiles;
-    const int64_t w_row = static_cast<int64_t>((w_tile / kC * p.N + min(n0 + w_tile % kC * 16, p.N - 16)) / kFp8Block) * blocks;
+    float sx, sw[kTiles];
+    // Block of scales of tile i (48 channels may lie in two).  fp32: each tile's scale is loaded by itself, into a scalar
+    // register.  Bytes have no scalar load: lane i loads tile i's.
+    auto w_row = [&](int i) { return static_cast<int64_t>((i / kC * p.N + min(n0 + i % kC * 16, p.N - 16)) / kFp8Block) * blocks; };
+    const int64_t w_mine = w_row(lane % kTiles);
+    const float* w_tile[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) w_tile[i] = static_cast<const float*>(p.w_scale) + w_row(i);
     uint32_t o0, o1;
     auto begin = [&](int kb) {    // the block's offsets; past the last block all reads as zeros
         const int k = kb * BK + 16 * g;
@@ -68,9 +73,18 @@ glu_small_kernel(GluParams p, float* sums) {
         const int kc = min(kb, blocks - 1);
         x0 = __builtin_amdgcn_raw_buffer_load_b128(rx, o0, 0, 0);
         x1 = __builtin_amdgcn_raw_buffer_load_b128(rx, o1, 0, 0);
-        const float a = load_scale<kE8M0>(p.x_scale, kc * p.T + min(l15, T - 1)), w = load_scale<kE8M0>(p.w_scale, w_row + kc);
+        const float a = load_scale<kE8M0>(p.x_scale, kc * p.T + min(l15, T - 1));
         sx = kb < blocks ? a : 0.f;   // past the last block no infinity meets the zeros
-        sw = kb < blocks ? w : 0.f;
+        if constexpr (kE8M0) {
+            const float w = load_scale<true>(p.w_scale, w_mine + kc);
+            sw[0] = kb < blocks ? w : 0.f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const float w = kC == 3 || i % kC == 0 ? w_tile[i][kc] : sw[i - 1];
+                sw[i] = kb < blocks ? w : 0.f;
+            }
+        }
     };
     v4f acc[kTiles];
 #pragma unroll
@@ -90,7 +104,7 @@ glu_small_kernel(GluParams p, float* sums) {
         const v8i a = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
         float s[kTiles];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) s[i] = sx * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw), i));
+        for (int i = 0; i < kTiles; ++i) s[i] = sx * (kE8M0 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw[0]), i)) : sw[i]);
         const int next = block(turn + 1);
         begin(next);
         load_tokens(next);
@@ -133,7 +147,7 @@ glu_small_kernel(GluParams p, float* sums) {
 }  // namespace
 
 // Channels per workgroup: as many as balance the CUs' rows (13 x 4096, 10880 channels, 680 tiles of 16: three a workgroup, one
-// workgroup on each of 227 CUs, 16.4 us; with two, 84 CUs have two workgroups, 23.3), and of equals the most.
+// workgroup on each of 227 CUs, 17.2 us; with two, 84 CUs have two workgroups, 23.3), and of equals the most.
 hipError_t launch_glu_small(GluParams p, bool e8m0, float* sums, hipStream_t stream) {
     const int tiles = p.N / 16, cus = device_cu_count();
     auto cost = [&](int c) { return ((tiles + c - 1) / c + cus - 1) / cus * c; };

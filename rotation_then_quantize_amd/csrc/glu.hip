@@ -144,24 +144,24 @@ hipError_t launch_small(const GluArgs& a, hipStream_t stream) {
 enum Form : int { kSmall, kSums, kTile64, kTile128, kLarge };
 // Measured with codes (us; T x K, N channels):
 //                        sums    64     128    256 tokens a tile
-//   64 x 512, 1152        7.7    6.2    8.6    9.5
-//   64 x 1024, 4096      10.8    8.2   11.8   13.1
-//   391 x 1936, 1152     13.8   15.9   21.5   24.8
-//   100 x 4096, 1152     12.4   21.0   32.5   36.9
-//   64 x 4096, 4096      14.1   21.5   32.6   36.3
-//   25 x 2048, 16384     16.5   14.2   19.4   21.4
-//   256 x 4096, 4096     22.7   21.4   33.2   37.3
-//   512 x 4096, 4096     30.3   25.2   33.5   37.3
-//   1024 x 4096, 4096    47.7   44.6   35.9   38.5
-//   2048 x 4096, 4096    82     90     72     64.6
-//   128 x 8192, 8192     52     57     73     81
-//   256 x 16384, 4096    83     98    133    159
-// A tile costs its chain of blocks (0.6, 1 and 1.15 us each) as long as each CU has one, so the smallest whose workgroups fit
+//   64 x 512, 1152        8.9    6.3    8.3    9.2
+//   64 x 1024, 4096      10.8    8.2   11.4   12.9
+//   391 x 1936, 1152     13.9   16.0   21.3   24.1
+//   100 x 4096, 1152     12.4   21.1   32.0   35.0
+//   64 x 4096, 4096      14.1   21.5   31.7   34.6
+//   25 x 2048, 16384     16.4   14.2   19.1   20.7
+//   256 x 4096, 4096     20.6   21.4   32.4   35.4
+//   512 x 4096, 4096     28.8   22.4   32.8   35.5
+//   1024 x 4096, 4096    46.1   43.7   35.1   37.2
+//   2048 x 4096, 4096    79.6   88.2   70.1   60.4
+//   128 x 8192, 8192     51.8   57.0   71.4   79.3
+//   256 x 16384, 4096    82.0   97.7  130     156
+// A tile costs its chain of blocks (0.6, 0.95 and 1.05 us each) as long as each CU has one, so the smallest whose workgroups fit
 // at once is taken, and where none fits the largest.  The product that leaves its sums in the workspace splits the reduction
 // over idle CUs and costs a launch: it is better where tiles of 64 are few or the reduction is long.
 // Few tokens: as the weights stream (fp8_glu_small.hip), but where workgroups are fewer than CUs and the reduction long (y
-// alone, with codes, and either from sums: 1 x 16384, 1024 channels 19.6, 21.5, 14.2; 1 x 8192, 1152: 11.3, 13.2, 9.7; 4 x 4096,
-// 1152: 7.3, 9.4, 7.9; 4 x 2048, 1152: 5.2, 7.5, 7.6).  Which outputs are asked for does not choose: y is the same bits with the
+// alone, with codes, and either from sums: 1 x 16384, 1024 channels 19.6, 21.5, 14.0; 1 x 8192, 1152: 11.3, 13.4, 9.7; 4 x 4096,
+// 1152: 7.4, 9.4, 8.4; 4 x 2048, 1152: 5.2, 7.8, 8.3).  Which outputs are asked for does not choose: y is the same bits with the
 // checkpoint and without.
 Form plan(int64_t T, int N, int K) {
     const int64_t cus = device_cu_count();
