@@ -657,7 +657,7 @@ def _bound():
 def rmsnorm_forward(x, gamma, eps: float, residual=None, h=None, codes=None, scale=None, y=None, stream=None):
     """n = h / sqrt(mean h^2 + eps) gamma for rows of h = x, or of h = x + residual, which is written to h [rows][d]
     (residual's type; h may be residual).  n comes back quantised, as codes [rows][d] (e4m3) and scale [groups][rows],
-    as y [rows][d] (x's type), or as both."""
+    as y [rows][d] (x's type), or as both.  Returns the residual stream: h, or x without a residual."""
     status = _bound().rmsnorm_forward(x, gamma, eps, residual, h, codes, scale, y, stream)
     if status:
         _check(status)
@@ -711,37 +711,59 @@ def glu_fp8_backward(dy, h_codes, h_scale, act: int, dh=None, dh_codes=None, dh_
     return dh if dh is not None else (dh_codes, dh_scale)
 
 
+def _overlap(reads, writes) -> bool:
+    """Whether any of the address ranges (begin, end) of writes overlaps another one, of reads or of writes."""
+    read_end = write_end = 0
+    for begin, end, written in sorted([(b, e, False) for b, e in reads if b < e] + [(b, e, True) for b, e in writes if b < e]):
+        if begin < write_end or (written and begin < read_end):
+            return True
+        if written:
+            write_end = max(write_end, end)
+        else:
+            read_end = max(read_end, end)
+    return False
+
+
 class TensorList:
     """Tensors (float32 or bfloat16, contiguous, on one GPU) as grad_norm and grad_clip take them, and where grad_clip puts
-    its results: outs, of the same shapes and types, or the tensors themselves.  It holds them; tensors that a program
-    replaces need a new list."""
+    its results: outs, of the same shapes and types, or the tensors themselves; no out may overlap another out or another
+    tensor.  It holds them; a program that replaces tensors, or their memory, needs a new list."""
 
     def __init__(self, tensors, outs=None):
-        self.tensors = list(tensors)
+        self.tensors = tuple(tensors)
         if not self.tensors:
             raise ValueError("no tensors")
-        self.outs = self.tensors if outs is None else list(outs)
+        self.outs = self.tensors if outs is None else tuple(outs)
         if len(self.outs) != len(self.tensors):
             raise ValueError(f"{len(self.outs)} outs for {len(self.tensors)} tensors")
+        for t in self.tensors + self.outs:
+            if not isinstance(t, _torch().Tensor):
+                raise TypeError(f"tensors are expected, not {type(t).__name__}")
         floats, like, n = _types()[0], self.tensors[0], len(self.tensors)
-        self._c, self._outs, self.count = (_Tensor * n)(), (ctypes.c_void_p * n)(), n
+        self._c, self._outs = (_Tensor * n)(), (ctypes.c_void_p * n)()
+        reads, writes = [], []
         for i, (t, o) in enumerate(zip(self.tensors, self.outs)):
             code = _operand(t, f"tensors[{i}]", floats, t.shape, like)
             _operand(o, f"outs[{i}]", {t.dtype: code}, t.shape, like)
             self._c[i] = _Tensor(t.data_ptr(), t.numel(), code)
             self._outs[i] = o.data_ptr()
+            writes.append((o.data_ptr(), o.data_ptr() + o.nbytes))
+            if t.data_ptr() != o.data_ptr():
+                reads.append((t.data_ptr(), t.data_ptr() + t.nbytes))
+        if _overlap(reads, writes):
+            raise ValueError("an out overlaps another out or another tensor")
         self._like, self._at, self._outs_at = like, ctypes.addressof(self._c), ctypes.addressof(self._outs)
 
 
 def grad_norm_workspace(tensors: TensorList) -> int:
-    return int(load_library().rtq_grad_norm_workspace(tensors._c, tensors.count))
+    return int(load_library().rtq_grad_norm_workspace(tensors._c, len(tensors.tensors)))
 
 
 def grad_norm(tensors: TensorList, norm, workspace=None, stream=None):
     """norm (one float32 on the GPU) = the 2-norm of all tensors together."""
     if workspace is None:
         workspace = _workspace(None, tensors._like, stream, grad_norm_workspace, tensors)
-    status = _bound().grad_norm(tensors._like, tensors._at, tensors.count, norm, workspace, stream)
+    status = _bound().grad_norm(tensors.tensors, tensors._at, norm, workspace, stream)
     if status:
         _check(status)
     return norm
@@ -749,7 +771,7 @@ def grad_norm(tensors: TensorList, norm, workspace=None, stream=None):
 
 def grad_clip(tensors: TensorList, norm, most: float, stream=None):
     """Each tensor times min(1, most / (norm + 1e-6)), to the list's outs."""
-    status = _bound().grad_clip(tensors._like, tensors._at, tensors._outs_at, tensors.count, norm, most, stream)
+    status = _bound().grad_clip(tensors.tensors, tensors._at, tensors.outs, tensors._outs_at, norm, most, stream)
     if status:
         _check(status)
     return tensors.outs

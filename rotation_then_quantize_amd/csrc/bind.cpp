@@ -128,6 +128,8 @@ Operand rows_of(PyObject* o, const char* name, Kind kind) {
     const int code = type_code(kind, t->scalar_type());
     if (code < 0) raise(PyExc_TypeError, std::string(name) + ": unsupported dtype " + c10::toString(t->scalar_type()));
     if (t->dim() != 2) raise(PyExc_ValueError, std::string(name) + ": shape " + text(t->sizes()) + ", expected two dimensions");
+    if (t->size(1) > INT32_MAX || (kind == kE4M3 && t->size(0) / 2 > INT32_MAX))   // the library's lengths
+        raise(PyExc_ValueError, std::string(name) + ": shape " + text(t->sizes()) + " is too large");
     Call{t}.place(*t, name);
     return {t, t->data_ptr(), static_cast<rtq_dtype>(code)};
 }
@@ -159,6 +161,11 @@ int64_t integer(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Raised{};
     return v;
+}
+// An activation's code; one that the library does not know stays one.
+rtq_act act_of(PyObject* o) {
+    const int64_t v = integer(o);
+    return static_cast<rtq_act>(v < 0 || v > INT32_MAX ? INT32_MAX : v);
 }
 bool truth(PyObject* o) {
     const int v = PyObject_IsTrue(o);
@@ -217,7 +224,7 @@ PyObject* fp8_glu(PyObject* const* a) {
         raise(PyExc_ValueError, "w_codes: " + std::to_string(rows) + " rows, expected two projections of a multiple of 128 each");
     const Operand w_scale = call.operand(a[3], "w_scale", kScale, {groups(rows), groups(K)});
     const Operand x_scale = call.operand(a[1], "x_scale", kScale, {groups(K), T}, false, w_scale.type);
-    const int64_t act = integer(a[4]);
+    const rtq_act act = act_of(a[4]);
     const Operand y = call.operand(a[5], "y", kFloat, {T, N}, true);
     const Operand y_codes = call.operand(a[6], "y_codes", kE4M3, {T, N}, true);
     const Operand y_scale = call.operand(a[7], "y_scale", kScale, {groups(N), T}, true, w_scale.type);
@@ -229,7 +236,7 @@ PyObject* fp8_glu(PyObject* const* a) {
     const Workspace ws(call, a[10]);
     return call.run(a[11], [&](void* stream) {
         return lib.fp8_glu(x.ptr, x_scale.ptr, T, w.ptr, w_scale.ptr, w_scale.type, static_cast<int32_t>(N), static_cast<int32_t>(K),
-                           static_cast<rtq_act>(act), h_codes.ptr, h_scale.ptr, y.ptr, y.type, y_codes.ptr, y_scale.ptr, ws.ptr, ws.bytes, stream);
+                           act, h_codes.ptr, h_scale.ptr, y.ptr, y.type, y_codes.ptr, y_scale.ptr, ws.ptr, ws.bytes, stream);
     });
 }
 
@@ -240,14 +247,14 @@ PyObject* glu_fp8_backward(PyObject* const* a) {
     const int64_t T = dy.t->size(0), N = dy.t->size(1);
     const Operand h = call.operand(a[1], "h_codes", kE4M3, {T, 2 * N});
     const Operand h_scale = call.operand(a[2], "h_scale", kScale, {groups(2 * N), T});
-    const int64_t act = integer(a[3]);
+    const rtq_act act = act_of(a[3]);
     const Operand dh = call.operand(a[4], "dh", kFloat, {T, 2 * N}, true, dy.type);
     const Operand codes = call.operand(a[5], "dh_codes", kCode, {T, 2 * N}, true);
     const Operand scale = call.operand(a[6], "dh_scale", kScale, {groups(2 * N), T}, true, h_scale.type);
     if (static_cast<bool>(codes) != static_cast<bool>(scale) || (!dh && !codes))
         raise(PyExc_ValueError, "give dh, or dh_codes and dh_scale, or all of them");
     return call.run(a[7], [&](void* stream) {
-        return lib.glu_fp8_backward(dy.ptr, dy.type, h.ptr, h_scale.ptr, h_scale.type, T, static_cast<int32_t>(N), static_cast<rtq_act>(act),
+        return lib.glu_fp8_backward(dy.ptr, dy.type, h.ptr, h_scale.ptr, h_scale.type, T, static_cast<int32_t>(N), act,
                                     dh.ptr, codes.ptr, codes ? codes.type : RTQ_E4M3, scale.ptr, stream);
     });
 }
@@ -260,25 +267,44 @@ Operand norm_of(const Call& call, PyObject* o) {
     return {t, t->data_ptr(), RTQ_F32};
 }
 
-// first tensor, address of the rtq_tensor array, count, norm, workspace, stream
+// A list's tensors as they were when it was made: a tensor whose memory has been replaced since is refused.
+struct List {
+    const at::Tensor* first;
+    const rtq_tensor* tensors;
+    int32_t count;
+    List(PyObject* tuple, PyObject* array)
+        : tensors(reinterpret_cast<const rtq_tensor*>(integer(array))), count(static_cast<int32_t>(PyTuple_Size(tuple))) {
+        if (count <= 0) throw Raised{};
+        first = tensor(PyTuple_GET_ITEM(tuple, 0), "tensors");
+        for (int32_t i = 0; i < count; ++i) check(PyTuple_GET_ITEM(tuple, i), tensors[i].data, tensors[i].n);
+    }
+    void outs(PyObject* tuple, void* const* at) const {
+        for (int32_t i = 0; i < count; ++i) check(PyTuple_GET_ITEM(tuple, i), at[i], tensors[i].n);
+    }
+    static void check(PyObject* o, const void* data, int64_t n) {
+        const at::Tensor* t = tensor(o, "tensors");
+        if (t->data_ptr() != data || t->numel() != n) raise(PyExc_ValueError, "a tensor's memory has been replaced since the list was made");
+    }
+};
+
+// tuple of tensors, address of their rtq_tensor array, norm, workspace, stream
 PyObject* grad_norm(PyObject* const* a) {
-    const Call call{tensor(a[0], "tensors")};
-    const auto* tensors = reinterpret_cast<const rtq_tensor*>(integer(a[1]));
-    const int32_t count = static_cast<int32_t>(integer(a[2]));
-    const Operand norm = norm_of(call, a[3]);
-    const Workspace ws(call, a[4]);
-    return call.run(a[5], [&](void* stream) { return lib.grad_norm(tensors, count, static_cast<float*>(norm.ptr), ws.ptr, ws.bytes, stream); });
+    const List list(a[0], a[1]);
+    const Call call{list.first};
+    const Operand norm = norm_of(call, a[2]);
+    const Workspace ws(call, a[3]);
+    return call.run(a[4], [&](void* stream) { return lib.grad_norm(list.tensors, list.count, static_cast<float*>(norm.ptr), ws.ptr, ws.bytes, stream); });
 }
 
-// first tensor, address of the rtq_tensor array, address of the outs, count, norm, most, stream
+// tuple of tensors, address of their rtq_tensor array, tuple of outs, address of their addresses, norm, most, stream
 PyObject* grad_clip(PyObject* const* a) {
-    const Call call{tensor(a[0], "tensors")};
-    const auto* tensors = reinterpret_cast<const rtq_tensor*>(integer(a[1]));
-    const auto* outs = reinterpret_cast<void* const*>(integer(a[2]));
-    const int32_t count = static_cast<int32_t>(integer(a[3]));
+    const List list(a[0], a[1]);
+    const Call call{list.first};
+    const auto* outs = reinterpret_cast<void* const*>(integer(a[3]));
+    if (a[2] != a[0]) list.outs(a[2], outs);
     const Operand norm = norm_of(call, a[4]);
     const float most = number(a[5]);
-    return call.run(a[6], [&](void* stream) { return lib.grad_clip(tensors, outs, count, static_cast<const float*>(norm.ptr), most, stream); });
+    return call.run(a[6], [&](void* stream) { return lib.grad_clip(list.tensors, outs, list.count, static_cast<const float*>(norm.ptr), most, stream); });
 }
 
 // No C++ exception goes into the interpreter.
@@ -339,7 +365,7 @@ PyMethodDef methods[] = {
     entry<rmsnorm_backward, 10>("rmsnorm_backward"),
     entry<fp8_glu, 12>("fp8_glu"),
     entry<glu_fp8_backward, 8>("glu_fp8_backward"),
-    entry<grad_norm, 6>("grad_norm"),
+    entry<grad_norm, 5>("grad_norm"),
     entry<grad_clip, 7>("grad_clip"),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -86,6 +86,8 @@ rtq_status rtq_rmsnorm_forward(const void* x, rtq_dtype xt, const void* residual
         RTQ_TRY(check_optional(y, "y"));
         RTQ_TRY(check_optional(codes, "codes"));
         RTQ_TRY(check_optional(scale, "scale"));
+        if (h != nullptr && (y == h || (h == x && rt != xt)))
+            return fail(RTQ_ERR_INVALID_ARG, "h must not be y, nor x of another type");
         const RmsForwardArgs a{x, xt == RTQ_BF16, residual, rt == RTQ_BF16, rows, d, gamma, gt == RTQ_BF16, eps,
                                h, y, codes, scale, st == RTQ_E8M0};
         return hip_status(launch_rmsnorm_forward(a, static_cast<hipStream_t>(stream)), "rmsnorm forward launch");
@@ -116,7 +118,8 @@ rtq_status rtq_rmsnorm_backward(const void* dn, rtq_dtype dnt, const void* h, rt
         RTQ_TRY(check_optional(dresidual, "dresidual"));
         RTQ_TRY(check_optional(dgamma, "dgamma"));
         RTQ_TRY(check_workspace(workspace));
-        if (rows > 0 && dh == h) return fail(RTQ_ERR_INVALID_ARG, "dh must not be h");
+        if (rows > 0 && (dh == h || (dh == dn && dnt != ht)))
+            return fail(RTQ_ERR_INVALID_ARG, "dh must not be h, nor dn of another type");
         if (rows > 0 && dgamma != nullptr) {
             const size_t need = rmsnorm_backward_workspace_bytes(rows, d);
             if (workspace == nullptr) return fail(RTQ_ERR_INVALID_ARG, "workspace is NULL");

@@ -21,7 +21,7 @@ using namespace fp8;
 constexpr int kThreads = 256;
 constexpr int kMost = 96;                        // tensors of a launch: their table fits the 4 KB of arguments
 constexpr int kPass = kThreads * 8;              // elements a workgroup takes at a time
-constexpr int64_t kScalePiece = 2 * kPass;       // elements of a piece that is scaled
+constexpr int64_t kScalePiece = 2 * kPass;       // elements of a piece that is scaled, or more
 
 struct Table {
     const void* data[kMost];
@@ -147,11 +147,13 @@ grad_scale_kernel(Table t, const float* __restrict__ norm, float most) {
 // 158; their sums are two loads a thread).  What is scaled goes in pieces of 4096 (norm and scaling of 805 MB 400 us, with
 // 2048 elements 404, 8192 409, 16384 415, 32768 425; with stores through the cache, which push out what the norm's pass has
 // left there, 454).
-int64_t piece_of(const TensorSpan* t, int count) {
+// Beyond 2^34 elements pieces are larger, so that a launch has fewer than 2^32 work-items.
+int64_t piece_of(const TensorSpan* t, int count, int64_t least, int64_t pieces) {
     int64_t total = 0;
     for (int i = 0; i < count; ++i) total += t[i].n;
-    return std::max<int64_t>(4, (total + 2048 * kPass - 1) / (2048 * kPass)) * kPass;
+    return std::max(least / kPass, (total + pieces * kPass - 1) / (pieces * kPass)) * kPass;
 }
+int64_t norm_piece(const TensorSpan* t, int count) { return piece_of(t, count, 4 * kPass, 2048); }
 
 // f(table, its pieces) for as many tables as the tensors need.
 template <typename F>
@@ -187,7 +189,7 @@ hipError_t each_table(const TensorSpan* t, int count, int64_t piece, F f) {
 }  // namespace
 
 size_t grad_norm_workspace_bytes(const TensorSpan* t, int count) {
-    const int64_t piece = piece_of(t, count);
+    const int64_t piece = norm_piece(t, count);
     int64_t pieces = 0;
     for (int i = 0; i < count; ++i) pieces += (t[i].n + piece - 1) / piece;
     return static_cast<size_t>(pieces) * sizeof(double);
@@ -196,7 +198,7 @@ size_t grad_norm_workspace_bytes(const TensorSpan* t, int count) {
 hipError_t launch_grad_norm(const TensorSpan* t, int count, float* norm, void* workspace, hipStream_t stream) {
     double* part = static_cast<double*>(workspace);
     int64_t done = 0;
-    const hipError_t e = each_table(t, count, piece_of(t, count), [&](const Table& table, int64_t n) {
+    const hipError_t e = each_table(t, count, norm_piece(t, count), [&](const Table& table, int64_t n) {
         grad_squares_kernel<<<static_cast<unsigned>(n), kThreads, 0, stream>>>(table, part + done);
         done += n;
         return hipGetLastError();
@@ -207,7 +209,7 @@ hipError_t launch_grad_norm(const TensorSpan* t, int count, float* norm, void* w
 }
 
 hipError_t launch_grad_clip(const TensorSpan* t, int count, const float* norm, float most, hipStream_t stream) {
-    return each_table(t, count, kScalePiece, [&](const Table& table, int64_t n) {
+    return each_table(t, count, piece_of(t, count, kScalePiece, 1 << 22), [&](const Table& table, int64_t n) {
         grad_scale_kernel<<<static_cast<unsigned>(n), kThreads, 0, stream>>>(table, norm, most);
         return hipGetLastError();
     });

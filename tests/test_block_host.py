@@ -24,7 +24,7 @@ def call(name, good, **change):
     return getattr(rtq.load_library(), name)(*args.values())
 
 
-NORM = dict(x=A, xt=BF16, r=A, rt=F32, rows=4, d=256, gamma=A, gt=BF16, eps=1e-6, h=A, y=None, codes=A, scale=A, st=F32,
+NORM = dict(x=A, xt=BF16, r=A, rt=F32, rows=4, d=256, gamma=A, gt=BF16, eps=1e-6, h=A + 4096, y=None, codes=A, scale=A, st=F32,
             stream=None)
 BACK = dict(dn=A, dnt=BF16, h=A, ht=F32, dr=A, rows=4, d=256, gamma=A, gt=BF16, eps=1e-6, dh=A + 4096, dgamma=A, dgt=F32,
             accumulate=0, ws=A, nbytes=BIG, stream=None)
@@ -40,13 +40,15 @@ REFUSALS = [
         (dict(codes=None), INVALID), (dict(scale=None), INVALID), (dict(codes=None, scale=None), INVALID),
         (dict(codes=A + 8), MISALIGNED), (dict(scale=A + 4), MISALIGNED), (dict(y=A + 8), MISALIGNED), (dict(rows=-1), INVALID),
         (dict(rows=1 << 31), UNSUPPORTED), (dict(d=0), INVALID), (dict(d=40), UNSUPPORTED), (dict(d=(1 << 20) + 16), UNSUPPORTED),
-        (dict(eps=0.0), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID)]),
+        (dict(eps=0.0), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID),
+        (dict(y=A + 4096), INVALID), (dict(h=A), INVALID)]),
     ("rtq_rmsnorm_backward", BACK, [
         (dict(dn=None), INVALID), (dict(h=None), INVALID), (dict(dh=None), INVALID), (dict(gamma=None), INVALID),
         (dict(dn=A + 8), MISALIGNED), (dict(dr=A + 8), MISALIGNED), (dict(dgamma=A + 8), MISALIGNED), (dict(dh=A + 8), MISALIGNED),
         (dict(dh=A), INVALID), (dict(dnt=C4), UNSUPPORTED), (dict(ht=I32), UNSUPPORTED), (dict(gt=S8), UNSUPPORTED),
         (dict(dgt=C4), UNSUPPORTED), (dict(accumulate=2), INVALID), (dict(ws=None), INVALID), (dict(nbytes=16), INVALID),
-        (dict(ws=A + 4), MISALIGNED), (dict(d=24), UNSUPPORTED), (dict(rows=-2), INVALID), (dict(eps=0.0), INVALID)]),
+        (dict(ws=A + 4), MISALIGNED), (dict(d=24), UNSUPPORTED), (dict(rows=-2), INVALID), (dict(eps=0.0), INVALID),
+        (dict(dn=A + 4096), INVALID)]),
     ("rtq_fp8_glu", GLU, [
         (dict(x=None), INVALID), (dict(x_scale=None), INVALID), (dict(w=None), INVALID), (dict(w_scale=None), INVALID),
         (dict(w=A + 8), MISALIGNED), (dict(st=BF16), UNSUPPORTED), (dict(N=0), INVALID), (dict(N=192), UNSUPPORTED),
@@ -146,6 +148,20 @@ def test_binding_refuses_what_the_kernels_do_not_take():
         rtq.TensorList([x])
     with pytest.raises(ValueError, match="outs"):
         rtq.TensorList([x, x], [x])
+    with pytest.raises(TypeError, match="tensors"):
+        rtq.TensorList([x, None])
+    with pytest.raises(ValueError, match="too large"):         # longer than the library's lengths
+        rtq.rmsnorm_forward(torch.zeros(0, (1 << 32) + 256, dtype=bf), gamma, 1e-6, y=x)
+    with pytest.raises(ValueError, match="too large"):
+        rtq.glu_fp8_backward(torch.zeros(0, (1 << 32) + 128, dtype=bf), x, gamma, rtq.RTQ_ACT_SILU, dh=x)
+
+
+@pytest.mark.parametrize("reads,writes,want", [
+    ([], [(0, 8), (8, 16)], False), ([], [(0, 8), (7, 16)], True), ([], [(0, 8), (0, 8)], True), ([(0, 8)], [(8, 16)], False),
+    ([(0, 9)], [(8, 16)], True), ([(4, 6)], [(0, 16)], True), ([(0, 8), (0, 8), (2, 20)], [(20, 24)], False),
+    ([(0, 30), (2, 4)], [(20, 24)], True), ([(5, 5)], [(0, 8), (3, 3)], False), ([(0, 8)], [(0, 8)], True)])
+def test_overlapping_ranges(reads, writes, want):
+    assert rtq._overlap(reads, writes) is want
 
 
 def test_plain_scales_and_gradients():

@@ -646,3 +646,37 @@ def test_binding_refusals():
         rtq.grad_norm(rtq.TensorList([flat]), e(2, dt=F32))
     with pytest.raises(rtq.RtqError, match="most"):
         rtq.grad_clip(rtq.TensorList([flat]), e(1, dt=F32), -1.0)
+
+
+def test_replaced_and_overlapping_tensors_are_refused():
+    x, y, n = torch.ones(1000, device="cuda"), torch.ones(600, device="cuda"), torch.zeros(1, device="cuda")
+    inplace, apart = rtq.TensorList([x, y]), rtq.TensorList([x], [torch.empty_like(x)])
+    assert float(rtq.grad_norm(inplace, n)) == 40.0
+    x.data = torch.ones(1000, device="cuda")       # the list's memory is gone
+    for lst in (inplace, apart):
+        with pytest.raises(ValueError, match="replaced"):
+            rtq.grad_norm(lst, n)
+        with pytest.raises(ValueError, match="replaced"):
+            rtq.grad_clip(lst, n, 1.0)
+    apart = rtq.TensorList([x], [torch.empty_like(x)])
+    apart.outs[0].data = torch.empty_like(x)
+    rtq.grad_norm(apart, n)
+    with pytest.raises(ValueError, match="replaced"):
+        rtq.grad_clip(apart, n, 1.0)
+    for tensors, outs in (([x, x], None), ([x, x[500:]], None), ([x[:500], x[500:]], [x[500:], y[:500]]), ([x[:600]], [x[4:604]])):
+        with pytest.raises(ValueError, match="overlaps"):
+            rtq.TensorList(tensors, outs)
+    assert float(rtq.grad_norm(rtq.TensorList([x, x], [torch.empty_like(x), torch.empty_like(x)]), n)) == pytest.approx(2000 ** 0.5, rel=1e-6)
+
+
+def test_clipping_past_32_bits_of_work_items():
+    n = (1 << 36) + 4099                           # in pieces of 4096 elements, 256 threads each: over 2^32 threads
+    if torch.cuda.mem_get_info()[0] < 2 * n + (8 << 30):
+        pytest.skip("not enough memory")
+    x, norm_ = torch.full((n,), 2.0, dtype=BF16, device="cuda"), torch.empty(1, device="cuda")
+    lst = rtq.TensorList([x])
+    want = 2 * n ** 0.5
+    assert float(rtq.grad_norm(lst, norm_)) == pytest.approx(want, rel=1e-6)
+    rtq.grad_clip(lst, norm_, want / 2)
+    for part in (x[:10000], x[-10000:], x[::1000003]):
+        assert bool((part == 1.0).all())
