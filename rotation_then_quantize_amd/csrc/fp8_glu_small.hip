@@ -1,8 +1,9 @@
 // fp8_glu_small.hip -- the gated feed-forward's product for at most 16 tokens: bound by the weights' bytes.
 //
-// A workgroup takes 16 kC channels, as many rows of the gate and their partners, and the whole reduction, its 8 waves the blocks of 128 in turn.  Each wave loads its operands straight into the matrix instruction's registers, 16
-// rows of its next block as soon as it has multiplied those before.  The waves' sums meet in LDS, in a fixed order, and y = f(g) u
-// is written from there; where codes are wanted, whose scales go over the channels of several workgroups, the sums are
+// A workgroup takes 16 kC channels, as many rows of the gate and their partners, and the whole reduction, its 8 waves the
+// blocks of 128 in turn.  Each wave loads its operands straight into the matrix instruction's registers, 16 rows of its next
+// block as soon as it has multiplied those before.  The waves' sums meet in LDS, in a fixed order, and y = f(g) u is written
+// from there; where codes are wanted, whose scales go over the channels of several workgroups, the sums are written
 // (glu_finish_kernel makes the codes).  A workgroup for the 128 channels of a scale, which needs no second launch, reads at
 // most 32 GB/s on its CU: 1 x 4096, 16384 channels in 39 us, 4096 channels in 33 (25 and 9 so).
 #include <hip/hip_runtime.h>
