@@ -63,8 +63,8 @@ struct LargeParams {
     int full;      // tiles [0, full) are taken whole; the rest as two halves of their tokens
 };
 
-// Tiles of BM tokens: kTileM, or half of that.
-template <int BM, bool kE8M0>
+// Tiles of BM tokens: kTileM, or half of that.  kInside: the instruction applies the scales.
+template <int BM, bool kInside, bool kE8M0>
 __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds, int first, int end, int stride) {
     constexpr int WM = BM / kWavesM, TM = WM / 16, TN = 4;
     constexpr int kABytes = BM * BK, kStage = kABytes + BN * BK;
@@ -73,7 +73,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     static_assert(TM == 4 || TM == 8, "row tiles");
     const GluParams& p = lp.g;
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
-    using Scale = std::conditional_t<kE8M0, uint8_t, float>;
+    using Scale = std::conditional_t<kInside, uint8_t, float>;
     Scale* s_scale = reinterpret_cast<Scale*>(lds + kRing);               // [slot][kSlotScales]
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -131,9 +131,9 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         r_w = load_raw<kE8M0>(sw, 0);
     };
     auto write_scales = [&](int slot) {
-        if constexpr (kE8M0) {
-            s_scale[slot * kSlotScales + s_at] = static_cast<uint8_t>(r_a);
-            s_scale[slot * kSlotScales + s_wat] = static_cast<uint8_t>(r_w);
+        if constexpr (kInside) {
+            s_scale[slot * kSlotScales + s_at] = static_cast<uint8_t>(kE8M0 ? r_a : r_a >> 23);
+            s_scale[slot * kSlotScales + s_wat] = static_cast<uint8_t>(kE8M0 ? r_w : r_w >> 23);
         } else {
             s_scale[slot * kSlotScales + s_at] = __uint_as_float(r_a);
             s_scale[slot * kSlotScales + s_wat] = __uint_as_float(r_w);
@@ -163,14 +163,14 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
 
     v4f acc[TM][TN];
     v8i fw[TN], fa[2];
-    // fp32 scales: the sums of the row tile multiplied last, the tokens' scales, the two weights', and the products
-    // carried over the stage's end.  E8M0: four row tiles' bytes a word, this stage's and the next's.
+    // Scales outside: the sums of the row tile multiplied last, the tokens' scales, the two weights', and the products
+    // carried over the stage's end.  Inside: four row tiles' bytes a word, this stage's and the next's.
     v4f d[TN];
     float sc[TM], sw[2], last[2] = {0.f, 0.f};
     uint32_t eb[TM / 4], eb_next[TM / 4], ew = 0u, ew_next = 0u;
     auto read_scales = [&](int slot) {
         const Scale* q = s_scale + slot * kSlotScales;
-        if constexpr (kE8M0) {
+        if constexpr (kInside) {
 #pragma unroll
             for (int i = 0; i < TM / 4; ++i) eb_next[i] = reinterpret_cast<const uint32_t*>(q + (wm * 16 + l15) * TM)[i];
             ew_next = *reinterpret_cast<const uint16_t*>(q + kTileM);
@@ -191,7 +191,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
 #pragma unroll
         for (int r = 0; r < 4; ++r) a[r] = __builtin_fmaf(x[r], s, a[r]);
     };
-    // E8M0: the scaled product of row tile i and column tile j
+    // kInside: the scaled product of row tile i and column tile j
     auto scaled = [&](auto ic, auto jc) {
         constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[j], fa[i & 1], acc[i][j], 0, 0, j / 2, static_cast<int>(ew),
@@ -201,7 +201,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     // One stage, from `slot`.  What it reads ahead is the next stage of this tile or of the next one; behind the last
     // stage of all that is whatever the other slot holds, and is not used.
     auto stage = [&](int slot) {
-        if constexpr (kE8M0) {
+        if constexpr (kInside) {
 #pragma unroll
             for (int i = 0; i < TM / 4; ++i) eb[i] = eb_next[i];
             ew = ew_next;
@@ -209,13 +209,13 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         auto row = [&](auto ic) {
             constexpr int i = decltype(ic)::value;
             float s[2] = {0.f, 0.f};
-            if constexpr (!kE8M0) {
+            if constexpr (!kInside) {
                 s[0] = i == 0 ? last[0] : sc[i == 0 ? 0 : i - 1] * sw[0];
                 s[1] = i == 0 ? last[1] : sc[i == 0 ? 0 : i - 1] * sw[1];
             }
             auto column = [&](auto jc) {
                 constexpr int j = decltype(jc)::value;
-                if constexpr (kE8M0) {
+                if constexpr (kInside) {
                     scaled(ic, jc);
                 } else {
                     // the sums of the row tile before this one, four instructions old
@@ -228,7 +228,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
             column(std::integral_constant<int, 1>{});
             column(std::integral_constant<int, 2>{});
             column(std::integral_constant<int, 3>{});
-            if constexpr (i == 0 && !kE8M0) read_scales(slot);
+            if constexpr (i == 0 && !kInside) read_scales(slot);
             if constexpr (i + 2 < TM) fa[i & 1] = read_a(slot, i + 2);
             if constexpr (i == TM - 2) {
                 lds_done();          // this wave's last fragments of the stage are in registers
@@ -238,7 +238,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
                 barrier();
                 issue(slot);
                 fa[0] = read_a(1 - slot, 0);
-                if constexpr (kE8M0) read_scales(1 - slot);
+                if constexpr (kInside) read_scales(1 - slot);
             }
             if constexpr (i == TM - 1) fa[1] = read_a(1 - slot, 1);
             __builtin_amdgcn_sched_barrier(0);
@@ -253,7 +253,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
             row(std::integral_constant<int, TM - 2>{});
             row(std::integral_constant<int, TM - 1>{});
         }
-        if constexpr (!kE8M0) {
+        if constexpr (!kInside) {
             last[0] = sc[TM - 1] * sw[0];
             last[1] = sc[TM - 1] * sw[1];
         }
@@ -270,7 +270,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     for (int j = 0; j < TN; ++j) fw[j] = read_w(0, j);
     fa[0] = read_a(0, 0);
     fa[1] = read_a(0, 1);
-    if constexpr (kE8M0) read_scales(0);
+    if constexpr (kInside) read_scales(0);
     int slot = 0, turn = 0;
     for (int lin = first; lin < end; lin += stride) {
 #pragma unroll
@@ -288,7 +288,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
             }
             if (half == 0) set_cursor(lin + stride);
         }
-        if constexpr (!kE8M0) {
+        if constexpr (!kInside) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) add(acc[TM - 1][j], d[j], last[j / 2]);
         }
@@ -301,6 +301,45 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     wait_vmcnt<0>();   // nothing is still writing LDS when the workgroup's next tiles, or another workgroup, use it
 }
 
+// Whether all fp32 scales of tiles first, first + stride, .. (`parts` of a whole one each) are powers of two that E8M0 has.  A
+// wave takes a whole tile's, 256 tokens of a block an instruction.
+__device__ __forceinline__ bool powers_of_two(const GluParams& p, int first, int end, int stride, int parts) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int nk = (p.K + BK - 1) / BK;
+    const uint32_t* xs = static_cast<const uint32_t*>(p.x_scale);
+    const uint32_t* ws = static_cast<const uint32_t*>(p.w_scale);
+    uint32_t bad = 0u;
+    auto look = [&](uint32_t v) { bad |= (v & 0x7fffffu) | (v - 0x800000u > 0x7e800000u ? 1u : 0u); };
+    for (int64_t lin = first + static_cast<int64_t>(wave) * stride; lin < end; lin += kWaves * static_cast<int64_t>(stride)) {
+        int tm, tn;
+        tile_of(static_cast<int>(lin) / parts, p.tiles_t, p.tiles_n, &tm, &tn);
+        const int64_t m = min(static_cast<int64_t>(tm) * kTileM + 4 * lane, p.T - 4);
+        auto scales = [&](int kb) {
+            struct { uint32_t v[4]; } q;   // at any token: 4-byte alignment
+            __builtin_memcpy(&q, xs + kb * p.T + m, sizeof(q));
+            return q;
+        };
+        int kb = 0;
+        for (; kb + 16 <= nk; kb += 16) {
+            decltype(scales(0)) q[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) q[i] = scales(kb + i);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) look(q[i].v[e]);
+        }
+        for (; kb < nk; ++kb) {
+            const auto q = scales(kb);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) look(q.v[e]);
+        }
+        for (int i = lane; i < 2 * nk; i += 64)
+            look(ws[static_cast<int64_t>(i < nk ? tn : p.N / kFp8Block + tn) * nk + (i < nk ? i : i - nk)]);
+    }
+    return __syncthreads_or(static_cast<int>(bad)) == 0;
+}
+
 template <bool kE8M0>
 __global__ void __launch_bounds__(kThreads, 1)
 glu_large_kernel(LargeParams p) {
@@ -309,12 +348,22 @@ glu_large_kernel(LargeParams p) {
     // range together, in bands of 8 N-tiles, and share operand panels in that L2.
     const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds, stride = gridDim.x / kXcds;
     const int per = (p.full + kXcds - 1) / kXcds;
-    large_tiles<kTileM, kE8M0>(p, lds, xcd * per + local, min((xcd + 1) * per, p.full), stride);
-    const int rest = 2 * (p.g.tiles_t * p.g.tiles_n - p.full), rper = (rest + kXcds - 1) / kXcds;
-    if (rest > 0) {
-        __syncthreads();
-        const int r0 = 2 * p.full;
-        large_tiles<kTileM / 2, kE8M0>(p, lds, r0 + xcd * rper + local, r0 + min((xcd + 1) * rper, rest), stride);
+    const int first = xcd * per + local, end = min((xcd + 1) * per, p.full);
+    const int rest = 2 * (p.g.tiles_t * p.g.tiles_n - p.full), rper = (rest + kXcds - 1) / kXcds, r0 = 2 * p.full;
+    const int rfirst = r0 + xcd * rper + local, rend = r0 + min((xcd + 1) * rper, rest);
+    auto tiles = [&](auto inside) {
+        constexpr bool kInside = decltype(inside)::value;
+        large_tiles<kTileM, kInside, kE8M0>(p, lds, first, end, stride);
+        if (rest > 0) {
+            __syncthreads();
+            large_tiles<kTileM / 2, kInside, kE8M0>(p, lds, rfirst, rend, stride);
+        }
+    };
+    if constexpr (kE8M0) {
+        tiles(std::true_type{});
+    } else {
+        const bool inside = powers_of_two(p.g, first, end, stride, 1) && powers_of_two(p.g, rfirst, rend, stride, 2);
+        inside ? tiles(std::true_type{}) : tiles(std::false_type{});
     }
 }
 

@@ -281,6 +281,27 @@ def check_glu(T, N, K, st, name):
     assert not ws[need:].any()                            # nothing past the size asked for
 
 
+@pytest.mark.parametrize("odd", [3.0, 0.0, -1.0, 2.0 ** -140, 2.0 ** -126])
+@pytest.mark.parametrize("T,N,K", [(2100, 4096, 272), (4610, 2176, 2064)])
+def test_glu_large_with_an_odd_scale(T, N, K, odd):
+    """One scale among powers of two that is none, or at the ends of their range, of a token or of a block of weights."""
+    step("glu odd scale", T, N, K, odd)
+    for rows, at in ((1, (-1, T - 1)), (1, (0, 700)), (3, (N // 128 + 5, 1)), (3, (2, -1))):
+        dev, _ = glu_operands(T, N, K, F32)
+        dev[rows][at] = odd
+        x, sx, w, sw = (t.double() for t in dev)
+        xv, wv = x * sx.t().repeat_interleave(128, 1)[:, :K], w * sw.repeat_interleave(128, 0).repeat_interleave(128, 1)[:, :K]
+        h = xv @ wv.t().contiguous()
+        y = torch.empty(T, N, device="cuda")
+        rtq.fp8_glu(*dev, ACTS["silu"], y=y)
+        want = glu(h, "silu")
+        lost = 0.0
+        if 0.0 < odd < 2.0 ** -100:    # each of a block's eight additions may cut the running sum off by a unit of its last place
+            most = 8 * 2.0 ** -23 * (xv.abs() @ wv.abs().t().contiguous())
+            lost = 1.1 * h[:, N:].abs() * most[:, :N] + h[:, :N].abs() * most[:, N:] + 1.1 * most[:, :N] * most[:, N:]
+        near(y, want, act_bound(h, "silu") * want.abs() + TINY * (1 + h[:, N:].abs()) + lost)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 512, 2048), (16, 256, 4096), (100, 384, 1040), (300, 512, 2064), (1100, 4096, 1040)])
 def test_glu_general(T, N, K):
     """General fp32 scales and codes over the whole range; equal calls give equal bits."""
