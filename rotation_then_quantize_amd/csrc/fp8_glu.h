@@ -95,8 +95,9 @@ constexpr int glu_bytes(int tokens) { return 3 * tokens * 4; }     // exponents 
 //
 // Codes take the largest magnitudes of 32 channels each, whose exponents the four waves of a group exchange as bytes (the
 // scale's exponent is monotone in the magnitude), and go through LDS to whole lines of a token's 128.  Two barriers for all
-// kinds of codes; kR is as large as the LDS for them allows (4608 x 4096, 16384 channels with the checkpoint: 593 us; the
-// three kinds one after the other, of four row tiles, 611, half of the outputs' time then waits for LDS and barriers).
+// kinds of codes; kR is as large as the LDS for them allows (4608 x 4096, 16384 channels with the checkpoint, fp32 scales outside the
+// instruction: 593 us; the three kinds one after the other, of four row tiles, 611, half of the outputs' time then waits for LDS
+// and barriers).
 //
 // stage: kGluStage bytes of LDS, bytes: glu_bytes, turn: the buffer of the next values, kept from call to call.
 template <int kR, bool kKeep, int kI0, int kWaveRows, bool kE8M0, int TM>

@@ -8,9 +8,12 @@
 //   - The 256 weight rows of a stage are 128 of the gate and the same 128 channels' of the other projection, laid so that
 //     a wave's column tiles 0 and 1 are 32 channels' gates and 2 and 3 their partners: g and u of a channel and token meet
 //     in one lane.
-//   - A wave needs two weight scales a stage.  fp32: the row's scale and the two factors are read apart and multiplied
-//     when used (two multiplies a row tile; tables of both products would take eight more registers, and there are none).
-//     E8M0: four rows' bytes a register, the two weights' bytes in one, chosen by the instruction.
+//   - A wave needs two weight scales a stage.  Inside the instruction (E8M0, and fp32 where all scales of a workgroup's tiles
+//     are powers of two, as the quantiser makes them): four rows' bytes a register, the two weights' bytes in one, chosen by
+//     the instruction.  Any other fp32 scales: the row's scale and the two factors are read apart and multiplied when used
+//     (two multiplies a row tile; tables of both products would take eight more registers, and there are none).  Looking
+//     through the scales takes 2 us (1 where a weight's is none), the additions in fp32 that it saves a tenth of the time (4608 x 4096, 16384 channels, to
+//     codes: 502 us inside, 554 outside; with the checkpoint 538 and 588).
 //   - The outputs (glu_outputs), two or four row tiles at a time: f(g) u fits beside the sums, and the LDS that is left holds
 //     their codes.
 //
@@ -302,7 +305,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
 }
 
 // Whether all fp32 scales of tiles first, first + stride, .. (`parts` of a whole one each) are powers of two that E8M0 has.  A
-// wave takes a whole tile's, 256 tokens of a block an instruction.
+// wave takes a whole tile's: the weights', then the tokens', 256 of a block an instruction.
 __device__ __forceinline__ bool powers_of_two(const GluParams& p, int first, int end, int stride, int parts) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int nk = (p.K + BK - 1) / BK;
@@ -313,6 +316,9 @@ __device__ __forceinline__ bool powers_of_two(const GluParams& p, int first, int
     for (int64_t lin = first + static_cast<int64_t>(wave) * stride; lin < end; lin += kWaves * static_cast<int64_t>(stride)) {
         int tm, tn;
         tile_of(static_cast<int>(lin) / parts, p.tiles_t, p.tiles_n, &tm, &tn);
+        for (int i = lane; i < 2 * nk; i += 64)
+            look(ws[static_cast<int64_t>(i < nk ? tn : p.N / kFp8Block + tn) * nk + (i < nk ? i : i - nk)]);
+        if (__any(bad != 0u)) break;
         const int64_t m = min(static_cast<int64_t>(tm) * kTileM + 4 * lane, p.T - 4);
         auto scales = [&](int kb) {
             struct { uint32_t v[4]; } q;   // at any token: 4-byte alignment
@@ -334,8 +340,6 @@ __device__ __forceinline__ bool powers_of_two(const GluParams& p, int first, int
 #pragma unroll
             for (int e = 0; e < 4; ++e) look(q.v[e]);
         }
-        for (int i = lane; i < 2 * nk; i += 64)
-            look(ws[static_cast<int64_t>(i < nk ? tn : p.N / kFp8Block + tn) * nk + (i < nk ? i : i - nk)]);
     }
     return __syncthreads_or(static_cast<int>(bad)) == 0;
 }
