@@ -204,13 +204,14 @@ def test_norm_backward_without_rows():
 
 # ------------------------------------------------------------------ gated feed-forward
 
-def glu_operands(T, N, K, st):
-    """Whole-number codes to 4 and power-of-two scales: sums are exact in fp32, of some hundredths to tens."""
+def glu_operands(T, N, K, st, by=1.0):
+    """Whole-number codes to 4 and power-of-two scales, the weights' times `by`: sums are exact in fp32, of some hundredths to
+    tens."""
     g = gen(T + N + K)
     x = torch.randint(-4, 5, (T, K), generator=g, device="cuda").float().to(E4M3)
     w = torch.randint(-4, 5, (2 * N, K), generator=g, device="cuda").float().to(E4M3)
     sx = torch.exp2(torch.randint(-6, -3, (groups(K), T), generator=g, device="cuda").float())
-    sw = torch.exp2(torch.randint(-5, -2, (groups(2 * N), groups(K)), generator=g, device="cuda").float())
+    sw = by * torch.exp2(torch.randint(-5, -2, (groups(2 * N), groups(K)), generator=g, device="cuda").float())
     xv = x.double() * sx.double().t().repeat_interleave(128, 1)[:, :K]
     wv = w.double() * sw.double().repeat_interleave(128, 0).repeat_interleave(128, 1)[:, :K]
     return (x, sx.to(st), w, sw.to(st)), xv @ wv.t().contiguous()
@@ -242,17 +243,18 @@ def test_glu_activations(T, N, K, st, name):
     check_glu(T, N, K, st, name)
 
 
-@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("st,by", [(F32, 1.0), (F32, 1.5), (E8M0, 1.0)])
 @pytest.mark.parametrize("T,N,K", [(4608, 2176, 640), (4099, 4096, 144), (2500, 2816, 2064), (8300, 1152, 272), (1500, 16384, 384),
                                    (4608, 1024, 112)])
-def test_glu_large(T, N, K, st):
-    """Whole rounds of tiles and parts of one, few blocks of the reduction and many, ragged last rows."""
-    check_glu(T, N, K, st, "silu")
+def test_glu_large(T, N, K, st, by):
+    """Whole rounds of tiles and parts of one, few blocks of the reduction and many, ragged last rows; scales inside the
+    instruction and outside."""
+    check_glu(T, N, K, st, "silu", by)
 
 
-def check_glu(T, N, K, st, name):
-    step("glu", T, N, K, st, name)
-    dev, h = glu_operands(T, N, K, st)
+def check_glu(T, N, K, st, name, by=1.0):
+    step("glu", T, N, K, st, name, by)
+    dev, h = glu_operands(T, N, K, st, by)
     want = glu(h, name)
     off = act_bound(h, name) * want.abs() + TINY * (1 + h[:, N:].abs())
     need = rtq.fp8_glu_workspace(T, N, K)
