@@ -1,8 +1,10 @@
 // fp8_glu_small.hip -- the gated feed-forward's product for at most 16 tokens: bound by the weights' bytes.
 //
 // A workgroup takes 16 kC channels, as many rows of the gate and their partners, and the whole reduction, its 8 waves the
-// blocks of 128 in turn.  Each wave loads its operands straight into the matrix instruction's registers, 16 rows of its next
-// block as soon as it has multiplied those before.  The waves' sums meet in LDS, in a fixed order, and y = f(g) u is written
+// blocks of 128 in turn.  Each wave loads its operands into registers, 16 rows of its next block as soon as it has decoded those
+// before.  They are multiplied as bf16, which has every code's value: its products are added in fp32 (1e-7 of the sums' 2-norm;
+// the 8-bit instruction aligns them first, 2e-5), and their time goes beside the loads' (1 x 4096, 16384 channels: 24.1 us; with
+// the rows' loads behind the products 26.0, the 8-bit instruction so 25.2).  The waves' sums meet in LDS, in a fixed order, and y = f(g) u is written
 // from there; where codes are wanted, whose scales go over the channels of several workgroups, the sums are written
 // (glu_finish_kernel makes the codes).  A workgroup for the 128 channels of a scale, which needs no second launch, reads at
 // most 32 GB/s on its CU: 1 x 4096, 16384 channels in 39 us, 4096 channels in 33 (25 and 9 so).
@@ -22,6 +24,18 @@ namespace {
 using namespace fp8;
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+// The values of eight e4m3 codes.
+__device__ __forceinline__ v8bf values(int lo, int hi) {
+    const auto a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<uint32_t>(lo), 1.f, false);
+    const auto b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<uint32_t>(lo), 1.f, true);
+    const auto c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<uint32_t>(hi), 1.f, false);
+    const auto d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<uint32_t>(hi), 1.f, true);
+    return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ v4f products(const v8bf& w, const v8bf& a, const v4f& c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, a, c, 0, 0, 0); }
 
 // sums: [T][2 N] fp32, or nullptr: y is written
 template <int kC, bool kE8M0>
@@ -102,7 +116,7 @@ glu_small_kernel(GluParams p, float* sums) {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) load_tile(i);
     for (int turn = 0; turn < turns; ++turn) {
-        const v8i a = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        const v8bf a[4] = {values(x0.x, x0.y), values(x0.z, x0.w), values(x1.x, x1.y), values(x1.z, x1.w)};
         float s[kTiles];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) s[i] = sx * (kE8M0 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw[0]), i)) : sw[i]);
@@ -111,11 +125,13 @@ glu_small_kernel(GluParams p, float* sums) {
         load_tokens(next);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-            const v8i w = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
-            const v4f d = mfma<false>(w, a, v4f{0.f, 0.f, 0.f, 0.f});
+            const v8bf w[4] = {values(lo[i].x, lo[i].y), values(lo[i].z, lo[i].w), values(hi[i].x, hi[i].y), values(hi[i].z, hi[i].w)};
+            load_tile(i);
+            constexpr v4f zero = {0.f, 0.f, 0.f, 0.f};
+            const v4f d = products(w[2], a[2], products(w[0], a[0], zero)) + products(w[3], a[3], products(w[1], a[1], zero));
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(d[r], s[i], acc[i][r]);
-            load_tile(i);
+            __builtin_amdgcn_sched_barrier(0);   // the loads stay before the products
         }
     }
 #pragma unroll
