@@ -266,7 +266,7 @@ __device__ __forceinline__ void glu_tile_outputs(const GluParams& p, const v4f (
 fp8::GluParams glu_params(const GluArgs& a);
 // 256 tokens by 128 channels per workgroup; reductions of at least two blocks.
 hipError_t launch_glu_large(const fp8::GluParams& p, bool e8m0, hipStream_t stream);
-// At most 16 tokens.  sums: [T][2 N] fp32 receives [g u], or nullptr: y is written.
+// At most 32 tokens.  sums: [T][2 N] fp32 receives [g u], or nullptr: y is written.
 hipError_t launch_glu_small(fp8::GluParams p, bool e8m0, float* sums, hipStream_t stream);
 // `tokens` (64 or 128) by 128 channels per workgroup.
 hipError_t launch_glu_tile(const fp8::GluParams& p, bool e8m0, int tokens, hipStream_t stream);

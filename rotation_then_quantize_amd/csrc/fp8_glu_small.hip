@@ -1,4 +1,4 @@
-// fp8_glu_small.hip -- the gated feed-forward's product for at most 16 tokens: bound by the weights' bytes.
+// fp8_glu_small.hip -- the gated feed-forward's product for at most 32 tokens: bound by the weights' bytes.
 //
 // A workgroup takes 16 kC channels, as many rows of the gate and their partners, and the whole reduction, its 8 waves the
 // blocks of 128 in turn.  Each wave loads its operands into registers, 16 rows of its next block as soon as it has decoded those
@@ -7,7 +7,7 @@
 // the rows' loads behind the products 26.0, the 8-bit instruction so 25.2).  The waves' sums meet in LDS, in a fixed order, and y = f(g) u is written
 // from there; where codes are wanted, whose scales go over the channels of several workgroups, the sums are written
 // (glu_finish_kernel makes the codes).  A workgroup for the 128 channels of a scale, which needs no second launch, reads at
-// most 32 GB/s on its CU: 1 x 4096, 16384 channels in 39 us, 4096 channels in 33 (25 and 9 so).
+// most 32 GB/s on its CU: 1 x 4096, 16384 channels in 39 us, 4096 channels in 33 (24 and 8 so).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -37,8 +37,8 @@ __device__ __forceinline__ v8bf values(int lo, int hi) {
 }
 __device__ __forceinline__ v4f products(const v8bf& w, const v8bf& a, const v4f& c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, a, c, 0, 0, 0); }
 
-// sums: [T][2 N] fp32, or nullptr: y is written
-template <int kC, bool kE8M0>
+// kTT tiles of 16 tokens.  sums: [T][2 N] fp32, or nullptr: y is written
+template <int kC, int kTT, bool kE8M0>
 __global__ void __launch_bounds__(kThreads)
 glu_small_kernel(GluParams p, float* sums) {
     constexpr int kTiles = 2 * kC, kSums = kTiles * 64;
@@ -49,7 +49,7 @@ glu_small_kernel(GluParams p, float* sums) {
     const int K = p.K, blocks = (K + BK - 1) / BK, T = static_cast<int>(p.T);
 
     // 8 contiguous ranges of channels, one per XCD (workgroup b runs on XCD b % 8); an XCD's workgroups begin at the same
-    // place of their rows, see below (1 x 4096, 16384 channels: 25.3 us, neighbours on different XCDs 32.1)
+    // place of their rows, see below (1 x 4096, 16384 channels: 24.1 us, neighbours on different XCDs 32.1)
     const int total = p.tiles_n, per = (total + 7) / 8;
     const int b = static_cast<int>(blockIdx.x), local = b / 8, lin = b % 8 * per + local;
     if (local >= per || lin >= total) return;
@@ -64,8 +64,8 @@ glu_small_kernel(GluParams p, float* sums) {
     const uint32_t off = static_cast<uint32_t>(l15 * K + 16 * g), tile = static_cast<uint32_t>(16 * K);
 
     v4i lo[kTiles], hi[kTiles];   // chunks g and g + 4 of 16 rows each: the gate's kC tiles, then their partners
-    v4i x0, x1;
-    float sx, sw[kTiles];
+    v4i x0[kTT], x1[kTT];
+    float sx[kTT], sw[kTiles];
     // Block of scales of tile i (48 channels may lie in two).  fp32: each tile's scale is loaded by itself, into a scalar
     // register.  Bytes have no scalar load: lane i loads tile i's.
     auto w_row = [&](int i) { return static_cast<int64_t>((i / kC * p.N + min(n0 + i % kC * 16, p.N - 16)) / kFp8Block) * blocks; };
@@ -86,10 +86,13 @@ glu_small_kernel(GluParams p, float* sums) {
     };
     auto load_tokens = [&](int kb) {
         const int kc = min(kb, blocks - 1);
-        x0 = __builtin_amdgcn_raw_buffer_load_b128(rx, o0, 0, 0);
-        x1 = __builtin_amdgcn_raw_buffer_load_b128(rx, o1, 0, 0);
-        const float a = load_scale<kE8M0>(p.x_scale, kc * p.T + min(l15, T - 1));
-        sx = kb < blocks ? a : 0.f;   // past the last block no infinity meets the zeros
+#pragma unroll
+        for (int t = 0; t < kTT; ++t) {
+            x0[t] = __builtin_amdgcn_raw_buffer_load_b128(rx, o0 + t * tile, 0, 0);
+            x1[t] = __builtin_amdgcn_raw_buffer_load_b128(rx, o1 + t * tile, 0, 0);
+            const float a = load_scale<kE8M0>(p.x_scale, kc * p.T + min(16 * t + l15, T - 1));
+            sx[t] = kb < blocks ? a : 0.f;   // past the last block no infinity meets the zeros
+        }
         if constexpr (kE8M0) {
             const float w = load_scale<true>(p.w_scale, w_mine + kc);
             sw[0] = kb < blocks ? w : 0.f;
@@ -101,9 +104,11 @@ glu_small_kernel(GluParams p, float* sums) {
             }
         }
     };
-    v4f acc[kTiles];
+    v4f acc[kTiles][kTT];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int t = 0; t < kTT; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
     // The wave's blocks: wave + 8 j, j over turns from a place of the XCD's own: rows a power of two apart share memory
     // channels, and workgroups at the same place of their rows would crowd them (33.6 us).
     const int turns = (blocks + kWaves - 1) / kWaves, start = b % turns;
@@ -116,10 +121,18 @@ glu_small_kernel(GluParams p, float* sums) {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) load_tile(i);
     for (int turn = 0; turn < turns; ++turn) {
-        const v8bf a[4] = {values(x0.x, x0.y), values(x0.z, x0.w), values(x1.x, x1.y), values(x1.z, x1.w)};
-        float s[kTiles];
+        v8bf a[kTT][4];
+        float s[kTT], now[kTiles];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) s[i] = sx * (kE8M0 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw[0]), i)) : sw[i]);
+        for (int t = 0; t < kTT; ++t) {
+            a[t][0] = values(x0[t].x, x0[t].y);
+            a[t][1] = values(x0[t].z, x0[t].w);
+            a[t][2] = values(x1[t].x, x1[t].y);
+            a[t][3] = values(x1[t].z, x1[t].w);
+            s[t] = sx[t];
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) now[i] = kE8M0 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw[0]), i)) : sw[i];
         const int next = block(turn + 1);
         begin(next);
         load_tokens(next);
@@ -128,56 +141,77 @@ glu_small_kernel(GluParams p, float* sums) {
             const v8bf w[4] = {values(lo[i].x, lo[i].y), values(lo[i].z, lo[i].w), values(hi[i].x, hi[i].y), values(hi[i].z, hi[i].w)};
             load_tile(i);
             constexpr v4f zero = {0.f, 0.f, 0.f, 0.f};
-            const v4f d = products(w[2], a[2], products(w[0], a[0], zero)) + products(w[3], a[3], products(w[1], a[1], zero));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(d[r], s[i], acc[i][r]);
+            for (int t = 0; t < kTT; ++t) {
+                const v4f d = products(w[2], a[t][2], products(w[0], a[t][0], zero)) + products(w[3], a[t][3], products(w[1], a[t][1], zero));
+                const float by = s[t] * now[i];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][t][r] = __builtin_fmaf(d[r], by, acc[i][t][r]);
+            }
             __builtin_amdgcn_sched_barrier(0);   // the loads stay before the products
         }
     }
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) s_sums[wave * kSums + i * 64 + lane] = acc[i];
-    __syncthreads();
-    auto sum = [&](int e) {
-        v4f s = s_sums[e];
+    for (int t = 0; t < kTT; ++t) {
+        if (t > 0) __syncthreads();
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) s += s_sums[w * kSums + e];
-        return s;
-    };
-    // a wave takes 16 rows: lane l token l % 16, channels 4 (l / 16) .. +4
-    if (sums != nullptr) {
-        const int c = n0 + wave % kC * 16 + 4 * g;
-        if (wave >= kTiles) return;
-        const v4f s = sum(tid);
-        if (l15 < T && c < p.N) *reinterpret_cast<v4f*>(sums + (static_cast<int64_t>(l15) * 2 + wave / kC) * p.N + c) = s;
-        return;
+        for (int i = 0; i < kTiles; ++i) s_sums[wave * kSums + i * 64 + lane] = acc[i][t];
+        __syncthreads();
+        auto sum = [&](int e) {
+            v4f v = s_sums[e];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) v += s_sums[w * kSums + e];
+            return v;
+        };
+        // a wave takes 16 rows: lane l token l % 16, channels 4 (l / 16) .. +4
+        const int token = 16 * t + l15;
+        if (sums != nullptr) {
+            const int c = n0 + wave % kC * 16 + 4 * g;
+            if (wave < kTiles) {
+                const v4f v = sum(tid);
+                if (token < T && c < p.N) *reinterpret_cast<v4f*>(sums + (static_cast<int64_t>(token) * 2 + wave / kC) * p.N + c) = v;
+            }
+        } else if (wave < kC) {
+            const v4f gate = sum(tid), up = sum(tid + 64 * kC);
+            v4f y;
+            for_act(p.out.act, [&](auto act) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] = act_value<decltype(act)::value>(gate[r]) * up[r];
+            });
+            store4(p.out.y, p.out.y_bf16, T, p.N, token, n0 + wave * 16 + 4 * g, y);
+        }
     }
-    if (wave >= kC) return;
-    const v4f gate = sum(tid), up = sum(tid + 64 * kC);
-    v4f y;
-    for_act(p.out.act, [&](auto act) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = act_value<decltype(act)::value>(gate[r]) * up[r];
-    });
-    store4(p.out.y, p.out.y_bf16, T, p.N, l15, n0 + wave * 16 + 4 * g, y);
 }
 
 }  // namespace
 
-// Channels per workgroup: as many as balance the CUs' rows (13 x 4096, 10880 channels, 680 tiles of 16: three a workgroup, one
-// workgroup on each of 227 CUs, 17.2 us; with two, 84 CUs have two workgroups, 23.3), and of equals the most.
+// Tiles of 16 channels per workgroup: as few bytes on the fullest CU as can be, a tile's two projections and the tokens once a
+// workgroup, and of equals the most (13 x 4096, 10880 channels, 680 tiles: three a workgroup, one workgroup on each of 227 CUs,
+// 17.0 us; with two, 84 CUs have two workgroups, 23.3; 16 x 4096, 14336: four 23.1, two 25.2; 32 x 4096, 16384: four 28.3, two
+// 32.5).  For up to 16 tokens two, where they fill all CUs alike (1 x 4096, 16384: 24.1, four 25.1).
 hipError_t launch_glu_small(GluParams p, bool e8m0, float* sums, hipStream_t stream) {
-    const int tiles = p.N / 16, cus = device_cu_count();
-    auto cost = [&](int c) { return ((tiles + c - 1) / c + cus - 1) / cus * c; };
-    auto go = [&](auto channels) {
-        constexpr int kC = decltype(channels)::value;
-        auto kernel = e8m0 ? glu_small_kernel<kC, true> : glu_small_kernel<kC, false>;
+    const int tiles = p.N / 16, cus = device_cu_count(), token_tiles = p.T <= 16 ? 1 : 2;
+    auto cost = [&](int c) { return ((tiles + c - 1) / c + cus - 1) / cus * (2 * c + token_tiles); };
+    int most = 1;
+    for (int c = 2; c <= 4; ++c)
+        if (cost(c) <= cost(most)) most = c;
+    if (token_tiles == 1 && tiles % (2 * cus) == 0) most = 2;
+    auto go = [&](auto channels, auto tokens) {
+        constexpr int kC = decltype(channels)::value, kTT = decltype(tokens)::value;
+        auto kernel = e8m0 ? glu_small_kernel<kC, kTT, true> : glu_small_kernel<kC, kTT, false>;
         p.tiles_n = (tiles + kC - 1) / kC;
         kernel<<<static_cast<unsigned>((p.tiles_n + 7) / 8 * 8), kThreads, 0, stream>>>(p, sums);
         return hipGetLastError();
     };
-    if (cost(3) <= std::min(cost(1), cost(2))) return go(std::integral_constant<int, 3>{});
-    if (cost(2) <= cost(1)) return go(std::integral_constant<int, 2>{});
-    return go(std::integral_constant<int, 1>{});
+    auto by_channels = [&](auto tokens) {
+        switch (most) {
+            case 1: return go(std::integral_constant<int, 1>{}, tokens);
+            case 2: return go(std::integral_constant<int, 2>{}, tokens);
+            case 3: return go(std::integral_constant<int, 3>{}, tokens);
+            default: return go(std::integral_constant<int, 4>{}, tokens);
+        }
+    };
+    return token_tiles == 1 ? by_channels(std::integral_constant<int, 1>{}) : by_channels(std::integral_constant<int, 2>{});
 }
 
 }  // namespace rtq

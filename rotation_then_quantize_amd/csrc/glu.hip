@@ -160,14 +160,19 @@ enum Form : int { kSmall, kSums, kTile64, kTile128, kLarge };
 // at once is taken, and where none fits the largest.  The product that leaves its sums in the workspace splits the reduction
 // over idle CUs and costs a launch: it is better where tiles of 64 are few or the reduction is long.
 // Few tokens: as the weights stream (fp8_glu_small.hip), but where workgroups are fewer than CUs and the reduction long (y
-// alone, with codes, and either from sums: 1 x 16384, 1024 channels 19.6, 21.5, 14.0; 1 x 8192, 1152: 11.3, 13.4, 9.7; 4 x 4096,
-// 1152: 7.4, 9.4, 8.4; 4 x 2048, 1152: 5.2, 7.8, 8.3).  Which outputs are asked for does not choose: y is the same bits with the
-// checkpoint and without.
+// alone, with codes, and either from sums: 1 x 16384, 1024 channels 18.7, 20.5, 13.9; 1 x 8192, 1152: 10.8, 12.8, 9.6; 4 x 4096,
+// 1152: 7.1, 9.1, 7.7; 4 x 2048, 1152: 4.9, 7.0, 7.7).  17 to 32 of them so where they are wide and the reduction is not short
+// (y alone, with codes, either from sums, either by tiles of 64: 32 x 2048, 4096: 7.5, 9.8, 12.5, 12.4; 32 x 4096, 4096: 11.0,
+// 12.9, 13.6, 20.9; 32 x 4096, 16384: 28.3, 31.1, 35.6, 37.0; 32 x 4096, 28672: 51.9, 55.3, 65.8, 54.8; but 32 x 2048, 16384:
+// 15.0, 17.6, 16.6, 14.0; 32 x 512, 4096: 4.9, 7.7, 9.3, 6.1; 32 x 4096, 2048: 10.9, 13.1, 11.6, 20.9); with 64 tokens their
+// loads from the caches are as long as the weights' (4096 x 16384 44.8, 47.0, 37.6, 38.2).  Which outputs are asked for does not
+// choose: y is the same bits with the checkpoint and without.
 Form plan(int64_t T, int N, int K) {
     const int64_t cus = device_cu_count();
     const int blocks = static_cast<int>(fp8_groups(K));
     auto tiles = [&](int tokens) { return (T + tokens - 1) / tokens * (N / 128); };
     if (T <= 16) return N / 16 < cus && blocks >= 32 ? kSums : kSmall;
+    if (T <= 32 && N / 16 >= cus && (blocks > 16 || (2 * tiles(64) < cus && blocks > 8))) return kSmall;
     if (tiles(64) <= cus) return blocks <= 12 || 2 * tiles(64) > cus || (2 * tiles(64) == cus && blocks <= 48) ? kTile64 : kSums;
     if (tiles(128) <= cus || blocks == 1) return kTile128;   // (the large form's loads run two blocks ahead)
     return kLarge;

@@ -237,6 +237,14 @@ def test_glu(T, N, K, st):
 
 
 @pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N,K", [(16, 14336, 528), (2, 32896, 272), (17, 4096, 1296), (32, 4096, 2064), (31, 8192, 1040), (20, 10880, 1168),
+                                   (27, 16384, 2064), (32, 33280, 2320)])
+def test_glu_few_tokens(T, N, K, st):
+    """One or two tiles of tokens, one to four of channels a workgroup, the last one's in part."""
+    check_glu(T, N, K, st, "gelu_tanh")
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
 @pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("T,N,K", [(9, 384, 528), (300, 2048, 400), (2100, 4096, 272)])
 def test_glu_activations(T, N, K, st, name):
@@ -304,7 +312,7 @@ def test_glu_large_with_an_odd_scale(T, N, K, odd):
         near(y, want, act_bound(h, "silu") * want.abs() + TINY * (1 + h[:, N:].abs()) + lost)
 
 
-@pytest.mark.parametrize("T,N,K", [(1, 512, 2048), (16, 256, 4096), (100, 384, 1040), (300, 512, 2064), (1100, 4096, 1040)])
+@pytest.mark.parametrize("T,N,K", [(1, 512, 2048), (16, 256, 4096), (30, 4096, 2064), (100, 384, 1040), (300, 512, 2064), (1100, 4096, 1040)])
 def test_glu_general(T, N, K):
     """General fp32 scales and codes over the whole range; equal calls give equal bits."""
     step("glu general", T, N, K)
@@ -327,7 +335,7 @@ def test_glu_general(T, N, K):
     assert rel(hq, h) <= GENERAL + 2.0 ** -4
 
 
-@pytest.mark.parametrize("T,N,K", [(5, 256, 528), (70, 256, 528), (2100, 4096, 272)])
+@pytest.mark.parametrize("T,N,K", [(5, 256, 528), (22, 4096, 1168), (70, 256, 528), (2100, 4096, 272)])
 def test_glu_non_finite(T, N, K):
     """NaN and infinite operands spread along their row or channel only."""
     step("glu non-finite", T, N, K)
@@ -351,7 +359,7 @@ def test_glu_non_finite(T, N, K):
     check_codes(torch.where(finite, cf[rows], torch.zeros_like(cf[rows])), s[:, rows], want, torch.zeros_like(want))
 
 
-@pytest.mark.parametrize("T,N,K", [(5, 256, 144), (16, 128, 1040), (40, 256, 2064), (100, 128, 144), (300, 256, 4112), (2100, 4096, 272)])
+@pytest.mark.parametrize("T,N,K", [(5, 256, 144), (16, 128, 1040), (21, 4096, 1168), (40, 256, 2064), (100, 128, 144), (300, 256, 4112), (2100, 4096, 272)])
 def test_glu_infinite_scale_of_the_last_block(T, N, K):
     """Nothing that fills a block, a stage or a turn meets the infinite scales: the last token's sums stay infinite, the first
     gate block's too."""
