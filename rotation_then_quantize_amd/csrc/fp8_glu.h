@@ -48,16 +48,11 @@ __device__ __forceinline__ void for_act(int act, F f) {
         f(std::integral_constant<int, RTQ_ACT_GELU_TANH>{});
 }
 
-// A group's scale exponent as a byte that orders like it, 0 for a group of zeros: the largest of several parts' bytes
-// is the whole group's.
-__device__ __forceinline__ uint32_t exponent_byte(uint32_t amax) { return amax == 0u ? 0u : static_cast<uint32_t>(scale_exponent<false>(amax) + 121); }
-__device__ __forceinline__ int byte_exponent(uint32_t b) { return b == 0u ? 0 : static_cast<int>(b) - 121; }
-// 2^e of a byte's exponent; for zeros, whose codes do not depend on it, 2^-121.
-__device__ __forceinline__ float byte_scale(uint32_t b) { return __uint_as_float((b + 6u) << 23); }
-// The largest of the four bytes of a word.
-__device__ __forceinline__ uint32_t max_byte(uint32_t w) {
-    return max(max(w & 0xffu, w >> 8 & 0xffu), max(w >> 16 & 0xffu, w >> 24));
-}
+// A group's scale as the bits of a float, which order like it: 2^-121 for a group of zeros, whose codes do not depend on it (it
+// is 1).  The largest of several parts' bits is the whole group's.
+constexpr uint32_t kZeros = 6u << 23;
+__device__ __forceinline__ uint32_t scale_bits(uint32_t amax) { return amax == 0u ? kZeros : static_cast<uint32_t>(scale_exponent<false>(amax) + 127) << 23; }
+__device__ __forceinline__ int bits_exponent(uint32_t b) { return b == kZeros ? 0 : static_cast<int>(b >> 23) - 127; }
 
 // The largest magnitude of m, a and b in one instruction; of numbers that are none, the others'.  (From fmaxf the compiler makes
 // it with an instruction more for each number.)  a and b must not come straight from a matrix instruction, for whose results
@@ -79,33 +74,37 @@ __device__ __forceinline__ uint32_t max_rows(float m0, float m1, float m2, float
 // Codes of four values by 2^e, as encode4 of the values times 2^-e.
 typedef short v2s __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t encode4_by(const float* v, float scale) {
-    v2s w = {0, 0};
+    v2s w = __builtin_bit_cast(v2s, v[0]);   // both halves are written: any register serves, without an instruction for it
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[0], v[1], scale, false);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[2], v[3], scale, true);
     return __builtin_bit_cast(uint32_t, w);
 }
 
 constexpr int kGluStep = 8192, kGluStage = 3 * kGluStep;           // LDS that outputs go through, in three buffers
-constexpr int glu_bytes(int tokens) { return 3 * tokens * 4; }     // exponents [y, g, u][token][wave]
+constexpr int kGluSet = 3 * 64, kGluScales = 2 * kGluSet * 4;      // and the scales of two steps
+
+struct GluLds {
+    uint8_t* stage;     // [kGluStage]
+    uint32_t* scales;   // [2][kGluSet], zeros at first
+    int turn = 0;       // the buffer of the next values
+    int set = 0;        // the scales of the next step
+};
 
 // The outputs of kR row tiles from kI0 on, kR * 16 tokens of a wave: acc[i][j], j < 2, are the sums of 16 channels' gates (lane:
 // token l % 16, channels 4 (l / 16) .. +4), j + 2 those of their partners.  All 8 waves of the workgroup come here: wave (wm,
 // wn) has kWaveRows tokens from kWaveRows wm on of the tile and 32 channels from 32 wn on of its 128, a group; m0 and n0 are the
 // tile's first token and channel.  kKeep: with the checkpoint.
 //
-// Codes take the largest magnitudes of 32 channels each, whose exponents the four waves of a group exchange as bytes (the
-// scale's exponent is monotone in the magnitude), and go through LDS to whole lines of a token's 128.  Two barriers for all
-// kinds of codes; kR is as large as the LDS for them allows (4608 x 4096, 16384 channels with the checkpoint, fp32 scales outside the
-// instruction: 593 us; the three kinds one after the other, of four row tiles, 611, half of the outputs' time then waits for LDS
-// and barriers).
-//
-// stage: kGluStage bytes of LDS, bytes: glu_bytes, turn: the buffer of the next values, kept from call to call.
+// Codes: the four waves of a group join the scales of their 32 channels in LDS (a scale is monotone in the magnitude), and the
+// codes go through LDS to whole lines of a token's 128.  Two barriers for all kinds of codes; kR is as large as the LDS for them
+// allows (4608 x 4096, 16384 channels with the checkpoint, fp32 scales outside the instruction: 593 us; the three kinds one
+// after the other, of four row tiles, 611, half of the outputs' time then waits for LDS and barriers).
 template <int kR, bool kKeep, int kI0, int kWaveRows, bool kE8M0, int TM>
 __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)[TM][4], int64_t m0, int n0, int wm, int wn, int tid,
-                                            uint8_t* stage, uint8_t* bytes, int& turn) {
-    constexpr int kTokens = 2 * kWaveRows, kKinds = kKeep ? 3 : 1, kBuffer = 32 * kR * kFp8Block;
+                                            GluLds& lds) {
+    constexpr int kTokens = 2 * kWaveRows, kKinds = kKeep ? 3 : 1, kStep = 32 * kR, kBuffer = kStep * kFp8Block;
     static_assert(kR == 2 || kR == 4, "row tiles");
-    static_assert(kKinds * kBuffer <= kGluStage, "a buffer for each kind of codes");
+    static_assert(kKinds * kBuffer <= kGluStage && kKinds * kStep <= kGluSet, "a buffer and scales for each kind of codes");
     const int lane = tid & 63, g = lane >> 4, l15 = lane & 15;
     const GluOut& o = p.out;
     const int rows = static_cast<int>(min<int64_t>(kTokens, p.T - m0));   // of the tile: what a lane adds to its first is below 2^32
@@ -125,8 +124,8 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
     });
     __builtin_amdgcn_sched_barrier(0);   // all sums have been read here, as magnitude() wants it
     // Values.  A step's rows in LDS: those of wave-row 0, then of 1; chunk c (16 bytes) of row r is at c ^ (r & 7).
-    auto buffer = [&]() { return stage + turn * kGluStep; };
-    auto next = [&]() { turn = turn == 2 ? 0 : turn + 1; };
+    auto buffer = [&]() { return lds.stage + lds.turn * kGluStep; };
+    auto next = [&]() { lds.turn = lds.turn == 2 ? 0 : lds.turn + 1; };
     auto handed = [&]() {   // what the waves wrote is in LDS, for every wave
         lds_done();
         barrier();
@@ -168,8 +167,12 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
     }
     const bool codes = o.y_codes != nullptr;
     if (!codes && !kKeep) return;
-    // Exponents of this wave's 32 channels, of four parts (a kind's row tile) at a time: lane row k has part k's.
+    // Scales of this wave's 32 channels, of four parts (a kind's row tile) at a time: lane row k has part k's.  Words: [kind][token of
+    // the step].
     const int row0 = kWaveRows * wm + kI0 * 16 + l15;
+    uint32_t* scales = lds.scales + lds.set * kGluSet;
+    lds.set ^= 1;
+    const int word0 = 16 * kR * wm + l15;
     auto largest = [&](const float* x) {
         float m = 0.f;
 #pragma unroll
@@ -182,38 +185,36 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
         for (int e = 0; e < 8; ++e) m = __builtin_fabsf(x[e]) < __builtin_inff() ? max(m, __builtin_fabsf(x[e])) : m;
         return m;
     };
-    auto put_bytes = [&](const float* x0, const float* x1, const float* x2, const float* x3, int kind, bool some) {
+    auto put_scales = [&](const float* x0, const float* x1, const float* x2, const float* x3, int kind, bool some) {
         float m0 = largest(x0), m1 = largest(x1), m2 = largest(x2), m3 = largest(x3);
         if (max(max(m0, m1), max(m2, m3)) == __builtin_inff()) m0 = finite(x0), m1 = finite(x1), m2 = finite(x2), m3 = finite(x3);
         const uint32_t mine = max_rows(m0, m1, m2, m3);
-        if (some) bytes[((kind + g / kR) * kTokens + row0 + 16 * (g % kR)) * 4 + wn] = static_cast<uint8_t>(exponent_byte(mine));
+        if (some) __hip_atomic_fetch_max(scales + (kind + g / kR) * kStep + word0 + 16 * (g % kR), scale_bits(mine), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     };
-    if (codes) put_bytes(v[0][0], v[0][1], v[0][kR - 2], v[0][kR - 1], 0, g < kR);
-    if constexpr (kKeep) put_bytes(v[1][0], v[1][1], v[2][0], v[2][1], 1, true);
+    if (codes) put_scales(v[0][0], v[0][1], v[0][kR - 2], v[0][kR - 1], 0, g < kR);
+    if constexpr (kKeep) put_scales(v[1][0], v[1][1], v[2][0], v[2][1], 1, true);
     handed();
-    // Codes: a buffer for each kind, 32 kR rows of 128 bytes.  All exponents are read first: behind a write to LDS the compiler
+    // Codes: a buffer for each kind, 32 kR rows of 128 bytes.  All scales are read first: behind a write to LDS the compiler
     // would hold the next read back until it has been done.
     uint32_t top[kKinds][kR];
 #pragma unroll
     for (int kind = 0; kind < kKinds; ++kind)
 #pragma unroll
-        for (int i = 0; i < kR; ++i) top[kind][i] = reinterpret_cast<const uint32_t*>(bytes)[kind * kTokens + row0 + 16 * i];
-    uint8_t* mine = stage + (16 * kR * wm + l15) * 128 + 4 * g;
+        for (int i = 0; i < kR; ++i) top[kind][i] = scales[kind * kStep + word0 + 16 * i];
+    uint8_t* mine = lds.stage + word0 * 128 + 4 * g;
     const int place[2] = {(2 * wn ^ (l15 & 7)) << 4, ((2 * wn + 1) ^ (l15 & 7)) << 4};
     auto put_codes = [&](auto kindc, void* scale, int group) {
         constexpr int kind = decltype(kindc)::value;
         uint32_t of_mine = 0u;   // lane row i's
 #pragma unroll
         for (int i = 0; i < kR; ++i) {
-            const uint32_t b = max_byte(top[kind][i]);
-            const float by = byte_scale(b);
-            of_mine = g == i ? b : of_mine;
+            of_mine = g == i ? top[kind][i] : of_mine;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<uint32_t*>(mine + kind * kBuffer + 16 * i * 128 + place[j]) = encode4_by(v[kind][i] + 4 * j, by);
+                *reinterpret_cast<uint32_t*>(mine + kind * kBuffer + 16 * i * 128 + place[j]) = encode4_by(v[kind][i] + 4 * j, __uint_as_float(top[kind][i]));
         }
         if (wn == kind && g < kR && row0 + 16 * g < rows)
-            store_scale(scale, kE8M0, group * p.T + m0 + row0 + 16 * g, byte_exponent(of_mine));
+            store_scale(scale, kE8M0, group * p.T + m0 + row0 + 16 * g, bits_exponent(of_mine));
     };
     if (codes) put_codes(std::integral_constant<int, 0>{}, o.y_scale, n0 / kFp8Block);
     if constexpr (kKeep) {
@@ -221,10 +222,11 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
         put_codes(std::integral_constant<int, kKinds - 1>{}, o.h_scale, (p.N + n0) / kFp8Block);
     }
     handed();
+    if (tid < kKinds * kStep) scales[tid] = 0u;   // for the step after the next one, two barriers from here
 #pragma unroll
     for (int q = 0; q < kR / 2; ++q) {
         const int r = 64 * q + (tid >> 3), c = tid & 7, line = r / (16 * kR) * kWaveRows + kI0 * 16 + r % (16 * kR);   // of the tile
-        const uint8_t* at = stage + r * 128 + ((c ^ (r & 7)) << 4);
+        const uint8_t* at = lds.stage + r * 128 + ((c ^ (r & 7)) << 4);
         v4i x[kKinds];
 #pragma unroll
         for (int kind = 0; kind < kKinds; ++kind) x[kind] = *reinterpret_cast<const v4i*>(at + kind * kBuffer);
@@ -247,17 +249,17 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
 // All outputs of a tile.
 template <int kWaveRows, bool kE8M0, int TM>
 __device__ __forceinline__ void glu_tile_outputs(const GluParams& p, const v4f (&acc)[TM][4], int64_t m0, int n0, int wm, int wn, int tid,
-                                                 uint8_t* stage, uint8_t* bytes, int& turn) {
+                                                 GluLds& lds) {
     if (p.out.h_codes != nullptr) {
-        glu_outputs<2, true, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
-        if constexpr (TM >= 4) glu_outputs<2, true, 2, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
+        glu_outputs<2, true, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
+        if constexpr (TM >= 4) glu_outputs<2, true, 2, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
         if constexpr (TM == 8) {
-            glu_outputs<2, true, 4, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
-            glu_outputs<2, true, 6, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
+            glu_outputs<2, true, 4, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
+            glu_outputs<2, true, 6, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
         }
     } else {
-        glu_outputs<TM == 2 ? 2 : 4, false, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
-        if constexpr (TM == 8) glu_outputs<4, false, 4, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, stage, bytes, turn);
+        glu_outputs<TM == 2 ? 2 : 4, false, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
+        if constexpr (TM == 8) glu_outputs<4, false, 4, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
     }
 }
 

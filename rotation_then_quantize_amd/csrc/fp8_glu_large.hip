@@ -38,8 +38,7 @@ constexpr int kWavesM = 2, kWavesN = 4, kWaves = kWavesM * kWavesN, kThreads = 6
 constexpr int kRing = 2 * (kTileM + BN) * BK;
 constexpr int kSlotScales = kTileM + 2 * 64;                                       // tokens', then 64 copies of the two weights'
 constexpr int kScaleBytes = 2 * kSlotScales * static_cast<int>(sizeof(float));
-constexpr int kBytes = glu_bytes(kTileM);
-constexpr int kLds = kRing + kScaleBytes + kGluStage + kBytes;
+constexpr int kLds = kRing + kScaleBytes + kGluStage + kGluScales;
 
 // Tile index within the XCD-ordered sequence -> (tile_m, tile_n), in bands of 8 N-tiles.
 __device__ __forceinline__ void tile_of(int lin, int tiles_m, int tiles_n, int* tm, int* tn) {
@@ -262,6 +261,8 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         }
     };
 
+    GluLds out_lds{lds + kRing + kScaleBytes, reinterpret_cast<uint32_t*>(lds + kRing + kScaleBytes + kGluStage)};
+    if (tid < 2 * kGluSet) out_lds.scales[tid] = 0u;
     set_cursor(first);
     issue(0);
     wait_vmcnt<0>();
@@ -274,7 +275,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     fa[0] = read_a(0, 0);
     fa[1] = read_a(0, 1);
     if constexpr (kInside) read_scales(0);
-    int slot = 0, turn = 0;
+    int slot = 0;
     for (int lin = first; lin < end; lin += stride) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
@@ -298,8 +299,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         int64_t m0;
         int n0;
         place(lin, &m0, &n0);
-        uint8_t* stg = lds + kRing + kScaleBytes;
-        glu_tile_outputs<WM, kE8M0>(p, acc, m0, n0, wm, wn, again(tid), stg, stg + kGluStage, turn);
+        glu_tile_outputs<WM, kE8M0>(p, acc, m0, n0, wm, wn, again(tid), out_lds);
     }
     wait_vmcnt<0>();   // nothing is still writing LDS when the workgroup's next tiles, or another workgroup, use it
 }

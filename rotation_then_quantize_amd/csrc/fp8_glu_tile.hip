@@ -27,7 +27,7 @@ constexpr int kWavesM = 2, kWavesN = 4, kWaves = kWavesM * kWavesN, kThreads = 6
 constexpr int kTable = 16;   // blocks whose scales are in LDS (an even number)
 
 template <int BM>
-constexpr int tile_lds() { return kSlots * (BM + BN) * BK + kTable * (BM + 2) * static_cast<int>(sizeof(float)); }
+constexpr int tile_lds() { return kSlots * (BM + BN) * BK + kTable * (BM + 2) * static_cast<int>(sizeof(float)) + kGluScales; }
 
 template <int BM, bool kE8M0>
 __global__ void __launch_bounds__(kThreads)
@@ -35,11 +35,12 @@ glu_tile_kernel(GluParams p) {
     constexpr int WM = BM / kWavesM, TM = WM / 16, TN = 4;
     constexpr int kABytes = BM * BK, kStage = kABytes + BN * BK;
     constexpr int kALoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves, kLoads = kALoads + kWLoads;   // 1 KB loads per wave
-    static_assert(kGluStage + glu_bytes(BM) <= kSlots * kStage, "the outputs' LDS");
+    static_assert(kGluStage <= kSlots * kStage, "the outputs' LDS");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
     float* table = reinterpret_cast<float*>(lds + kSlots * kStage);   // [block][token], then [block][gate, partner]
     float* w_table = table + kTable * BM;
+    GluLds out_lds{lds, reinterpret_cast<uint32_t*>(w_table + 2 * kTable)};
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -140,6 +141,7 @@ glu_tile_kernel(GluParams p) {
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) issue(s, s);
     fill(0);
+    if (tid < 2 * kGluSet) out_lds.scales[tid] = 0u;
     wait_vmcnt<(kSlots - 1) * kLoads>();
     lds_done();
     barrier();
@@ -168,8 +170,7 @@ glu_tile_kernel(GluParams p) {
     wait_vmcnt<0>();   // nothing is still writing the LDS that the outputs go through ...
     lds_done();
     barrier();         // ... nor reading it, in any wave
-    int turn = 0;
-    glu_tile_outputs<WM, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds, lds + kGluStage, turn);
+    glu_tile_outputs<WM, kE8M0>(p, acc, m0, n0, wm, wn, tid, out_lds);
 }
 
 template <int BM>
