@@ -103,7 +103,7 @@ template <int kR, bool kKeep, int kI0, int kWaveRows, bool kE8M0, int TM>
 __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)[TM][4], int64_t m0, int n0, int wm, int wn, int tid,
                                             GluLds& lds) {
     constexpr int kTokens = 2 * kWaveRows, kKinds = kKeep ? 3 : 1, kStep = 32 * kR, kBuffer = kStep * kFp8Block;
-    static_assert(kR == 2 || kR == 4, "row tiles");
+    static_assert(kR == 1 || kR == 2 || kR == 4, "row tiles");
     static_assert(kKinds * kBuffer <= kGluStage && kKinds * kStep <= kGluSet, "a buffer and scales for each kind of codes");
     const int lane = tid & 63, g = lane >> 4, l15 = lane & 15;
     const GluOut& o = p.out;
@@ -191,8 +191,12 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
         const uint32_t mine = max_rows(m0, m1, m2, m3);
         if (some) __hip_atomic_fetch_max(scales + (kind + g / kR) * kStep + word0 + 16 * (g % kR), scale_bits(mine), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     };
-    if (codes) put_scales(v[0][0], v[0][1], v[0][kR - 2], v[0][kR - 1], 0, g < kR);
-    if constexpr (kKeep) put_scales(v[1][0], v[1][1], v[2][0], v[2][1], 1, true);
+    if constexpr (kR == 1) {
+        put_scales(v[0][0], v[kKeep ? 1 : 0][0], v[kKinds - 1][0], v[0][0], 0, g < kKinds && (g > 0 || codes));
+    } else {
+        if (codes) put_scales(v[0][0], v[0][1], v[0][kR - 2], v[0][kR - 1], 0, g < kR);
+        if constexpr (kKeep) put_scales(v[1][0], v[1][1], v[2][0], v[2][1], 1, true);
+    }
     handed();
     // Codes: a buffer for each kind, 32 kR rows of 128 bytes.  All scales are read first: behind a write to LDS the compiler
     // would hold the next read back until it has been done.
@@ -224,7 +228,7 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
     handed();
     if (tid < kKinds * kStep) scales[tid] = 0u;   // for the step after the next one, two barriers from here
 #pragma unroll
-    for (int q = 0; q < kR / 2; ++q) {
+    for (int q = 0; q < (kR + 1) / 2; ++q) {
         const int r = 64 * q + (tid >> 3), c = tid & 7, line = r / (16 * kR) * kWaveRows + kI0 * 16 + r % (16 * kR);   // of the tile
         const uint8_t* at = lds.stage + r * 128 + ((c ^ (r & 7)) << 4);
         v4i x[kKinds];
@@ -232,7 +236,7 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
         for (int kind = 0; kind < kKinds; ++kind) x[kind] = *reinterpret_cast<const v4i*>(at + kind * kBuffer);
         // a tile's lines are at most 2^28 bytes apart
         const uint32_t far = static_cast<uint32_t>(line) * static_cast<uint32_t>(p.N) + static_cast<uint32_t>(16 * c);
-        if (line < rows) {
+        if (line < rows && (kR > 1 || r < kStep)) {
             if (codes) *reinterpret_cast<v4i*>(static_cast<uint8_t*>(o.y_codes) + m0 * p.N + n0 + far) = x[0];
             if constexpr (kKeep) {
                 uint8_t* out = static_cast<uint8_t*>(o.h_codes) + m0 * 2 * p.N + n0;
@@ -252,7 +256,12 @@ __device__ __forceinline__ void glu_outputs(const GluParams& p, const v4f (&acc)
 template <int kWaveRows, bool kE8M0, int TM>
 __device__ __forceinline__ void glu_tile_outputs(const GluParams& p, const v4f (&acc)[TM][4], int64_t m0, int n0, int wm, int wn, int tid,
                                                  GluLds& lds) {
-    if (p.out.h_codes != nullptr) {
+    if constexpr (TM == 1) {
+        if (p.out.h_codes != nullptr)
+            glu_outputs<1, true, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
+        else
+            glu_outputs<1, false, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
+    } else if (p.out.h_codes != nullptr) {
         glu_outputs<2, true, 0, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
         if constexpr (TM >= 4) glu_outputs<2, true, 2, kWaveRows, kE8M0>(p, acc, m0, n0, wm, wn, tid, lds);
         if constexpr (TM == 8) {
@@ -272,7 +281,7 @@ fp8::GluParams glu_params(const GluArgs& a);
 hipError_t launch_glu_large(const fp8::GluParams& p, bool e8m0, hipStream_t stream);
 // At most 32 tokens.  sums: [T][2 N] fp32 receives [g u], or nullptr: y is written.
 hipError_t launch_glu_small(fp8::GluParams p, bool e8m0, float* sums, hipStream_t stream);
-// `tokens` (64 or 128) by 128 channels per workgroup.
+// `tokens` (32, 64 or 128) by 128 channels per workgroup.
 hipError_t launch_glu_tile(const fp8::GluParams& p, bool e8m0, int tokens, hipStream_t stream);
 
 }  // namespace rtq

@@ -1,4 +1,4 @@
-// fp8_glu_tile.hip -- the gated feed-forward's product for outputs of few tiles: 64 or 128 tokens by 128 channels per
+// fp8_glu_tile.hip -- the gated feed-forward's product for outputs of few tiles: 32, 64 or 128 tokens by 128 channels per
 // workgroup.
 //
 // 8 waves in 2 x 4, each BM / 2 tokens by 32 channels and their partners, laid as in the large kernel.  A ring of three LDS
@@ -6,10 +6,11 @@
 // it is multiplied.  The tokens' and the two weights' scales, of kTable blocks at a time, are put into LDS beforehand.  The
 // outputs' staging takes the ring's place.
 //
-// Bound by LDS: a stage of 64 tokens writes 40 KB and reads 96, in 0.55-0.6 us.  Four waves with larger tiles, which read 64
-// KB, have twice the loads each to issue and took 0.95 us.  Weights straight into registers, where no other wave needs them (8
-// waves of 16 channels each), took 1 us: the instruction's operand is 16 rows, so that a load touches half of 16 lines of 128
-// bytes, and each line is touched twice.
+// Bound by LDS: a stage of 64 tokens writes 40 KB and reads 96, in 0.55-0.6 us, one of 32 writes 36 and reads 80, in 0.5.  Four
+// waves with larger tiles, which read 64 KB for 64 tokens, have twice the loads each to issue and took 0.95 us.  Weights straight
+// into registers, where no other wave needs them (8 waves of 16 channels each), took 1 us: the instruction's operand is 16 rows,
+// so that a load touches half of 16 lines of 128 bytes, and each line is touched twice.  bf16 products of the decoded codes
+// (fp8_glu_small.hip) take 1.3 to 1.7 times the time here.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -34,7 +35,8 @@ __global__ void __launch_bounds__(kThreads)
 glu_tile_kernel(GluParams p) {
     constexpr int WM = BM / kWavesM, TM = WM / 16, TN = 4;
     constexpr int kABytes = BM * BK, kStage = kABytes + BN * BK;
-    constexpr int kALoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves, kLoads = kALoads + kWLoads;   // 1 KB loads per wave
+    constexpr int kALoads = BM < 64 ? 1 : BM / 8 / kWaves, kWLoads = BN / 8 / kWaves, kLoads = kALoads + kWLoads;   // 1 KB loads per wave
+    constexpr int kARows = BM < 64 ? BM / kWaves : 8;   // of a load: 32 tokens are half a load each
     static_assert(kGluStage <= kSlots * kStage, "the outputs' LDS");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
@@ -63,14 +65,20 @@ glu_tile_kernel(GluParams p) {
     // LDS rows of 128 bytes, chunk c (16 bytes) of row r at chunk c ^ ((r >> 1) & 7); LDS weight row 64 q + 16 j + l is
     // channel 32 q + 16 (j % 2) + l of the gate (j < 2) or of its partner.
     const int kcol = ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) << 4;
-    const uint32_t a_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * p.K + kcol);
+    const int a_row = kARows * wave + (lane >> 3), a_kcol = ((lane & 7) ^ ((a_row >> 1) & 7)) << 4;
+    const uint32_t a_off = static_cast<uint32_t>(a_row * p.K + a_kcol);
     const uint32_t w_off = static_cast<uint32_t>((8 * (wave % (kWaves / 2)) + (lane >> 3)) * p.K + kcol);
     const uint32_t a_step = static_cast<uint32_t>(8 * kWaves * p.K), w_step = a_step / 2;
     auto issue = [&](int kb, int slot) {
         const uint32_t base = lds_base + static_cast<uint32_t>(slot * kStage + wave * 1024);
-        const uint32_t k0 = kb * BK + kcol < p.K ? static_cast<uint32_t>(kb * BK) : kOob;   // zeros past the row's end
+        auto from = [&](int col) { return kb * BK + col < p.K ? static_cast<uint32_t>(kb * BK) : kOob; };   // zeros past the row's end
+        const uint32_t k0 = from(kcol);
+        if constexpr (kARows < 8) {
+            if (lane < 8 * kARows) load_to_lds(rsa, a_off + from(a_kcol), base - wave * 1024 + wave * kARows * BK);
+        } else {
 #pragma unroll
-        for (int q = 0; q < kALoads; ++q) load_to_lds(rsa, a_off + q * a_step + k0, base + q * kWaves * 1024);
+            for (int q = 0; q < kALoads; ++q) load_to_lds(rsa, a_off + q * a_step + k0, base + q * kWaves * 1024);
+        }
 #pragma unroll
         for (int q = 0; q < kWLoads; ++q) load_to_lds(rsw, w_off + q * w_step + k0, base + kABytes + q * kWaves * 1024);
     };
@@ -189,7 +197,7 @@ hipError_t launch(GluParams p, bool e8m0, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_glu_tile(const GluParams& p, bool e8m0, int tokens, hipStream_t stream) {
-    return tokens == 64 ? launch<64>(p, e8m0, stream) : launch<128>(p, e8m0, stream);
+    return tokens == 32 ? launch<32>(p, e8m0, stream) : tokens == 64 ? launch<64>(p, e8m0, stream) : launch<128>(p, e8m0, stream);
 }
 
 }  // namespace rtq

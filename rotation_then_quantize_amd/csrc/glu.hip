@@ -141,24 +141,30 @@ hipError_t launch_small(const GluArgs& a, hipStream_t stream) {
 }
 
 // How a product runs.
-enum Form : int { kSmall, kSums, kTile64, kTile128, kLarge };
-// Measured with codes (us; T x K, N channels):
-//                        sums    64     128    256 tokens a tile
-//   64 x 512, 1152        8.9    6.3    8.3    9.2
-//   64 x 1024, 4096      10.8    8.2   11.4   12.9
-//   391 x 1936, 1152     13.9   16.0   21.3   24.1
-//   100 x 4096, 1152     12.4   21.1   32.0   35.0
-//   64 x 4096, 4096      14.1   21.5   31.7   34.6
-//   25 x 2048, 16384     16.4   14.2   19.1   20.7
-//   256 x 4096, 4096     20.6   21.4   32.4   35.4
-//   512 x 4096, 4096     28.8   22.4   32.8   35.5
-//   1024 x 4096, 4096    46.1   43.7   35.1   37.2
-//   2048 x 4096, 4096    79.6   88.2   70.1   60.4
-//   128 x 8192, 8192     51.8   57.0   71.4   79.3
-//   256 x 16384, 4096    82.0   97.7  130     156
-// A tile costs its chain of blocks (0.6, 0.95 and 1.05 us each) as long as each CU has one, so the smallest whose workgroups fit
-// at once is taken, and where none fits the largest.  The product that leaves its sums in the workspace splits the reduction
-// over idle CUs and costs a launch: it is better where tiles of 64 are few or the reduction is long.
+enum Form : int { kSmall, kSums, kTile32, kTile64, kTile128, kLarge };
+// Measured with codes (us; T x K, N channels; powers of two as scales):
+//                        sums    32     64     128    256 tokens a tile
+//   64 x 512, 1152        8.7    5.6    6.3    8.3    9.2
+//   64 x 1024, 4096      10.8    7.4    8.3   11.4   12.9
+//   391 x 1936, 1152     13.9   14.4   16.0   21.3   24.1
+//   391 x 2048, 1152     13.5   11.3   12.8
+//   100 x 2048, 4096     13.2   11.2   12.7
+//   300 x 2560, 1152     14.4   14.1   16.6
+//   506 x 3136, 768      16.3   17.5   20.5
+//   64 x 4096, 4096      14.1   18.7   21.5   31.7   34.6
+//   64 x 4096, 10880     26.6   23.9   26.9
+//   64 x 4096, 16384     37.7   36.1   38.5
+//   256 x 4096, 4096     22.2   20.0   21.4   32.4   35.4
+//   512 x 4096, 4096     28.8          22.8   32.8   36.1
+//   1024 x 4096, 4096    46.1          45.2   36.5   39.2
+//   2048 x 4096, 4096    79.6          92.1   72.3   59.2
+//   48 x 8192, 8192      37.5   52.0   56.9
+//   128 x 8192, 8192     52.7   52.0   57.4   71.4   79.3
+//   256 x 16384, 4096    84.7   86.1   98.1  130     156
+// A tile costs its chain of blocks (0.5, 0.6, 0.95 and 1.2 us each) as long as each CU has one, so the smallest whose workgroups
+// fit at once is taken, and where none fits the largest.  The product that leaves its sums in the workspace splits the reduction
+// over idle CUs and costs a launch: it is better where the reduction is long (rows that begin inside a line of 128 bytes are
+// slower to load, and more so in tiles), with tiles for more than half of the CUs where it is very long.
 // Few tokens: as the weights stream (fp8_glu_small.hip), but where workgroups are fewer than CUs and the reduction long (y
 // alone, with codes, and either from sums: 1 x 16384, 1024 channels 18.7, 20.5, 13.9; 1 x 8192, 1152: 10.8, 12.8, 9.6; 4 x 4096,
 // 1152: 7.1, 9.1, 7.7; 4 x 2048, 1152: 4.9, 7.0, 7.7).  17 to 32 of them so where they are wide and the reduction is not short
@@ -173,7 +179,8 @@ Form plan(int64_t T, int N, int K) {
     auto tiles = [&](int tokens) { return (T + tokens - 1) / tokens * (N / 128); };
     if (T <= 16) return N / 16 < cus && blocks >= 32 ? kSums : kSmall;
     if (T <= 32 && N / 16 >= cus && (blocks > 16 || (2 * tiles(64) < cus && blocks > 8))) return kSmall;
-    if (tiles(64) <= cus) return blocks <= 12 || 2 * tiles(64) > cus || (2 * tiles(64) == cus && blocks <= 48) ? kTile64 : kSums;
+    if (tiles(32) <= cus) return blocks <= (K % kFp8Block == 0 ? 20 : 14) || (2 * tiles(32) > cus && blocks <= 48) ? kTile32 : kSums;
+    if (tiles(64) <= cus) return kTile64;
     if (tiles(128) <= cus || blocks == 1) return kTile128;   // (the large form's loads run two blocks ahead)
     return kLarge;
 }
@@ -270,6 +277,7 @@ size_t fp8_glu_workspace_bytes(int64_t T, int N, int K) {
 hipError_t launch_fp8_glu(const GluArgs& a, hipStream_t stream) {
     switch (plan(a.T, a.N, a.K)) {
         case kSmall: return launch_small(a, stream);
+        case kTile32: return launch_glu_tile(glu_params(a), a.e8m0, 32, stream);
         case kTile64: return launch_glu_tile(glu_params(a), a.e8m0, 64, stream);
         case kTile128: return launch_glu_tile(glu_params(a), a.e8m0, 128, stream);
         case kLarge: return launch_glu_large(glu_params(a), a.e8m0, stream);

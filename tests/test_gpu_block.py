@@ -245,6 +245,14 @@ def test_glu_few_tokens(T, N, K, st):
 
 
 @pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N,K", [(33, 128, 16), (63, 1152, 1680), (391, 1152, 2048), (230, 4096, 1024), (64, 10880, 2192), (520, 2048, 144),
+                                   (450, 2304, 528), (1000, 2048, 400)])
+def test_glu_few_tiles(T, N, K, st):
+    """Tiles of 32, 64 and 128 tokens, the last one's in part."""
+    check_glu(T, N, K, st, "silu")
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
 @pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("T,N,K", [(9, 384, 528), (300, 2048, 400), (2100, 4096, 272)])
 def test_glu_activations(T, N, K, st, name):
