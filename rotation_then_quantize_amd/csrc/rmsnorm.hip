@@ -260,10 +260,15 @@ struct RmsBackwardParams {
     float* part;             // [workgroups][d] sums of dgamma, or nullptr
 };
 
-// One row's dh of a chunk.
-__device__ __forceinline__ void row_gradient(float* dr, const float* a, const float* h, float rho, float k) {
+// A chunk of a row: dr becomes dh = dr + rho (a - h k), a = gamma dn, k = rho^2 mean(a h), and sum, dgamma's, takes dn (h rho).
+// Rows far from 1 keep their bits: k is about as large as dh itself and h rho about 1, where rho^3 mean(a h) and dn rho would
+// leave fp32's range with h rho^3 mean(a h) and dn h rho still ordinary numbers.
+__device__ __forceinline__ void row_gradient(float* dr, float* sum, const float* dn, const float* gamma, const float* h, float rho, float k) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dr[i] = __builtin_fmaf(-h[i], k, __builtin_fmaf(rho, a[i], dr[i]));
+    for (int i = 0; i < 8; ++i) {
+        sum[i] = __builtin_fmaf(dn[i], h[i] * rho, sum[i]);
+        dr[i] = __builtin_fmaf(rho, __builtin_fmaf(-h[i], k, dn[i] * gamma[i]), dr[i]);
+    }
 }
 
 constexpr int backward_waves(int team) { return team < 8 ? 8 : team; }
@@ -336,7 +341,7 @@ rmsnorm_backward_kernel(RmsBackwardParams p) {
         team_sum<kTeam, 2>(s, slots[turn] + team * 2 * kTeam, mine);
         turn ^= 1;
         const double r64 = rsqrt64(__builtin_fma(s[0], p.inv_d, p.eps));
-        const float rho = static_cast<float>(r64), k = static_cast<float>(r64 * r64 * r64 * s[1] * p.inv_d);
+        const float rho = static_cast<float>(r64), k = static_cast<float>(r64 * r64 * (s[1] * p.inv_d));
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             float h[8], a[8], w[8], v[8];
@@ -344,12 +349,7 @@ rmsnorm_backward_kernel(RmsBackwardParams p) {
             now.dn[i].get(a);
             now.dr[i].get(v);
             g[i].get(w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                acc[i][e] = __builtin_fmaf(a[e] * rho, h[e], acc[i][e]);
-                a[e] *= w[e];
-            }
-            row_gradient(v, a, h, rho, k);
+            row_gradient(v, acc[i], a, w, h, rho, k);
             if (row < p.rows && c[i] < p.d) stream8<kH16>(p.dh, row * p.d + c[i], v);
         }
     }
@@ -417,27 +417,21 @@ rmsnorm_backward_long_kernel(RmsBackwardParams p) {
         team_sum<kMostTeam, 2>(s, slots[turn], static_cast<int>(threadIdx.x >> 6));
         turn ^= 1;
         const double r64 = rsqrt64(__builtin_fma(s[0], p.inv_d, p.eps));
-        const float rho = static_cast<float>(r64), k = static_cast<float>(r64 * r64 * r64 * s[1] * p.inv_d);
+        const float rho = static_cast<float>(r64), k = static_cast<float>(r64 * r64 * (s[1] * p.inv_d));
         for (int c = c0; c < p.d; c += kStep) {
             load(c);
             Row8<kH16> o;
             o.zero();
             if (p.dresidual != nullptr) o.load(p.dresidual, row * p.d + c);
             o.get(v);
-            if (p.part != nullptr) {
-                Row8<false> old;
-                float sum[8];
-                old.zero();
-                const int64_t at = static_cast<int64_t>(blockIdx.x) * p.d + c;
-                if (row != blockIdx.x) old.load(p.part, at);
-                old.get(sum);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(a[e] * rho, h[e], sum[e]);
-                store8<false>(p.part, at, sum);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) a[e] *= w[e];
-            row_gradient(v, a, h, rho, k);
+            Row8<false> old;
+            float sum[8];
+            old.zero();
+            const int64_t at = static_cast<int64_t>(blockIdx.x) * p.d + c;
+            if (p.part != nullptr && row != blockIdx.x) old.load(p.part, at);
+            old.get(sum);
+            row_gradient(v, sum, a, w, h, rho, k);
+            if (p.part != nullptr) store8<false>(p.part, at, sum);
             store8<kH16>(p.dh, row * p.d + c, v);
         }
     }
