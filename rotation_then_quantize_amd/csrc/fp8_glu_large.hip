@@ -8,12 +8,12 @@
 //   - The 256 weight rows of a stage are 128 of the gate and the same 128 channels' of the other projection, laid so that
 //     a wave's column tiles 0 and 1 are 32 channels' gates and 2 and 3 their partners: g and u of a channel and token meet
 //     in one lane.
-//   - A wave needs two weight scales a stage.  Inside the instruction (E8M0, and fp32 where all scales of a workgroup's tiles
-//     are powers of two, as the quantiser makes them): four rows' bytes a register, the two weights' bytes in one, chosen by
-//     the instruction.  Any other fp32 scales: the row's scale and the two factors are read apart and multiplied when used
-//     (two multiplies a row tile; tables of both products would take eight more registers, and there are none).  Looking
-//     through the scales takes 2 us (1 where a weight's is none), the additions in fp32 that it saves a tenth of the time (4608 x 4096, 16384 channels, to
-//     codes: 502 us inside, 554 outside; with the checkpoint 538 and 588).
+//   - A wave needs two weight scales a stage.  E8M0, applied inside the instruction: four rows' bytes a register, the two weights'
+//     bytes in one, chosen by the instruction.  fp32, applied outside: the row's scale and the two factors are read apart
+//     and multiplied when used (two multiplies a row tile; tables of both products would take eight more registers, and
+//     there are none).  4608 x 4096, 16384 channels: to codes 506 us with E8M0 scales, 562 with fp32; with the checkpoint 533
+//     and 593.  fp32 scales that happen to be powers of two stay outside all the same: the instruction cuts up to 2^-20 of the
+//     running sum off with each block that it adds, and an output's bits would go by its neighbours' scales.
 //   - The outputs (glu_outputs), two or four row tiles at a time: f(g) u fits beside the sums, and the LDS that is left holds
 //     their codes.
 //
@@ -65,8 +65,8 @@ struct LargeParams {
     int full;      // tiles [0, full) are taken whole; the rest as two halves of their tokens
 };
 
-// Tiles of BM tokens: kTileM, or half of that.  kInside: the instruction applies the scales.
-template <int BM, bool kInside, bool kE8M0>
+// Tiles of BM tokens: kTileM, or half of that.
+template <int BM, bool kE8M0>
 __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds, int first, int end, int stride) {
     constexpr int WM = BM / kWavesM, TM = WM / 16, TN = 4;
     constexpr int kABytes = BM * BK, kStage = kABytes + BN * BK;
@@ -75,7 +75,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     static_assert(TM == 4 || TM == 8, "row tiles");
     const GluParams& p = lp.g;
     const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
-    using Scale = std::conditional_t<kInside, uint8_t, float>;
+    using Scale = std::conditional_t<kE8M0, uint8_t, float>;
     Scale* s_scale = reinterpret_cast<Scale*>(lds + kRing);               // [slot][kSlotScales]
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -133,9 +133,9 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         r_w = load_raw<kE8M0>(sw, 0);
     };
     auto write_scales = [&](int slot) {
-        if constexpr (kInside) {
-            s_scale[slot * kSlotScales + s_at] = static_cast<uint8_t>(kE8M0 ? r_a : r_a >> 23);
-            s_scale[slot * kSlotScales + s_wat] = static_cast<uint8_t>(kE8M0 ? r_w : r_w >> 23);
+        if constexpr (kE8M0) {
+            s_scale[slot * kSlotScales + s_at] = static_cast<uint8_t>(r_a);
+            s_scale[slot * kSlotScales + s_wat] = static_cast<uint8_t>(r_w);
         } else {
             s_scale[slot * kSlotScales + s_at] = __uint_as_float(r_a);
             s_scale[slot * kSlotScales + s_wat] = __uint_as_float(r_w);
@@ -172,7 +172,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     uint32_t eb[TM / 4], eb_next[TM / 4], ew = 0u, ew_next = 0u;
     auto read_scales = [&](int slot) {
         const Scale* q = s_scale + slot * kSlotScales;
-        if constexpr (kInside) {
+        if constexpr (kE8M0) {
 #pragma unroll
             for (int i = 0; i < TM / 4; ++i) eb_next[i] = reinterpret_cast<const uint32_t*>(q + (wm * 16 + l15) * TM)[i];
             ew_next = *reinterpret_cast<const uint16_t*>(q + kTileM);
@@ -193,7 +193,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
 #pragma unroll
         for (int r = 0; r < 4; ++r) a[r] = __builtin_fmaf(x[r], s, a[r]);
     };
-    // kInside: the scaled product of row tile i and column tile j
+    // E8M0: the scaled product of row tile i and column tile j
     auto scaled = [&](auto ic, auto jc) {
         constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[j], fa[i & 1], acc[i][j], 0, 0, j / 2, static_cast<int>(ew),
@@ -203,7 +203,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     // One stage, from `slot`.  What it reads ahead is the next stage of this tile or of the next one; behind the last
     // stage of all that is whatever the other slot holds, and is not used.
     auto stage = [&](int slot) {
-        if constexpr (kInside) {
+        if constexpr (kE8M0) {
 #pragma unroll
             for (int i = 0; i < TM / 4; ++i) eb[i] = eb_next[i];
             ew = ew_next;
@@ -211,13 +211,13 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         auto row = [&](auto ic) {
             constexpr int i = decltype(ic)::value;
             float s[2] = {0.f, 0.f};
-            if constexpr (!kInside) {
+            if constexpr (!kE8M0) {
                 s[0] = i == 0 ? last[0] : sc[i == 0 ? 0 : i - 1] * sw[0];
                 s[1] = i == 0 ? last[1] : sc[i == 0 ? 0 : i - 1] * sw[1];
             }
             auto column = [&](auto jc) {
                 constexpr int j = decltype(jc)::value;
-                if constexpr (kInside) {
+                if constexpr (kE8M0) {
                     scaled(ic, jc);
                 } else {
                     // the sums of the row tile before this one, four instructions old
@@ -230,7 +230,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
             column(std::integral_constant<int, 1>{});
             column(std::integral_constant<int, 2>{});
             column(std::integral_constant<int, 3>{});
-            if constexpr (i == 0 && !kInside) read_scales(slot);
+            if constexpr (i == 0 && !kE8M0) read_scales(slot);
             if constexpr (i + 2 < TM) fa[i & 1] = read_a(slot, i + 2);
             if constexpr (i == TM - 2) {
                 lds_done();          // this wave's last fragments of the stage are in registers
@@ -240,7 +240,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
                 barrier();
                 issue(slot);
                 fa[0] = read_a(1 - slot, 0);
-                if constexpr (kInside) read_scales(1 - slot);
+                if constexpr (kE8M0) read_scales(1 - slot);
             }
             if constexpr (i == TM - 1) fa[1] = read_a(1 - slot, 1);
             __builtin_amdgcn_sched_barrier(0);
@@ -255,7 +255,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
             row(std::integral_constant<int, TM - 2>{});
             row(std::integral_constant<int, TM - 1>{});
         }
-        if constexpr (!kInside) {
+        if constexpr (!kE8M0) {
             last[0] = sc[TM - 1] * sw[0];
             last[1] = sc[TM - 1] * sw[1];
         }
@@ -274,7 +274,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
     for (int j = 0; j < TN; ++j) fw[j] = read_w(0, j);
     fa[0] = read_a(0, 0);
     fa[1] = read_a(0, 1);
-    if constexpr (kInside) read_scales(0);
+    if constexpr (kE8M0) read_scales(0);
     int slot = 0;
     for (int lin = first; lin < end; lin += stride) {
 #pragma unroll
@@ -292,7 +292,7 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
             }
             if (half == 0) set_cursor(lin + stride);
         }
-        if constexpr (!kInside) {
+        if constexpr (!kE8M0) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) add(acc[TM - 1][j], d[j], last[j / 2]);
         }
@@ -302,46 +302,6 @@ __device__ __forceinline__ void large_tiles(const LargeParams& lp, uint8_t* lds,
         glu_tile_outputs<WM, kE8M0>(p, acc, m0, n0, wm, wn, again(tid), out_lds);
     }
     wait_vmcnt<0>();   // nothing is still writing LDS when the workgroup's next tiles, or another workgroup, use it
-}
-
-// Whether all fp32 scales of tiles first, first + stride, .. (`parts` of a whole one each) are powers of two that E8M0 has.  A
-// wave takes a whole tile's: the weights', then the tokens', 256 of a block an instruction.
-__device__ __forceinline__ bool powers_of_two(const GluParams& p, int first, int end, int stride, int parts) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int nk = (p.K + BK - 1) / BK;
-    const uint32_t* xs = static_cast<const uint32_t*>(p.x_scale);
-    const uint32_t* ws = static_cast<const uint32_t*>(p.w_scale);
-    uint32_t bad = 0u;
-    auto look = [&](uint32_t v) { bad |= (v & 0x7fffffu) | (v - 0x800000u > 0x7e800000u ? 1u : 0u); };
-    for (int64_t lin = first + static_cast<int64_t>(wave) * stride; lin < end; lin += kWaves * static_cast<int64_t>(stride)) {
-        int tm, tn;
-        tile_of(static_cast<int>(lin) / parts, p.tiles_t, p.tiles_n, &tm, &tn);
-        for (int i = lane; i < 2 * nk; i += 64)
-            look(ws[static_cast<int64_t>(i < nk ? tn : p.N / kFp8Block + tn) * nk + (i < nk ? i : i - nk)]);
-        if (__any(bad != 0u)) break;
-        const int64_t m = min(static_cast<int64_t>(tm) * kTileM + 4 * lane, p.T - 4);
-        auto scales = [&](int kb) {
-            struct { uint32_t v[4]; } q;   // at any token: 4-byte alignment
-            __builtin_memcpy(&q, xs + kb * p.T + m, sizeof(q));
-            return q;
-        };
-        int kb = 0;
-        for (; kb + 16 <= nk; kb += 16) {
-            decltype(scales(0)) q[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) q[i] = scales(kb + i);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) look(q[i].v[e]);
-        }
-        for (; kb < nk; ++kb) {
-            const auto q = scales(kb);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) look(q.v[e]);
-        }
-    }
-    return __syncthreads_or(static_cast<int>(bad)) == 0;
 }
 
 template <bool kE8M0>
@@ -355,19 +315,10 @@ glu_large_kernel(LargeParams p) {
     const int first = xcd * per + local, end = min((xcd + 1) * per, p.full);
     const int rest = 2 * (p.g.tiles_t * p.g.tiles_n - p.full), rper = (rest + kXcds - 1) / kXcds, r0 = 2 * p.full;
     const int rfirst = r0 + xcd * rper + local, rend = r0 + min((xcd + 1) * rper, rest);
-    auto tiles = [&](auto inside) {
-        constexpr bool kInside = decltype(inside)::value;
-        large_tiles<kTileM, kInside, kE8M0>(p, lds, first, end, stride);
-        if (rest > 0) {
-            __syncthreads();
-            large_tiles<kTileM / 2, kInside, kE8M0>(p, lds, rfirst, rend, stride);
-        }
-    };
-    if constexpr (kE8M0) {
-        tiles(std::true_type{});
-    } else {
-        const bool inside = powers_of_two(p.g, first, end, stride, 1) && powers_of_two(p.g, rfirst, rend, stride, 2);
-        inside ? tiles(std::true_type{}) : tiles(std::false_type{});
+    large_tiles<kTileM, kE8M0>(p, lds, first, end, stride);
+    if (rest > 0) {
+        __syncthreads();
+        large_tiles<kTileM / 2, kE8M0>(p, lds, rfirst, rend, stride);
     }
 }
 
