@@ -329,8 +329,10 @@ rtq_status rtq_fp8_dequantize(const void* codes, rtq_dtype ct, const void* scale
  *   a_codes [T][K] of at (E4M3 or E5M2), row groups; w_codes [N][K] E4M3, blocks; y [T][N] of yt.
  *   Accuracy: each 128-long inner sum is one matrix instruction, which aligns its products to about
  *   2^-14 of the largest; block sums are scaled and added in fp32.  With E8M0 scales large outputs add the
- *   block inside the instruction, which cuts off what lies below 2^-20 of the running sum.  So an fp32 y
- *   is good to about 4e-5 of its 2-norm, not to fp32.
+ *   block inside the instruction, which may cut off up to 2^-20 of the running sum for each block of K, K 2^-27
+ *   of it in all.  So an fp32 y is good to about 4e-5 of its 2-norm, not to fp32, with E8M0 scales and a large
+ *   output K 2^-27 more at the most (measured: 1.5e-5 for sums of both signs, 2.7e-6 for sums of one, with either
+ *   type of scales and K of 1024 to 65536).
  *   workspace: may be NULL.  With at least rtq_fp8_qgemm_workspace(T, N, K) bytes (any contents,
  *   16-byte aligned), products with few output tiles are split along the reduction; the fp32
  *   partial sums are then added in a fixed order, so equal calls give equal bits.  Calls sharing a
