@@ -410,7 +410,8 @@ rtq_status rtq_act_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_cod
  *   n = h / sqrt(mean_j h_j^2 + eps) * gamma, from h as it is stored;
  *   y = n rounded to xt, and/or codes (E4M3), scale (row groups, st): n quantised.
  *   x, y [rows][d] of xt; residual, h [rows][d] of rt (all F32 or BF16); residual and h are given together or not at
- *   all (rt is not used then); h may be residual, or x where rt is xt, not y; y may be x where h is not.  gamma [d] of gt.
+ *   all (rt is not used then).  gamma [d] of gt.  h and y may each be x or residual where the types agree, not both the
+ *   same; no output may overlap another array otherwise.
  *   y may be NULL, or codes and scale.  eps > 0.  The sum of squares is held in 64 bits; n is good to 4 units of 2^-24 before it is rounded.
  *   rows == 0 is a no-op. */
 rtq_status rtq_rmsnorm_forward(const void* x, rtq_dtype xt, const void* residual, rtq_dtype rt, int64_t rows, int32_t d,
@@ -421,7 +422,7 @@ rtq_status rtq_rmsnorm_forward(const void* x, rtq_dtype xt, const void* residual
  *   dh = dresidual + rho a - h rho^3 mean_j(a_j h_j): the gradient of h, thus of x and of residual;
  *   dgamma_j (+)= sum over rows of dn_j h_j rho, summed in fp32 in an order that equal calls share.
  *   dn [rows][d] of dnt; h, dresidual (or NULL: nothing is added), dh [rows][d] of ht; dh may be dresidual, or dn where
- *   dnt is ht, not h.  dgamma [d] of dgt, or NULL; accumulate 0 (overwrite) or 1 (add; a BF16 dgamma is read, added in
+ *   dnt is ht, not h, and no output may overlap another array otherwise.  dgamma [d] of dgt, or NULL; accumulate 0 (overwrite) or 1 (add; a BF16 dgamma is read, added in
  *   fp32 and rounded again).  workspace: rtq_rmsnorm_backward_workspace(rows, d) bytes (any contents), required with
  *   dgamma; calls sharing a workspace must not overlap.  rows == 0 writes zeros to dgamma, or with accumulate leaves it as it is. */
 rtq_status rtq_rmsnorm_backward(const void* dn, rtq_dtype dnt, const void* h, rtq_dtype ht, const void* dresidual,
@@ -436,7 +437,7 @@ size_t rtq_rmsnorm_backward_workspace(int64_t rows, int32_t d);
  *   rtq_fp8_dgrad and rtq_fp8_wgrad); N a multiple of 128, so that no block or group holds both.
  *   y: either y [T][N] of yt (F32 or BF16; y_codes and y_scale NULL), or y_codes (E4M3), y_scale (row groups) for the
  *   next product (y NULL).  h_codes (E4M3) [T][2 N], h_scale (row groups): [g u] quantised, the checkpoint that
- *   rtq_glu_fp8_backward takes; both NULL: not kept.  All scales of type st.
+ *   rtq_glu_fp8_backward takes; both NULL: not kept.  All scales of type st.  No output may overlap another array.
  *   workspace: rtq_fp8_glu_workspace(T, N, K) bytes (any contents), required where that is not 0.  Calls sharing a
  *   workspace must not overlap.  Accuracy of g and u as for rtq_fp8_qgemm, of f as for rtq_act_fp8_forward; y has the same
  *   bits whichever outputs are asked for beside it.  T == 0 is a no-op. */
@@ -448,7 +449,7 @@ size_t rtq_fp8_glu_workspace(int64_t T, int32_t N, int32_t K);
 /* Its backward pass from the checkpoint: dg = dy u^ f'(g^), du = dy f(g^), [g^ u^] = h_scale h_codes.
  *   dy [T][N] of dyt (F32 or BF16).  dh [T][2 N] of dyt: [dg du] (rtq_fp8_wgrad takes it in BF16), and/or dh_codes of gt
  *   (E4M3 or E5M2) [T][2 N], dh_scale (row groups, st): the same quantised, for rtq_fp8_dgrad.  What is not wanted is
- *   NULL.  T == 0 is a no-op. */
+ *   NULL.  No output may overlap another array.  T == 0 is a no-op. */
 rtq_status rtq_glu_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_codes, const void* h_scale, rtq_dtype st,
                                 int64_t T, int32_t N, rtq_act act, void* dh, void* dh_codes, rtq_dtype gt, void* dh_scale,
                                 void* stream);

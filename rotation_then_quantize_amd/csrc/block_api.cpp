@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <vector>
 
 #include "../../include/rtq.h"
@@ -38,6 +39,40 @@ rtq_status check_channels(int64_t N) {
 }
 
 bool glu_sizes_ok(int64_t T, int64_t N, int64_t K) { return sizes_ok(T, 2 * N, K) && N % 128 == 0 && K % 16 == 0; }
+
+// An array of a call: what it reads, or writes.  `place`: it goes element by element, each read by the thread that then writes
+// there, so that an output may lie exactly on an input of the same size.
+struct Array {
+    const char* name;
+    const void* data;
+    size_t bytes;
+    bool out;
+    bool place;
+};
+Array input(const char* name, const void* p, size_t bytes, bool place = false) { return {name, p, bytes, false, place}; }
+Array output(const char* name, const void* p, size_t bytes, bool place = false) { return {name, p, bytes, true, place}; }
+
+// No output overlaps another array (a workgroup would write over what another has yet to read), but for those `place`s.
+rtq_status check_apart(std::initializer_list<Array> arrays) {
+    for (const Array* o = arrays.begin(); o != arrays.end(); ++o) {
+        if (!o->out || o->data == nullptr) continue;
+        const uintptr_t begin = reinterpret_cast<uintptr_t>(o->data);
+        for (const Array* a = arrays.begin(); a != arrays.end(); ++a) {
+            if (a == o || a->data == nullptr) continue;
+            const uintptr_t other = reinterpret_cast<uintptr_t>(a->data);
+            if (begin + o->bytes <= other || other + a->bytes <= begin) continue;
+            if (!a->out && o->place && a->place && begin == other && o->bytes == a->bytes) continue;
+            return fail(RTQ_ERR_INVALID_ARG, "%s overlaps %s", o->name, a->name);
+        }
+    }
+    return RTQ_OK;
+}
+
+size_t elements(int64_t rows, int64_t d, size_t size) { return static_cast<size_t>(rows) * static_cast<size_t>(d) * size; }
+size_t float_size(rtq_dtype t) { return t == RTQ_BF16 ? 2 : 4; }
+size_t scale_size(rtq_dtype t) { return t == RTQ_E8M0 ? 1 : 4; }
+// Scales of row groups.
+size_t row_scales(int64_t rows, int64_t d, rtq_dtype st) { return elements(rows, fp8_groups(d), scale_size(st)); }
 
 rtq_status spans_of(const rtq_tensor* tensors, void* const* outs, int32_t count, std::vector<TensorSpan>* spans) {
     if (count < 0 || count > kMostTensors) return fail(RTQ_ERR_INVALID_ARG, "count must be 0..%d (got %d)", kMostTensors, count);
@@ -88,6 +123,10 @@ rtq_status rtq_rmsnorm_forward(const void* x, rtq_dtype xt, const void* residual
         RTQ_TRY(check_optional(scale, "scale"));
         if (h != nullptr && (y == h || (h == x && rt != xt)))
             return fail(RTQ_ERR_INVALID_ARG, "h must not be y, nor x of another type");
+        const size_t nx = elements(rows, d, float_size(xt)), nr = elements(rows, d, float_size(rt));
+        RTQ_TRY(check_apart({input("x", x, nx, true), input("residual", residual, nr, true), input("gamma", gamma, elements(1, d, float_size(gt))),
+                             output("h", h, nr, true), output("y", y, nx, true), output("codes", codes, elements(rows, d, 1)),
+                             output("scale", scale, row_scales(rows, d, st))}));
         const RmsForwardArgs a{x, xt == RTQ_BF16, residual, rt == RTQ_BF16, rows, d, gamma, gt == RTQ_BF16, eps,
                                h, y, codes, scale, st == RTQ_E8M0};
         return hip_status(launch_rmsnorm_forward(a, static_cast<hipStream_t>(stream)), "rmsnorm forward launch");
@@ -124,6 +163,13 @@ rtq_status rtq_rmsnorm_backward(const void* dn, rtq_dtype dnt, const void* h, rt
             const size_t need = rmsnorm_backward_workspace_bytes(rows, d);
             if (workspace == nullptr) return fail(RTQ_ERR_INVALID_ARG, "workspace is NULL");
             if (ws_bytes < need) return fail(RTQ_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+        }
+        if (rows > 0) {
+            const size_t nh = elements(rows, d, float_size(ht));
+            RTQ_TRY(check_apart({input("dn", dn, elements(rows, d, float_size(dnt)), true), input("h", h, nh),
+                                 input("dresidual", dresidual, nh, true), input("gamma", gamma, elements(1, d, float_size(gt))),
+                                 output("dh", dh, nh, true), output("dgamma", dgamma, elements(1, d, float_size(dgt))),
+                                 output("workspace", workspace, dgamma != nullptr ? rmsnorm_backward_workspace_bytes(rows, d) : 0)}));
         }
         const RmsBackwardArgs a{dn, dnt == RTQ_BF16, h, ht == RTQ_BF16, dresidual, rows, d, gamma, gt == RTQ_BF16, eps,
                                 dh, dgamma, dgt == RTQ_BF16, accumulate != 0, workspace};
@@ -164,6 +210,13 @@ rtq_status rtq_fp8_glu(const void* x_codes, const void* x_scale, int64_t T, cons
         const size_t need = fp8_glu_workspace_bytes(T, N, K);
         if (need > 0 && workspace == nullptr) return fail(RTQ_ERR_INVALID_ARG, "workspace is NULL");
         if (need > 0 && ws_bytes < need) return fail(RTQ_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+        RTQ_TRY(check_apart({input("x_codes", x_codes, elements(T, K, 1)), input("x_scale", x_scale, row_scales(T, K, st)),
+                             input("w_codes", w_codes, elements(2 * static_cast<int64_t>(N), K, 1)),
+                             input("w_scale", w_scale, row_scales(fp8_groups(2 * static_cast<int64_t>(N)), K, st)),
+                             output("h_codes", h_codes, elements(T, 2 * static_cast<int64_t>(N), 1)),
+                             output("h_scale", h_scale, row_scales(T, 2 * static_cast<int64_t>(N), st)),
+                             output("y", y, elements(T, N, float_size(yt))), output("y_codes", y_codes, elements(T, N, 1)),
+                             output("y_scale", y_scale, row_scales(T, N, st)), output("workspace", workspace, need)}));
         const GluArgs a{x_codes, x_scale, w_codes, w_scale, st == RTQ_E8M0, T, N, K, act, h_codes, h_scale, y, yt == RTQ_BF16,
                         y_codes, y_scale, workspace, ws_bytes};
         return hip_status(launch_fp8_glu(a, static_cast<hipStream_t>(stream)), "fp8 glu launch");
@@ -189,6 +242,10 @@ rtq_status rtq_glu_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_cod
         RTQ_TRY(check_optional(dh, "dh"));
         RTQ_TRY(check_optional(dh_codes, "dh_codes"));
         RTQ_TRY(check_optional(dh_scale, "dh_scale"));
+        const int64_t both = 2 * static_cast<int64_t>(N);
+        RTQ_TRY(check_apart({input("dy", dy, elements(T, N, float_size(dyt))), input("h_codes", h_codes, elements(T, both, 1)),
+                             input("h_scale", h_scale, row_scales(T, both, st)), output("dh", dh, elements(T, both, float_size(dyt))),
+                             output("dh_codes", dh_codes, elements(T, both, 1)), output("dh_scale", dh_scale, row_scales(T, both, st))}));
         const GluBackwardArgs a{dy, dyt == RTQ_BF16, h_codes, h_scale, st == RTQ_E8M0, T, N, act, dh, dh_codes, gt == RTQ_E5M2, dh_scale};
         return hip_status(launch_glu_backward(a, static_cast<hipStream_t>(stream)), "glu backward launch");
     });
