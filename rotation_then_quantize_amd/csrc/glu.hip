@@ -142,29 +142,35 @@ hipError_t launch_small(const GluArgs& a, hipStream_t stream) {
 
 // How a product runs.
 enum Form : int { kSmall, kSums, kTile32, kTile64, kTile128, kLarge };
-// Measured with codes (us; T x K, N channels; powers of two as scales):
+// Measured with codes (us; T x K, N channels; fp32 scales, E8M0 ones within 2% but for the last column's long reductions of many
+// tiles: 1024 and 2048 x 4096, 4096 in 35.2 and 56.9):
 //                        sums    32     64     128    256 tokens a tile
-//   64 x 512, 1152        8.7    5.6    6.3    8.3    9.2
-//   64 x 1024, 4096      10.8    7.4    8.3   11.4   12.9
-//   391 x 1936, 1152     13.9   14.4   16.0   21.3   24.1
-//   391 x 2048, 1152     13.5   11.3   12.8
-//   100 x 2048, 4096     13.2   11.2   12.7
-//   300 x 2560, 1152     14.4   14.1   16.6
-//   506 x 3136, 768      16.3   17.5   20.5
-//   64 x 4096, 4096      14.1   18.7   21.5   31.7   34.6
-//   64 x 4096, 10880     26.6   23.9   26.9
-//   64 x 4096, 16384     37.7   36.1   38.5
-//   256 x 4096, 4096     22.2   20.0   21.4   32.4   35.4
-//   512 x 4096, 4096     28.8          22.8   32.8   36.1
-//   1024 x 4096, 4096    46.1          45.2   36.5   39.2
-//   2048 x 4096, 4096    79.6          92.1   72.3   59.2
-//   48 x 8192, 8192      37.5   52.0   56.9
-//   128 x 8192, 8192     52.7   52.0   57.4   71.4   79.3
-//   256 x 16384, 4096    84.7   86.1   98.1  130     156
-// A tile costs its chain of blocks (0.5, 0.6, 0.95 and 1.2 us each) as long as each CU has one, so the smallest whose workgroups
-// fit at once is taken, and where none fits the largest.  The product that leaves its sums in the workspace splits the reduction
-// over idle CUs and costs a launch: it is better where the reduction is long (rows that begin inside a line of 128 bytes are
-// slower to load, and more so in tiles), with tiles for more than half of the CUs where it is very long.
+//   64 x 512, 1152        8.1    5.5    6.4    8.2    9.3
+//   64 x 1024, 4096      11.1    7.2    8.2   11.4   12.9
+//   391 x 1936, 1152     14.1   14.3   16.0   21.3   24.1
+//   391 x 2048, 1152     13.8   11.0   12.9   18.8   20.7
+//   100 x 2048, 4096     13.3   11.0   12.8   18.7   20.5
+//   300 x 2560, 1152     14.5   14.1   16.7   23.5   25.6
+//   506 x 3136, 768      16.6   17.4   20.5   29.1   31.3
+//   64 x 4096, 4096      14.3   18.4   21.6   31.8   34.7
+//   64 x 4096, 10880     26.3   24.7   27.5   34.2   38.8
+//   64 x 4096, 16384     37.5   35.9   38.2   40.7   46.8
+//   256 x 4096, 4096     22.6   19.0   21.5   32.5   35.3
+//   512 x 4096, 4096     29.8   35.9   23.4   32.9   35.5
+//   1024 x 4096, 4096    46.8   71.0   45.5   35.8   37.9
+//   2048 x 4096, 4096    79.9  140     92.9   72.7   62.3
+//   48 x 8192, 8192      37.5   51.9   56.4   66.0   77.9
+//   128 x 8192, 8192     52.2   51.7   57.1   71.2   78.6
+//   256 x 16384, 4096    83.1   85.1   97.5  130     154
+// A tile costs its chain of blocks as long as each CU has one (0.5, 0.6, 0.95 and 1.1 us a block where the weights are in the
+// caches; where they come from HBM and fill the CUs, 64 x 4096, 16384, 1.1 to 1.4, for which LDS does not account), so the
+// smallest whose workgroups fit at once is taken, and where none fits the largest.  The product that leaves its sums in the
+// workspace splits the reduction over idle CUs and costs a launch: it is better where the reduction is long, with tiles for
+// more than half of the CUs where it is very long.  Rows that begin inside a line of 128 bytes are slower to load, and more so
+// in tiles, so that the sums are level with them sooner (sums and tiles of 32; whole lines, blocks 16, 20, 22, 26: 391 tokens,
+// 1152 channels 13.6 11.1, 15.1 14.3, 15.6 14.1, 17.0 15.7; 64, 4096: 13.1 11.1, 14.1 14.2, 14.6 14.0, 13.6 15.8; 100, 2048:
+// 13.1 10.6, 13.8 13.6, 14.4 13.9, 13.4 15.6; others, blocks 11, 14, 16, 19: 391, 1152: 12.2 10.9, 13.3 12.8, 14.0 14.4, 15.2
+// 16.6; 64, 4096: 10.5 10.7, 11.1 12.8, 11.3 14.3, 14.2 16.6; 100, 2048: 9.9 8.4, 10.4 9.7, 10.7 12.0, 13.7 15.2).
 // Few tokens: as the weights stream (fp8_glu_small.hip), but where workgroups are fewer than CUs and the reduction long (y
 // alone, with codes, and either from sums: 1 x 16384, 1024 channels 18.7, 20.5, 13.9; 1 x 8192, 1152: 10.8, 12.8, 9.6; 4 x 4096,
 // 1152: 7.1, 9.1, 7.7; 4 x 2048, 1152: 4.9, 7.0, 7.7).  17 to 32 of them so where they are wide and the reduction is not short
