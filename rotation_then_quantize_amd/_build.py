@@ -56,13 +56,13 @@ def build(verbose: bool = False) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=8) as ex:
         native = ex.submit(_build_native)
         objs = list(ex.map(_compile, SOURCES))
-        native.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    native.result()   # raises where the binding failed; the C ABI does not need it
     if verbose:
         print("built", LIB, "and", NATIVE)
     return LIB
