@@ -188,8 +188,8 @@ glu_small_kernel(GluParams p, float* sums) {
 // Tiles of 16 channels per workgroup: as few bytes on the fullest CU as can be, a tile's two projections and the tokens once a
 // workgroup, and of equals the most (13 x 4096, 10880 channels, 680 tiles: three a workgroup, one workgroup on each of 227 CUs,
 // 17.0 us; with two, 84 CUs have two workgroups, 23.3; 16 x 4096, 14336: four 23.1, two 25.2; 32 x 4096, 16384: four 28.3, two
-// 32.5).  For up to 16 tokens two, where they fill all CUs alike: a CU's second workgroup loads while the first one joins its
-// sums, which a larger one does alone (two, three, four; 1 x 4096, 16384 channels: 24.2, 32.9, 25.2; 24576: 36.7, 37.6, 42.4;
+// 32.5).  For up to 16 tokens two, where they fill all CUs alike: within 3% of the best (a CU's second workgroup
+// can load while the first joins its sums; two, three, four; 1 x 4096, 16384 channels: 24.2, 32.9, 25.2; 24576: 36.7, 37.6, 42.4;
 // 32768: 44.7, 50.9, 47.4; 49152: 65.6, 70.5, 68.9; 65536: 85.4, 98.0, 89.9; 1 x 8192, 16384: 45.0, 59.3, 47.0; 1 x 2048, 32768:
 // 26.1, 30.7, 26.8; 16 x 4096, 16384: 25.2, 34.8, 25.7; 32768: 46.7, 54.1, 48.5; 49152: 71.1, 74.1, 71.0).
 hipError_t launch_glu_small(GluParams p, bool e8m0, float* sums, hipStream_t stream) {
