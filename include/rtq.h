@@ -412,7 +412,8 @@ rtq_status rtq_act_fp8_backward(const void* dy, rtq_dtype dyt, const void* h_cod
  *   x, y [rows][d] of xt; residual, h [rows][d] of rt (all F32 or BF16); residual and h are given together or not at
  *   all (rt is not used then).  gamma [d] of gt.  h and y may each be x or residual where the types agree, not both the
  *   same; no output may overlap another array otherwise.
- *   y may be NULL, or codes and scale.  eps > 0.  The sum of squares is held in 64 bits; n is good to 4 units of 2^-24 before it is rounded.
+ *   y may be NULL, or codes and scale.  eps > 0 and finite.  The sum of squares is held in 64 bits; n is good to 4 units of
+ *   2^-24 before it is rounded (8 in rows whose root mean square passes 2^126).
  *   rows == 0 is a no-op. */
 rtq_status rtq_rmsnorm_forward(const void* x, rtq_dtype xt, const void* residual, rtq_dtype rt, int64_t rows, int32_t d,
                                const void* gamma, rtq_dtype gt, float eps, void* h, void* y, void* codes, void* scale,
@@ -468,9 +469,9 @@ typedef struct {
 rtq_status rtq_grad_norm(const rtq_tensor* tensors, int32_t count, float* norm, void* workspace, size_t ws_bytes, void* stream);
 size_t rtq_grad_norm_workspace(const rtq_tensor* tensors, int32_t count);
 
-/* out = g * min(1, most / (norm[0] + 1e-6)) for every tensor, rounded to its type; most >= 0.  outs: `count` device
+/* out = g * min(1, most / (norm[0] + 1e-6)) for every tensor, rounded to its type; most finite and not negative.  outs: `count` device
  * pointers in HOST memory, tensors of the same sizes and types; NULL, or an entry that is the tensor's own data: in
- * place (nothing is written then where the factor is 1).  An out may not overlap any other tensor or out.  norm: as
+ * place (nothing is written then where the factor is 1).  An out may not overlap any other tensor or out, nor norm.  norm: as
  * rtq_grad_norm wrote it, or any other (the norm over several GPUs); a NaN spreads to every element. */
 rtq_status rtq_grad_clip(const rtq_tensor* tensors, void* const* outs, int32_t count, const float* norm, float most, void* stream);
 

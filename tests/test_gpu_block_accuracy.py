@@ -66,6 +66,18 @@ def test_norm_backward_far_from_one(T, d, ht, at, eps):
     near(dh, want, 6 * U * size + 2.0 ** -149 * (1 + h64.abs() * rho) + (2.0 ** -134 if ht == BF16 else 0.0))
 
 
+@pytest.mark.parametrize("T,d", [(6, 272), (3, 16400)])
+def test_norm_of_the_largest_rows(T, d):
+    """Past a root mean square of 2^126, rho has down to 22 bits: within 2^-22, with the products by h and gamma 6 u."""
+    step("norm largest", T, d)
+    x = (1 + torch.rand(T, d, generator=gen(T), device="cuda")) * 2.0 ** 126.99
+    x[0] = -3.3e38
+    gamma, y = 1 + 0.3 * randn(gen(d), d), torch.empty(T, d, device="cuda")
+    rtq.rmsnorm_forward(x, gamma, 1e-6, y=y)
+    want = x.double() / torch.sqrt(x.double().square().mean(1, keepdim=True)) * gamma.double()
+    near(y, want, 8 * U * want.abs())
+
+
 # ------------------------------------------------------------------ gated feed-forward
 
 # few tokens as weights stream, sums of split parts, tiles of 32, 64 and 128 tokens, and large ones of short and long reductions
