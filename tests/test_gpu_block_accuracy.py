@@ -199,3 +199,26 @@ def test_scales_of_other_tokens_and_channels_change_nothing(T, N, K):
         rtq.fp8_glu(xc, xs, wc, odd, rtq.RTQ_ACT_SILU, y=z)
         rest = torch.arange(N, device="cuda") // 128 != block % (N // 128)
         assert same(z[:, rest], y[:, rest]), block
+
+
+@pytest.mark.parametrize("st", [F32, E8M0])
+@pytest.mark.parametrize("T,N", [(2, 384), (64, 1024), (450, 2304), (2100, 4096)])
+def test_small_blocks_beside_a_large_one(T, N, st):
+    """Blocks whose products of 16 are three quarters of the running sum's last place: with fp32 scales their sums are added
+    whole, all numbers here being exact in fp32 (the gate is 32, where SiLU is the identity); with E8M0 scales a large output may
+    lose 2^-20 of the running sum for each block."""
+    step("glu small blocks", T, N, st)
+    K, blocks = 1024, 8
+    x, w = torch.zeros(T, K, device="cuda"), torch.zeros(2 * N, K, device="cuda")
+    x[:, 0], w[:N, 0], w[N:, 0] = 1.0, 2.0 ** -5, 1.0
+    x[:, 128:], w[N:, 128:] = 1.0, 1.5
+    xs, ws = torch.ones(blocks, T, device="cuda"), torch.ones(groups(2 * N), blocks, device="cuda")
+    xs[0], ws[:N // 128, 0], xs[1:] = 2.0 ** 10, 1.0, 2.0 ** -7
+    ws[N // 128:, 0] = 2.0 ** 11
+    y = torch.empty(T, N, device="cuda")
+    rtq.fp8_glu(x.to(E4M3), xs.to(st), w.to(E4M3), ws.to(st), rtq.RTQ_ACT_SILU, y=y)
+    want = 32.0 * (2.0 ** 21 + 7 * 1.5)
+    if T == 2100 and st == E8M0:
+        assert ((y <= want) & (y >= want * (1 - 7 * 2.0 ** -20))).all()
+    else:
+        assert (y == want).all(), float((y.double() - want).abs().max())
