@@ -440,8 +440,9 @@ size_t rtq_rmsnorm_backward_workspace(int64_t rows, int32_t d);
  *   next product (y NULL).  h_codes (E4M3) [T][2 N], h_scale (row groups): [g u] quantised, the checkpoint that
  *   rtq_glu_fp8_backward takes; both NULL: not kept.  All scales of type st.  No output may overlap another array.
  *   workspace: rtq_fp8_glu_workspace(T, N, K) bytes (any contents), required where that is not 0.  Calls sharing a
- *   workspace must not overlap.  Accuracy of g and u as for rtq_fp8_qgemm, of f as for rtq_act_fp8_forward; y has the same
- *   bits whichever outputs are asked for beside it.  T == 0 is a no-op. */
+ *   workspace must not overlap.  Accuracy of g and u as for rtq_fp8_qgemm, of f as for rtq_act_fp8_forward; codes and scales
+ *   are those of g, u and y so computed, so that one whose exact value lies as near to the border between two codes, or two
+ *   scales, may be the neighbour.  y has the same bits whichever outputs are asked for beside it.  T == 0 is a no-op. */
 rtq_status rtq_fp8_glu(const void* x_codes, const void* x_scale, int64_t T, const void* w_codes, const void* w_scale,
                        rtq_dtype st, int32_t N, int32_t K, rtq_act act, void* h_codes, void* h_scale, void* y, rtq_dtype yt,
                        void* y_codes, void* y_scale, void* workspace, size_t ws_bytes, void* stream);

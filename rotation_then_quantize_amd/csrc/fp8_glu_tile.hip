@@ -6,7 +6,8 @@
 // it is multiplied.  The tokens' and the two weights' scales, of kTable blocks at a time, are put into LDS beforehand.  The
 // outputs' staging takes the ring's place.
 //
-// Bound by LDS: a stage of 64 tokens writes 40 KB and reads 96, in 0.55-0.6 us, one of 32 writes 36 and reads 80, in 0.5.  Four
+// Bound by LDS where the weights are in the caches: a stage of 64 tokens writes 40 KB and reads 96, in 0.55-0.6 us, one of 32
+// writes 36 and reads 80, in 0.5 (1.1 and more where they come from HBM and fill the CUs: 64 x 4096, 16384 channels).  Four
 // waves with larger tiles, which read 64 KB for 64 tokens, have twice the loads each to issue and took 0.95 us.  Weights straight
 // into registers, where no other wave needs them (8 waves of 16 channels each), took 1 us: the instruction's operand is 16 rows,
 // so that a load touches half of 16 lines of 128 bytes, and each line is touched twice.  bf16 products of the decoded codes

@@ -9,7 +9,7 @@
 // fp32 rate), so rho is good to its rounding to fp32.
 //
 // h and dh are stored past the caches: the residual stream is read again a sublayer later, the codes at once (4608 x 4096: 23.9
-// us, 26.9 with plain stores, backward 31.3 and 33.3; 132 and 151 MB, 5.5 and 4.8 TB/s.  Non-temporal loads of x and r bring as
+// us, 26.9 with plain stores, backward 30.3 and 33.3; 132 and 151 MB, 5.5 and 5.0 TB/s.  Non-temporal loads of x and r bring as
 // much where they come from HBM and cost 20% where a kernel before has left them in the cache).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -274,8 +274,8 @@ __device__ __forceinline__ void row_gradient(float* dr, float* sum, const float*
 constexpr int backward_waves(int team) { return team < 8 ? 8 : team; }
 
 // Workgroups of teams of kTeam waves walk the rows, the next row's loads in flight behind each (but for the longest
-// rows, whose 16 waves have not the registers); a lane keeps the sums of dgamma of its columns, the teams' meet in LDS
-// at the end.
+// rows, whose 16 waves leave 128 registers a thread, of which 3 to 11 spill as it is: 2304 x 16384 66.5 us, 4608 x 8192
+// 57.2); a lane keeps the sums of dgamma of its columns, the teams' meet in LDS at the end.
 template <bool kN16, bool kH16, bool kG16, int kTeam>
 __global__ void __launch_bounds__(64 * backward_waves(kTeam))
 rmsnorm_backward_kernel(RmsBackwardParams p) {
