@@ -55,10 +55,10 @@ Array output(const char* name, const void* p, size_t bytes, bool place = false) 
 // No output overlaps another array (a workgroup would write over what another has yet to read), but for those `place`s.
 rtq_status check_apart(std::initializer_list<Array> arrays) {
     for (const Array* o = arrays.begin(); o != arrays.end(); ++o) {
-        if (!o->out || o->data == nullptr) continue;
+        if (!o->out || o->data == nullptr || o->bytes == 0) continue;
         const uintptr_t begin = reinterpret_cast<uintptr_t>(o->data);
         for (const Array* a = arrays.begin(); a != arrays.end(); ++a) {
-            if (a == o || a->data == nullptr) continue;
+            if (a == o || a->data == nullptr || a->bytes == 0) continue;
             const uintptr_t other = reinterpret_cast<uintptr_t>(a->data);
             if (begin + o->bytes <= other || other + a->bytes <= begin) continue;
             if (!a->out && o->place && a->place && begin == other && o->bytes == a->bytes) continue;

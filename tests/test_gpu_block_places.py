@@ -32,3 +32,13 @@ def test_norm_in_place(T, d, xt, rt):
         y2 = own[y_on] if y_on else torch.empty_like(x)
         rtq.rmsnorm_forward(own["x"], gamma, 1e-6, residual=own["r"], h=h2, y=y2)
         assert torch.equal(h2, h) and torch.equal(y2, y), (h_on, y_on)
+
+
+def test_workspaces_that_nothing_uses():
+    """A workspace is not looked at where the call needs none."""
+    print("unused workspace", flush=True)
+    h, gamma = torch.randn(4, 256, device="cuda"), torch.ones(256, device="cuda")
+    dh, again = torch.empty_like(h), torch.empty_like(h)
+    rtq.rmsnorm_backward(h, h, gamma, 1e-6, dh)
+    rtq.rmsnorm_backward(h, h, gamma, 1e-6, again, workspace=dh[1:])
+    assert torch.equal(again, dh)
